@@ -1,6 +1,7 @@
 /*
  * kmeans_mi355x.h -- C ABI of the MI355X (gfx950) k-means assignment library
- * (with the centroid update that follows assignment in a Lloyd iteration).
+ * (with the centroid update that follows assignment in a Lloyd iteration, and
+ * the operators that train a centroid table by gradients inside a model).
  *
  * The operation.  flashlib PR #22, "Optimize Blackwell k-means assignment
  * reduction", Summary: the assignment step scores every (point, centroid)
@@ -46,7 +47,7 @@
 extern "C" {
 #endif
 
-#define KMEANS_ABI_VERSION 7
+#define KMEANS_ABI_VERSION 8
 
 /* Supported feature dimension: 16 <= D <= 512 and D % 16 == 0. */
 #define KMEANS_MIN_D 16
@@ -261,6 +262,156 @@ kmeans_status_t kmeans_update_path(const void *X, const int32_t *labels, const v
                                    int64_t N, int64_t D, int64_t K, void *C_new, float *norms,
                                    int32_t *counts, float *means, int32_t path,
                                    hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Training a codebook by gradients.  A centroid table that sits inside a
+ * model (a codebook of discrete tokens, an embedding) is read back by label,
+ * learns from the gradient of what was read, stands between linear layers,
+ * and its gradients are clipped together with theirs.  The pages describe
+ * none of these steps; the formulas below define them.
+ *
+ * Matrices are row-major with unit column stride; a `*_stride` is the
+ * distance between rows in elements (at least the row length, at most 2^20
+ * for kmeans_linear and kmeans_linear_grad).  Pointers need the alignment of
+ * one element only; rows whose address and stride are multiples of 16 bytes
+ * take the fast loads.  The conventions at the top of this file hold,
+ * determinism included: no floating-point value is accumulated with atomics,
+ * every sum is fp32 or wider in an order fixed by the shapes and labels.
+ */
+typedef enum {
+    KMEANS_BF16 = 0,
+    KMEANS_FP16 = 1,
+    KMEANS_FP32 = 2
+} kmeans_dtype_t;
+
+typedef enum {
+    KMEANS_INT32 = 0,
+    KMEANS_INT64 = 1
+} kmeans_label_t;
+
+typedef enum {
+    KMEANS_ACT_NONE = 0,       /* z */
+    KMEANS_ACT_RELU = 1,       /* max(z, 0); NaN stays NaN */
+    KMEANS_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution function */
+    KMEANS_ACT_GELU_TANH = 3,  /* z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    KMEANS_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} kmeans_activation_t;
+
+/*
+ * Table lookup with scaling:  Y[i] = scale * C[labels[i]], the product in
+ * fp32 rounded once to the table's type; a label outside [0, K) gives a row
+ * of zeros.
+ *
+ *   C         [K][D] of `dtype`, rows c_stride apart.
+ *   labels    [N] of `label_type`.
+ *   N, D, K   0 <= N < 2^31, 1 <= D < 2^31, 1 <= K < 2^31.
+ *   Y         [N][D] of `dtype`, rows y_stride apart, written.
+ */
+kmeans_status_t kmeans_lookup(const void *C, int64_t c_stride, const void *labels,
+                              int32_t label_type, int64_t N, int64_t D, int64_t K,
+                              int32_t dtype, float scale, void *Y, int64_t y_stride,
+                              hipStream_t stream);
+
+/*
+ * Gradient of kmeans_lookup with respect to the table:
+ *
+ *     dC[k] = scale * (sum of dY[i] over the i with labels[i] == k)
+ *
+ * in fp32 (each sum in an order fixed by the labels), rounded once to
+ * `out_dtype`.  With accumulate != 0 the result is added to dC instead
+ * (dC[k] + scale * sum, rounded once), and rows without a label stay bit
+ * for bit as they are; otherwise such rows become zero.  Labels outside
+ * [0, K) count for no row.
+ *
+ *   dY        [N][D] of `dtype`, rows dy_stride apart.
+ *   N, D, K   0 <= N < 2^31, 1 <= D < 2^31, 1 <= K < 2^31.
+ *   dC        [K][D] of `out_dtype` (`dtype` or KMEANS_FP32), rows dc_stride
+ *             apart, written (accumulate: read and written).
+ *
+ * Scratch (about 16 bytes per label and 8 D bytes per 64 labels) is the
+ * stream's workspace; KMEANS_ERR_NO_MEMORY if it cannot grow.
+ */
+kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride, const void *labels,
+                                   int32_t label_type, int64_t N, int64_t D, int64_t K,
+                                   int32_t dtype, float scale, int32_t accumulate, void *dC,
+                                   int32_t out_dtype, int64_t dc_stride, hipStream_t stream);
+
+/*
+ * Linear layer with its epilogue in one pass:
+ *
+ *     Z = X W^T + bias          (fp32 accumulation)
+ *     Y = act(Z) + residual     (fp32, rounded once)
+ *
+ *   X         [N][D], W [F][D] of `dtype` (KMEANS_BF16 or KMEANS_FP16).
+ *   bias      [F] of `dtype`, or NULL.   residual  [N][F] of `dtype`, or NULL.
+ *   activation  kmeans_activation_t.
+ *   Y         [N][F] of `dtype`, written (may be `residual` itself).
+ *   pre       [N][F] of `dtype` or NULL: Z rounded once, which
+ *             kmeans_linear_grad needs unless the activation is
+ *             KMEANS_ACT_NONE.
+ *   N, D, F   0 <= N < 2^31, 1 <= D, F <= 2^20.
+ *
+ * Small N or few output tiles split the sum over D between workgroups; the
+ * partial sums (fp32) are the stream's workspace.
+ */
+kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const void *W, int64_t w_stride,
+                              const void *bias, const void *residual, int64_t residual_stride,
+                              int64_t N, int64_t D, int64_t F, int32_t dtype,
+                              int32_t activation, void *Y, int64_t y_stride, void *pre,
+                              int64_t pre_stride, hipStream_t stream);
+
+/*
+ * Gradients of kmeans_linear for the output gradient dY (the residual's
+ * gradient is dY itself):
+ *
+ *     dZ = dY * act'(Z)      dX = dZ W      dW = dZ^T X      dbias = sum_i dZ[i]
+ *
+ *   dY        [N][F];  X [N][D];  W [F][D];  pre = Z [N][F] (as kept by
+ *             kmeans_linear; NULL only with KMEANS_ACT_NONE), all of `dtype`
+ *             (KMEANS_BF16 or KMEANS_FP16).
+ *   dX        [N][D], dW [F][D], dbias [F] of `dtype`, written; each may be
+ *             NULL (then it is not computed).
+ *   N, D, F   0 <= N < 2^31, 1 <= D, F <= 2^20 (N == 0: dW and dbias are zero).
+ *
+ * dZ is rounded once to `dtype` (the matrix instructions take 16-bit
+ * operands; an fp16 dZ past 65504 becomes infinite), dbias sums it
+ * unrounded.  dZ and partial sums are the stream's workspace (2 bytes per
+ * element of dY, and partial sums where few tiles fill the GPU).
+ */
+kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride, const void *X,
+                                   int64_t x_stride, const void *W, int64_t w_stride,
+                                   const void *pre, int64_t pre_stride, int64_t N, int64_t D,
+                                   int64_t F, int32_t dtype, int32_t activation, void *dX,
+                                   int64_t dx_stride, void *dW, int64_t dw_stride, void *dbias,
+                                   hipStream_t stream);
+
+/* One gradient of a list: `numel` contiguous elements of `dtype`. */
+typedef struct {
+    const void *src;    /* the gradient */
+    void *dst;          /* where its clipped values go (src itself: in place) */
+    int64_t numel;      /* >= 0 */
+    int32_t dtype;      /* kmeans_dtype_t */
+    int32_t reserved;   /* 0 */
+} kmeans_gradient_t;
+
+/*
+ * Global 2-norm over a list of gradients, and clipping by it:
+ *
+ *     n = sqrt(sum over the list of sum_j src_j^2)     (fp64 sums)
+ *     dst = src * min(1, max_norm / (n + 1e-6))        (fp32, rounded once)
+ *
+ * norm (fp32 [1], device) receives n.  `list` is a host array, read before
+ * the call returns; its buffers must not overlap one another, except that a
+ * dst may be its own src.  A NaN anywhere makes n and every output NaN, an
+ * infinity makes n infinite and the outputs 0 or NaN, as the formula says.
+ * When nothing is to be clipped, dst == src tensors are not written.
+ * kmeans_gradient_norm computes n alone and ignores dst.  count and numel
+ * may be 0 (n = 0).  max_norm must be >= 0.
+ */
+kmeans_status_t kmeans_gradient_norm(const kmeans_gradient_t *list, int64_t count, float *norm,
+                                     hipStream_t stream);
+kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t count,
+                                      float max_norm, float *norm, hipStream_t stream);
 
 /*
  * The workspace of `stream` on the current device.  kmeans_assign's K-split

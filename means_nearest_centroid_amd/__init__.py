@@ -12,6 +12,16 @@ CPU fallback: if the library is missing, the first call raises.
 
 ``X`` and ``C`` are ``torch.bfloat16`` CUDA tensors of shape ``[N, D]`` and
 ``[K, D]``, contiguous.  Calls are asynchronous on the current stream.
+
+A table that is trained by gradients inside a model (a codebook, an embedding)
+has these operators around the two steps above (bf16 or fp16; the lookup,
+its gradient and the clipping also fp32):
+
+    Y, Z = kmeans_linear(X, W, bias, residual, activation="gelu", save_pre=True)
+    rows = kmeans_lookup(C, labels, scale=1.0)
+    dC = kmeans_lookup_grad(dY, labels, K, scale=1.0)
+    dX, dW, db = kmeans_linear_grad(dY, X, W, Z, activation="gelu")
+    norm, _ = kmeans_clip_gradients([dW, db, dC], max_norm=1.0)
 """
 
 from __future__ import annotations
@@ -41,6 +51,11 @@ PATH_PERSISTENT = 3
 UPDATE_AUTO = 0
 UPDATE_SORT = 1
 UPDATE_BUCKETS = 2
+# kmeans_dtype_t, kmeans_label_t
+BF16, FP16, FP32 = 0, 1, 2
+INT32, INT64 = 0, 1
+# kmeans_activation_t, by the name the functions below take
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 _STATUS_NAMES = {
     0: "KMEANS_OK", 1: "KMEANS_ERR_INVALID_ARG", 2: "KMEANS_ERR_UNSUPPORTED",
@@ -48,6 +63,12 @@ _STATUS_NAMES = {
 }
 
 _lib = None
+
+
+class _Gradient(ctypes.Structure):
+    """kmeans_gradient_t."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class KmeansError(RuntimeError):
@@ -88,6 +109,22 @@ def load_library(path: str = LIBRARY):
     lib.kmeans_update.restype = ctypes.c_int
     lib.kmeans_update_path.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, vp]
     lib.kmeans_update_path.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.kmeans_lookup.argtypes = [vp, i64, vp, i32, i64, i64, i64, i32, f32, vp, i64, vp]
+    lib.kmeans_lookup.restype = ctypes.c_int
+    lib.kmeans_lookup_grad.argtypes = [vp, i64, vp, i32, i64, i64, i64, i32, f32, i32, vp, i32,
+                                       i64, vp]
+    lib.kmeans_lookup_grad.restype = ctypes.c_int
+    lib.kmeans_linear.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, i32, i32, vp, i64,
+                                  vp, i64, vp]
+    lib.kmeans_linear.restype = ctypes.c_int
+    lib.kmeans_linear_grad.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32,
+                                       i32, vp, i64, vp, i64, vp, vp]
+    lib.kmeans_linear_grad.restype = ctypes.c_int
+    lib.kmeans_gradient_norm.argtypes = [vp, i64, vp, vp]
+    lib.kmeans_gradient_norm.restype = ctypes.c_int
+    lib.kmeans_clip_gradients.argtypes = [vp, i64, f32, vp, vp]
+    lib.kmeans_clip_gradients.restype = ctypes.c_int
     lib.kmeans_release_workspace.argtypes = [vp]
     lib.kmeans_release_workspace.restype = ctypes.c_int
     lib.kmeans_last_error.argtypes = []
@@ -288,6 +325,279 @@ def kmeans_update(X, labels, C_old, C_new=None, norms=None, counts=None, means=N
                                            _ptr(C_new), _ptr(norms), _ptr(counts), _ptr(means),
                                            int(path), _stream_handle(stream, dev)))
     return C_new, norms, counts, means
+
+
+# ---- training a codebook by gradients ----
+
+_DTYPES = None
+
+
+def _dtype(t, name):
+    """kmeans_dtype_t of a tensor."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32 (got {t.dtype})")
+    return code
+
+
+def _rows(t, name, like=None, shape=None):
+    """Check a 2-D CUDA tensor with unit column stride; its row stride.  A
+    tensor of one row or less, or one column, may report any stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor (got {tuple(t.shape)}, {t.device})")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride (strides {t.stride()})")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device} "
+                         f"(got {t.dtype} on {t.device})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    stride = t.stride(0) if rows > 1 else max(cols, 1)
+    if stride < cols:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return stride
+
+
+def _flat(t, name):
+    """A tensor of rows [..., D] as 2-D (a view: no copy is made)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() == 2:
+        return t
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions (got {tuple(t.shape)})")
+    try:
+        return t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}: rows of shape {tuple(t.shape)}, strides {t.stride()} are not "
+                         "evenly spaced; make it contiguous") from None
+
+
+def _labels(labels, device):
+    import torch
+    if (not isinstance(labels, torch.Tensor) or labels.dtype not in (torch.int32, torch.int64)
+            or labels.device != device or not labels.is_contiguous()):
+        got = (f"{labels.dtype}, {labels.device}, contiguous={labels.is_contiguous()}"
+               if isinstance(labels, torch.Tensor) else type(labels).__name__)
+        raise ValueError(f"labels must be a contiguous int32 or int64 tensor on {device} "
+                         f"(got {got})")
+    return INT64 if labels.dtype == torch.int64 else INT32
+
+
+def kmeans_lookup(C, labels, scale: float = 1.0, out=None, stream=None):
+    """``out[i] = scale * C[labels[i]]``, a row of zeros for a label outside
+    ``[0, K)``.  ``C``: ``[K, D]`` bf16, fp16 or fp32, any row stride;
+    ``labels``: int32 or int64 of any shape; ``out``: ``[*labels.shape, D]``."""
+    import torch
+    c_stride = _rows(C, "C")
+    code = _dtype(C, "C")
+    K, D = C.shape
+    kind = _labels(labels, C.device)
+    if out is None:
+        out = torch.empty((*labels.shape, D), dtype=C.dtype, device=C.device)
+        y_stride = D
+    else:
+        if tuple(out.shape) != (*labels.shape, D):
+            raise ValueError(f"out must have shape {(*labels.shape, D)} (got {tuple(out.shape)})")
+        y_stride = _rows(_flat(out, "out") if out.dim() != 1 else out.view(1, D), "out", like=C)
+    lib = load_library()
+    with _on(C.device):
+        _check(lib, lib.kmeans_lookup(_ptr(C), c_stride, _ptr(labels), kind, labels.numel(), D, K,
+                                      code, scale, _ptr(out), y_stride,
+                                      _stream_handle(stream, C.device)))
+    return out
+
+
+def kmeans_lookup_grad(dY, labels, K: int, scale: float = 1.0, out=None,
+                       accumulate: bool = False, stream=None):
+    """Gradient of ``kmeans_lookup`` with respect to the table:
+    ``out[k] = scale * sum of dY[i] over labels[i] == k``.  ``dY``:
+    ``[*labels.shape, D]``; ``out``: ``[K, D]`` of ``dY``'s type (made when
+    not given) or fp32; ``accumulate`` adds to ``out`` instead."""
+    import torch
+    if labels.dim() == 0:
+        dY = dY.view(1, -1)
+    dY = _flat(dY, "dY")
+    y_stride = _rows(dY, "dY")
+    code = _dtype(dY, "dY")
+    N, D = dY.shape
+    kind = _labels(labels, dY.device)
+    if labels.numel() != N:
+        raise ValueError(f"dY has {N} rows but there are {labels.numel()} labels")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((K, D), dtype=dY.dtype, device=dY.device)
+    c_stride = _rows(out, "out", shape=(K, D))
+    if out.device != dY.device or out.dtype not in (dY.dtype, torch.float32):
+        raise ValueError(f"out must be {dY.dtype} or float32 on {dY.device} "
+                         f"(got {out.dtype} on {out.device})")
+    lib = load_library()
+    with _on(dY.device):
+        _check(lib, lib.kmeans_lookup_grad(_ptr(dY), y_stride, _ptr(labels), kind, N, D, K, code,
+                                           scale, int(accumulate), _ptr(out), _dtype(out, "out"),
+                                           c_stride, _stream_handle(stream, dY.device)))
+    return out
+
+
+def _activation(name) -> int:
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)} (got {name!r})")
+    return code
+
+
+def _bias(t, F, like):
+    import torch
+    if (not isinstance(t, torch.Tensor) or t.dtype != like.dtype or t.device != like.device
+            or t.numel() != F or not t.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous {like.dtype} tensor of {F} elements on "
+                         f"{like.device}")
+    return t
+
+
+def kmeans_linear(X, W, bias=None, residual=None, activation: str = "none",
+                  save_pre: bool = False, out=None, pre=None, stream=None):
+    """``Z = X W^T + bias``, ``Y = act(Z) + residual``, one pass.  ``X``:
+    ``[..., D]``, ``W``: ``[F, D]``, bf16 or fp16; ``activation``: a key of
+    ``ACTIVATIONS``.  Returns ``Y``, or ``(Y, Z)`` with ``save_pre`` (or
+    ``pre`` given), which ``kmeans_linear_grad`` needs."""
+    import torch
+    lead = X.shape[:-1]
+    X = _flat(X, "X")
+    x_stride = _rows(X, "X")
+    code = _dtype(X, "X")
+    N, D = X.shape
+    w_stride = _rows(W, "W", like=X)
+    F = W.shape[0]
+    if W.shape[1] != D:
+        raise ValueError(f"X has D={D} but W has D={W.shape[1]}")
+    act = _activation(activation)
+    if bias is not None:
+        _bias(bias, F, X)
+    r_stride = 0
+    if residual is not None:
+        residual = _flat(residual, "residual")
+        r_stride = _rows(residual, "residual", like=X, shape=(N, F))
+    if out is None:
+        out = torch.empty((*lead, F), dtype=X.dtype, device=X.device)
+        y_stride = F
+    else:
+        y_stride = _rows(_flat(out, "out"), "out", like=X, shape=(N, F))
+    z_stride = 0
+    if pre is not None:
+        z_stride = _rows(_flat(pre, "pre"), "pre", like=X, shape=(N, F))
+    elif save_pre:
+        pre = torch.empty((*lead, F), dtype=X.dtype, device=X.device)
+        z_stride = F
+    lib = load_library()
+    with _on(X.device):
+        _check(lib, lib.kmeans_linear(_ptr(X), x_stride, _ptr(W), w_stride, _ptr(bias),
+                                      _ptr(residual), r_stride, N, D, F, code, act, _ptr(out),
+                                      y_stride, _ptr(pre), z_stride,
+                                      _stream_handle(stream, X.device)))
+    return out if pre is None else (out, pre)
+
+
+def kmeans_linear_grad(dY, X, W, Z=None, activation: str = "none", bias: bool = True,
+                       need_dx: bool = True, need_dw: bool = True, stream=None):
+    """Gradients of ``kmeans_linear`` for the output gradient ``dY``:
+    ``(dX, dW, dbias)``, ``None`` for one not asked for.  ``Z``: the
+    pre-activations that ``kmeans_linear`` kept (not needed for ``"none"``).
+    The residual's gradient is ``dY`` itself."""
+    import torch
+    x_shape = X.shape
+    X = _flat(X, "X")
+    dY = _flat(dY, "dY")
+    x_stride = _rows(X, "X")
+    code = _dtype(X, "X")
+    N, D = X.shape
+    w_stride = _rows(W, "W", like=X)
+    F = W.shape[0]
+    if W.shape[1] != D:
+        raise ValueError(f"X has D={D} but W has D={W.shape[1]}")
+    y_stride = _rows(dY, "dY", like=X, shape=(N, F))
+    act = _activation(activation)
+    z_stride = 0
+    if act == 0:
+        Z = None
+    elif Z is None:
+        raise ValueError(f"activation {activation!r} needs Z")
+    else:
+        Z = _flat(Z, "Z")
+        z_stride = _rows(Z, "Z", like=X, shape=(N, F))
+    dX = torch.empty(x_shape, dtype=X.dtype, device=X.device) if need_dx else None
+    dW = torch.empty((F, D), dtype=X.dtype, device=X.device) if need_dw else None
+    db = torch.empty(F, dtype=X.dtype, device=X.device) if bias else None
+    lib = load_library()
+    with _on(X.device):
+        _check(lib, lib.kmeans_linear_grad(_ptr(dY), y_stride, _ptr(X), x_stride, _ptr(W),
+                                           w_stride, _ptr(Z), z_stride, N, D, F, code, act,
+                                           _ptr(dX), D, _ptr(dW), D, _ptr(db),
+                                           _stream_handle(stream, X.device)))
+    return dX, dW, db
+
+
+def _gradient_list(grads, out, device):
+    items = (_Gradient * max(len(grads), 1))()
+    for item, g, o in zip(items, grads, grads if out is None else out):
+        if not g.is_cuda or g.device != device or not g.is_contiguous():
+            raise ValueError(f"gradients must be contiguous tensors on one GPU "
+                             f"(got {g.device}, strides {g.stride()})")
+        if o is not g and (o.dtype != g.dtype or o.device != device or o.shape != g.shape
+                           or not o.is_contiguous()):
+            raise ValueError(f"out must match the gradients: {g.dtype}, {tuple(g.shape)}, "
+                             f"contiguous, on {device}")
+        item.src = g.data_ptr()
+        item.dst = o.data_ptr()
+        item.numel = g.numel()
+        item.dtype = _dtype(g, "gradients")
+    return items
+
+
+def _norm_of(grads, norm, device):
+    import torch
+    if device is None:
+        device = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+    return _vector(norm, "norm", torch.float32, 1, device), device
+
+
+def kmeans_gradient_norm(grads, norm=None, stream=None):
+    """Global 2-norm of a list of contiguous gradients (bf16, fp16 and fp32
+    mixed as they come): fp32 tensor of one element."""
+    norm, device = _norm_of(grads, norm, None)
+    items = _gradient_list(grads, None, device)
+    lib = load_library()
+    with _on(device):
+        _check(lib, lib.kmeans_gradient_norm(ctypes.byref(items), len(grads), _ptr(norm),
+                                             _stream_handle(stream, device)))
+    return norm
+
+
+def kmeans_clip_gradients(grads, max_norm: float, out=None, norm=None, stream=None):
+    """Clip a list of contiguous gradients by their global 2-norm:
+    ``g * min(1, max_norm / (norm + 1e-6))``, in place or into the list
+    ``out``.  Returns ``(norm, clipped)``."""
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out has {len(out)} tensors for {len(grads)} gradients")
+    norm, device = _norm_of(grads, norm, None)
+    items = _gradient_list(grads, out, device)
+    lib = load_library()
+    with _on(device):
+        _check(lib, lib.kmeans_clip_gradients(ctypes.byref(items), len(grads), max_norm,
+                                              _ptr(norm), _stream_handle(stream, device)))
+    return norm, list(grads if out is None else out)
 
 
 def kmeans_release_workspace(stream=None):

@@ -1,0 +1,335 @@
+// kmeans_clip.hip -- gfx950 kernels of the global gradient norm over a list of
+// tensors and of clipping by it.
+//
+//     n = sqrt(sum of all squares),   dst = src * min(1, max_norm / (n + 1e-6))
+//
+// Bound by memory: every element is read once for the norm and, since n is
+// needed before the first product, read again and written once.  The list
+// travels in the kernel arguments (no device table, nothing to upload), in
+// batches of kBatch tensors.  Pass 1: a fixed set of workgroups walks fixed
+// chunks of the batch's tensors, each leaving one fp64 partial sum.  Pass 2:
+// every workgroup adds all partial sums in one fixed order, so all of them
+// derive the same factor without a third launch, and scales its chunks.
+// Squares are summed in fp64: no fp32 value over- or underflows there, and
+// the conversions and additions stay far below the memory time.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "kmeans_internal.h"
+#include "kmeans_types.h"
+
+namespace kmeans {
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kBatch = 96;                 // tensors per launch: 2.8 KiB of arguments
+constexpr int kChunkBytes = 32768;         // of the source, per workgroup step
+constexpr int kLoads = kChunkBytes / 16 / kClipThreads;   // 16-byte loads of a thread in flight
+constexpr int64_t kMaxPartials = 2048;
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+struct Batch {
+    const void *src[kBatch];
+    void *dst[kBatch];
+    int64_t numel[kBatch];
+    int first[kBatch + 1];   // first chunk of each tensor
+    uint8_t dtype[kBatch];
+    int count;
+    int first_partial;       // of this batch's workgroups
+};
+
+// Tensor that chunk c belongs to (wave-uniform).
+__device__ __forceinline__ int tensor_of(const Batch &b, int c) {
+    int lo = 0, hi = b.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+// The workgroup's total, on every thread.
+__device__ __forceinline__ double group_sum(double v) {
+    __shared__ double total[kClipThreads / 64];
+    v = wave_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        total[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kClipThreads / 64; ++w)
+        s += total[w];
+    return s;
+}
+
+// Chunk `c` of a tensor: elements [c E, min(numel, (c + 1) E)), E = elements
+// of kChunkBytes.  Each thread holds kLoads runs of V elements.
+template <typename T>
+__device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c, double (&s)[4]) {
+    typedef typename T::bits B;
+    constexpr int V = 16 / sizeof(B);
+    constexpr int E = kChunkBytes / sizeof(B);
+    const int64_t beg = static_cast<int64_t>(c) * E;
+    const int left = static_cast<int>(min(static_cast<int64_t>(E), numel - beg));
+    const B *p = static_cast<const B *>(src) + beg;
+    auto add = [&](const Packed<B, V> &v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const double x = static_cast<double>(T::widen(v.v[e]));
+            s[e & 3] = fma(x, x, s[e & 3]);
+        }
+    };
+    if (left == E) {
+        Packed<B, V> v[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            v[u] = *reinterpret_cast<const Packed<B, V> *>(p + (u * kClipThreads + threadIdx.x) * V);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            add(v[u]);
+        return;
+    }
+    for (int at = threadIdx.x * V; at < left; at += kClipThreads * V) {
+        if (at + V <= left) {
+            add(*reinterpret_cast<const Packed<B, V> *>(p + at));
+        } else {
+            for (int e = at; e < left; ++e) {
+                const double x = static_cast<double>(T::widen(p[e]));
+                s[0] = fma(x, x, s[0]);
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t numel, int c,
+                                            float factor) {
+    typedef typename T::bits B;
+    constexpr int V = 16 / sizeof(B);
+    constexpr int E = kChunkBytes / sizeof(B);
+    const int64_t beg = static_cast<int64_t>(c) * E;
+    const int left = static_cast<int>(min(static_cast<int64_t>(E), numel - beg));
+    const B *p = static_cast<const B *>(src) + beg;
+    B *o = static_cast<B *>(dst) + beg;
+    auto put = [&](int at, Packed<B, V> v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            v.v[e] = T::narrow(T::widen(v.v[e]) * factor);
+        *reinterpret_cast<Packed<B, V> *>(o + at) = v;
+    };
+    if (left == E) {
+        Packed<B, V> v[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            v[u] = *reinterpret_cast<const Packed<B, V> *>(p + (u * kClipThreads + threadIdx.x) * V);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            put((u * kClipThreads + threadIdx.x) * V, v[u]);
+        return;
+    }
+    for (int at = threadIdx.x * V; at < left; at += kClipThreads * V) {
+        if (at + V <= left)
+            put(at, *reinterpret_cast<const Packed<B, V> *>(p + at));
+        else
+            for (int e = at; e < left; ++e)
+                o[e] = T::narrow(T::widen(p[e]) * factor);
+    }
+}
+
+__global__ __launch_bounds__(kClipThreads)
+void clip_norm_kernel(const Batch b, double *__restrict__ partial) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
+        const int t = tensor_of(b, c);
+        const int in = c - b.first[t];
+        if (b.dtype[t] == KMEANS_BF16)
+            sum_chunk<Bf16>(b.src[t], b.numel[t], in, s);
+        else if (b.dtype[t] == KMEANS_FP16)
+            sum_chunk<Fp16>(b.src[t], b.numel[t], in, s);
+        else
+            sum_chunk<Fp32>(b.src[t], b.numel[t], in, s);
+    }
+    const double total = group_sum((s[0] + s[1]) + (s[2] + s[3]));
+    if (threadIdx.x == 0)
+        partial[b.first_partial + blockIdx.x] = total;
+}
+
+// The norm from all partial sums, the same on every workgroup.
+__device__ __forceinline__ float total_norm(const double *partial, int partials) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < partials; i += kClipThreads)
+        v += partial[i];
+    return static_cast<float>(sqrt(group_sum(v)));
+}
+
+__global__ __launch_bounds__(kClipThreads)
+void clip_scale_kernel(const Batch b, const double *__restrict__ partial, int partials,
+                       float max_norm, float *__restrict__ norm) {
+    const float n = total_norm(partial, partials);
+    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
+        *norm = n;
+    const float ratio = max_norm / (n + 1e-6f);
+    const float factor = ratio > 1.0f ? 1.0f : ratio;     // a NaN stays
+    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
+        const int t = tensor_of(b, c);
+        const int in = c - b.first[t];
+        if (factor == 1.0f && b.src[t] == b.dst[t])
+            continue;                                      // nothing changes
+        if (b.dtype[t] == KMEANS_BF16)
+            scale_chunk<Bf16>(b.src[t], b.dst[t], b.numel[t], in, factor);
+        else if (b.dtype[t] == KMEANS_FP16)
+            scale_chunk<Fp16>(b.src[t], b.dst[t], b.numel[t], in, factor);
+        else
+            scale_chunk<Fp32>(b.src[t], b.dst[t], b.numel[t], in, factor);
+    }
+}
+
+__global__ __launch_bounds__(kClipThreads)
+void clip_finish_kernel(const double *__restrict__ partial, int partials,
+                        float *__restrict__ norm) {
+    const float n = total_norm(partial, partials);
+    if (threadIdx.x == 0)
+        *norm = n;
+}
+
+int64_t chunks_of(const kmeans_gradient_t &t) {
+    const int64_t per = kChunkBytes / static_cast<int64_t>(dtype_size(t.dtype));
+    return (t.numel + per - 1) / per;
+}
+
+kmeans_status_t check_list(const kmeans_gradient_t *list, int64_t count, bool clip,
+                           const float *norm) {
+    if (count < 0)
+        return fail(KMEANS_ERR_INVALID_ARG, "count=%lld must be >= 0",
+                    static_cast<long long>(count));
+    if (count > kMaxRows)
+        return fail(KMEANS_ERR_UNSUPPORTED, "count=%lld too large", static_cast<long long>(count));
+    if (!norm || (count > 0 && !list))
+        return fail(KMEANS_ERR_INVALID_ARG, "null pointer argument (list=%p norm=%p)",
+                    static_cast<const void *>(list), static_cast<const void *>(norm));
+    if (!aligned(norm, 4))
+        return fail(KMEANS_ERR_ALIGNMENT, "norm must be 4-byte aligned");
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const kmeans_gradient_t &t = list[i];
+        const auto at = static_cast<long long>(i);
+        if (t.numel < 0)
+            return fail(KMEANS_ERR_INVALID_ARG, "gradient %lld: numel=%lld must be >= 0", at,
+                        static_cast<long long>(t.numel));
+        if (t.dtype < KMEANS_BF16 || t.dtype > KMEANS_FP32)
+            return fail(KMEANS_ERR_INVALID_ARG, "gradient %lld: dtype=%d is not a kmeans_dtype_t",
+                        at, t.dtype);
+        if (t.reserved != 0)
+            return fail(KMEANS_ERR_INVALID_ARG, "gradient %lld: reserved must be 0", at);
+        if (t.numel == 0)
+            continue;
+        if (!t.src || (clip && !t.dst))
+            return fail(KMEANS_ERR_INVALID_ARG, "gradient %lld: null pointer (src=%p dst=%p)", at,
+                        t.src, t.dst);
+        if (!aligned(t.src, dtype_size(t.dtype)) || (clip && !aligned(t.dst, dtype_size(t.dtype))))
+            return fail(KMEANS_ERR_ALIGNMENT, "gradient %lld must be aligned to its element size",
+                        at);
+        if (t.numel > kMaxElements || (total += t.numel) > kMaxElements)
+            return fail(KMEANS_ERR_UNSUPPORTED, "gradients of more than 2^40 elements");
+    }
+    return KMEANS_OK;
+}
+
+kmeans_status_t run_clip(const kmeans_gradient_t *list, int64_t count, bool clip, float max_norm,
+                         float *norm, hipStream_t stream) {
+    kmeans_status_t st = check_list(list, count, clip, norm);
+    if (st != KMEANS_OK)
+        return st;
+    int64_t total = 0, tensors = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        total += chunks_of(list[i]);
+        tensors += list[i].numel > 0;
+    }
+    const int64_t batches = (tensors + kBatch - 1) / kBatch;
+    // Each batch gets its share of the workgroups, by chunks, and one at least.
+    const WorkspaceLease lease(stream, static_cast<size_t>(kMaxPartials + batches) * sizeof(double));
+    if (lease.error() != hipSuccess)
+        return fail(KMEANS_ERR_NO_MEMORY, "workspace of %lld partial sums: %s",
+                    static_cast<long long>(kMaxPartials + batches),
+                    hipGetErrorString(lease.error()));
+    auto *partial = static_cast<double *>(lease.ptr());
+    int partials = 0;
+    for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
+        int64_t i = 0;
+        int used = 0;
+        while (i < count) {
+            Batch b;
+            b.count = 0;
+            b.first_partial = used;
+            int64_t chunks = 0;
+            for (; i < count && b.count < kBatch; ++i) {
+                const kmeans_gradient_t &t = list[i];
+                if (t.numel == 0)
+                    continue;
+                b.src[b.count] = t.src;
+                b.dst[b.count] = t.dst;
+                b.numel[b.count] = t.numel;
+                b.dtype[b.count] = static_cast<uint8_t>(t.dtype);
+                b.first[b.count++] = static_cast<int>(chunks);
+                chunks += chunks_of(t);
+            }
+            if (b.count == 0)
+                break;
+            b.first[b.count] = static_cast<int>(chunks);
+            const int64_t share =
+                total <= kMaxPartials ? chunks : std::max<int64_t>(1, chunks * kMaxPartials / total);
+            if (pass == 0)
+                hipLaunchKernelGGL(clip_norm_kernel, dim3(static_cast<unsigned>(share)),
+                                   dim3(kClipThreads), 0, stream, b, partial);
+            else
+                hipLaunchKernelGGL(clip_scale_kernel, dim3(static_cast<unsigned>(share)),
+                                   dim3(kClipThreads), 0, stream, b, partial, partials, max_norm,
+                                   used == 0 ? norm : nullptr);
+            used += static_cast<int>(share);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return fail(KMEANS_ERR_HIP, "clip launch failed: %s", hipGetErrorString(e));
+        }
+        partials = used;
+    }
+    if (!clip || partials == 0) {
+        hipLaunchKernelGGL(clip_finish_kernel, dim3(1), dim3(kClipThreads), 0, stream, partial,
+                           partials, norm);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return fail(KMEANS_ERR_HIP, "norm launch failed: %s", hipGetErrorString(e));
+    }
+    return ok();
+}
+
+}  // namespace
+}  // namespace kmeans
+
+// ---- C entry points --------------------------------------------------------
+
+extern "C" kmeans_status_t kmeans_gradient_norm(const kmeans_gradient_t *list, int64_t count,
+                                                float *norm, hipStream_t stream) {
+    return kmeans::run_clip(list, count, false, 0.0f, norm, stream);
+}
+
+extern "C" kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t count,
+                                                 float max_norm, float *norm,
+                                                 hipStream_t stream) {
+    if (!(max_norm >= 0.0f))
+        return kmeans::fail(KMEANS_ERR_INVALID_ARG, "max_norm=%g must be >= 0",
+                            static_cast<double>(max_norm));
+    return kmeans::run_clip(list, count, true, max_norm, norm, stream);
+}

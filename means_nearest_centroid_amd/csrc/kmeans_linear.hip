@@ -1,0 +1,1095 @@
+// kmeans_linear.hip -- gfx950 kernels of the linear layer around a codebook
+// and of its gradients.
+//
+//     forward   Z = X W^T + b,  Y = act(Z) + R
+//     backward  dZ = dY * act'(Z),  dX = dZ W,  dW = dZ^T X,  db = sum_i dZ[i]
+//
+// All three products are one kernel, out[i][j] = sum_k P[i][k] Q[j][k], on
+// operands that lie in memory either with k contiguous or with their own row
+// index contiguous:
+//
+//     Y  (i = row,     j = F, k = D):  P = X  (k contiguous),  Q = W  (k contiguous)
+//     dX (i = row,     j = D, k = F):  P = dZ (k contiguous),  Q = W  (j contiguous)
+//     dW (i = feature, j = D, k = N):  P = dZ (i contiguous),  Q = X  (j contiguous)
+//
+// so no operand is ever transposed in memory: an operand whose own index is
+// contiguous is staged in LDS as it lies and transposed by the LDS reads
+// (ds_read_b64_tr_b16) on its way to the matrix instruction.
+#include <stdint.h>
+
+#include <algorithm>
+#include <memory>
+#include <type_traits>
+
+#include "kmeans_internal.h"
+#include "kmeans_types.h"
+
+namespace kmeans {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+#define KM_LDS __attribute__((address_space(3)))
+#define KM_INLINE __attribute__((always_inline))
+
+constexpr int kTileK = 64;            // k extent of a staged tile: two MFMA k-steps of 32
+constexpr uint32_t kOutOfRange = 0x80000000u;
+constexpr int64_t kMaxWidth = 1 << 20;   // D, F and row strides: 64 rows stay below 2^31 bytes
+constexpr int kMaxKSplits = 64;
+
+// ---- activations -----------------------------------------------------------
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// (erfc(|x|) / 2, exp(-x^2)) by Abramowitz and Stegun's formula 7.1.26 (a
+// degree-5 polynomial in 1 / (1 + p |x|) times exp(-x^2)), error below 1.5e-7.
+__device__ __forceinline__ float half_erfc_abs(float x, float &gauss) {
+    const float a = fabsf(x);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, a, 1.0f));
+    gauss = exp_fast(-a * a);
+    float p = 1.061405429f;
+    p = fmaf(p, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    return 0.5f * p * t * gauss;
+}
+
+// 1 / (1 + exp(-x)): 0 and 1 at the infinities.
+__device__ __forceinline__ float logistic(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x));
+}
+
+constexpr float kTanhC = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+
+__device__ __forceinline__ float activate(int act, float z) {
+    switch (act) {
+    case KMEANS_ACT_RELU:
+        return z <= 0.0f ? 0.0f : z;
+    case KMEANS_ACT_GELU: {
+        float g;
+        const float h = half_erfc_abs(z * kSqrtHalf, g);
+        return z * (z < 0.0f ? h : 1.0f - h);
+    }
+    case KMEANS_ACT_GELU_TANH:
+        // (1 + tanh(u)) / 2 = logistic(2 u)
+        return z * logistic(kTanhC * fmaf(kTanhA * z, z * z, z));
+    case KMEANS_ACT_SILU:
+        return z * logistic(z);
+    default:
+        return z;
+    }
+}
+
+// d * act'(z)
+__device__ __forceinline__ float activate_grad(int act, float z, float d) {
+    switch (act) {
+    case KMEANS_ACT_RELU:
+        return z <= 0.0f ? 0.0f : d;
+    case KMEANS_ACT_GELU: {
+        float g;
+        const float h = half_erfc_abs(z * kSqrtHalf, g);
+        const float phi = z < 0.0f ? h : 1.0f - h;
+        return d * fmaf(z * 0.3989422804014327f, g, phi);   // 1 / sqrt(2 pi)
+    }
+    case KMEANS_ACT_GELU_TANH: {
+        const float s = logistic(kTanhC * fmaf(kTanhA * z, z * z, z));
+        const float du = kTanhC * fmaf(3.0f * kTanhA * z, z, 1.0f);
+        return d * fmaf(z * s * (1.0f - s), du, s);
+    }
+    case KMEANS_ACT_SILU: {
+        const float s = logistic(z);
+        return d * fmaf(z * s, 1.0f - s, s);
+    }
+    default:
+        return d;
+    }
+}
+
+// ---- the product -----------------------------------------------------------
+
+struct Epilogue {
+    const void *bias;       // [J] or null
+    const void *residual;   // [I][J] or null
+    int64_t ldr;
+    void *out;              // [I][J]
+    int64_t ldo;
+    void *pre;              // [I][J] or null
+    int64_t ldp;
+    int act;
+};
+
+struct Product {
+    const void *P, *Q;
+    int64_t ldp, ldq;       // elements between rows as they lie in memory
+    int I, J, K;
+    bool p_padded;          // P's rows may be read up to a whole chunk of 8 (zeros past the end)
+    int k_chunk;            // k per split, a multiple of kTileK
+    int splits;
+    float *partial;         // [splits][I][J] fp32 when splits > 1
+    Epilogue epi;
+};
+
+template <typename B, int n>
+__device__ __forceinline__ Packed<B, n> load_packed(const B *p) {
+    return *reinterpret_cast<const Packed<B, n> *>(p);
+}
+
+// Up to V elements at any alignment: one access where all V exist.
+template <typename B, int V>
+__device__ __forceinline__ Packed<B, V> load_run(const B *p, int n) {
+    if (n >= V)
+        return load_packed<B, V>(p);
+    Packed<B, V> q = {};
+#pragma unroll
+    for (int c = 0; c < V - 1; ++c)
+        if (c < n)
+            q.v[c] = p[c];
+    return q;
+}
+template <typename B, int V>
+__device__ __forceinline__ void store_run(B *p, int n, const Packed<B, V> &q) {
+    if (n >= V) {
+        *reinterpret_cast<Packed<B, V> *>(p) = q;
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < V - 1; ++c)
+        if (c < n)
+            p[c] = q.v[c];
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate_run(float (&v)[8]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        v[c] = activate(ACT, v[c]);
+}
+
+// Eight consecutive outputs of row i from column j on (those below J): bias,
+// activation, residual, one rounding.
+template <typename T>
+__device__ __forceinline__ void finish_run(const Epilogue &e, int i, int j, int J, float (&v)[8]) {
+    typedef typename T::bits B;
+    const int n = J - j;
+    Packed<B, 8> q;
+    if (e.bias != nullptr) {
+        q = load_run<B, 8>(static_cast<const B *>(e.bias) + j, n);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            v[c] += T::widen(q.v[c]);
+    }
+    if (e.pre != nullptr) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            q.v[c] = T::narrow(v[c]);
+        store_run<B, 8>(static_cast<B *>(e.pre) + static_cast<int64_t>(i) * e.ldp + j, n, q);
+    }
+    switch (e.act) {
+    case KMEANS_ACT_RELU: activate_run<KMEANS_ACT_RELU>(v); break;
+    case KMEANS_ACT_GELU: activate_run<KMEANS_ACT_GELU>(v); break;
+    case KMEANS_ACT_GELU_TANH: activate_run<KMEANS_ACT_GELU_TANH>(v); break;
+    case KMEANS_ACT_SILU: activate_run<KMEANS_ACT_SILU>(v); break;
+    default: break;
+    }
+    if (e.residual != nullptr) {
+        q = load_run<B, 8>(static_cast<const B *>(e.residual) + static_cast<int64_t>(i) * e.ldr + j,
+                           n);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            v[c] += T::widen(q.v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        q.v[c] = T::narrow(v[c]);
+    store_run<B, 8>(static_cast<B *>(e.out) + static_cast<int64_t>(i) * e.ldo + j, n, q);
+}
+
+__device__ __forceinline__ f32x4 mfma(Bf16::mfma a, Bf16::mfma b, f32x4 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+#else
+    return c;
+#endif
+}
+__device__ __forceinline__ f32x4 mfma(Fp16::mfma a, Fp16::mfma b, f32x4 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+#else
+    return c;
+#endif
+}
+
+// s_waitcnt vmcnt(0): this wave's global-to-LDS copies have landed (a
+// workgroup barrier does not imply it).
+__device__ __forceinline__ void wait_vmem() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// One operand's tile of kTileK values of k by R values of its own index, as
+// it is staged in LDS.
+//
+//   own index contiguous == false: R rows of 64 k (128 bytes, 8 chunks of 16).
+//     Chunk c of row r lies at chunk c ^ ((r >> 1) & 7): the 16 rows that a
+//     ds_read_b128 group reads at one k cover all 64 banks once.
+//   own index contiguous == true: 64 rows (k) of R values (R / 16 granules of
+//     32 bytes).  Granule g of row k lies at g ^ f(k), f(k) = (k & 3) |
+//     ((k >> 3) & 3) << 2 (as many bits as there are granules): the 16 rows
+//     that one ds_read_b64_tr_b16 reads of one granule then lie in different
+//     granules, so in different banks.
+template <bool OWN, int R>
+struct TileMap {
+    static constexpr int kRows = OWN ? kTileK : R;
+    static constexpr int kRowBytes = (OWN ? R : kTileK) * 2;
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kBytes = kRows * kRowBytes;
+    static constexpr int kGranules = R / 16;
+
+    static __device__ __forceinline__ int spread(int k) {
+        return ((k & 3) | (((k >> 3) & 3) << 2)) & (kGranules - 1);
+    }
+    // The chunk of row r that lies at chunk slot c (its own inverse).
+    static __device__ __forceinline__ int chunk(int r, int c) {
+        if (OWN)
+            return (((c >> 1) ^ spread(r)) << 1) | (c & 1);
+        return c ^ ((r >> 1) & 7);
+    }
+};
+
+// Copies tiles of one operand from global memory into LDS, THREADS threads
+// together; tile t covers k in [t * 64, t * 64 + 64) of the workgroup's range.
+// Rows and columns past the operand's end read as zero where they are k
+// (so they add nothing), and as anything where they are the own index (their
+// outputs are not stored).
+//
+// DMA (16-byte aligned rows): buffer loads straight into LDS, nothing held in
+// registers.  Else: loads of 8 elements at any alignment into registers at
+// issue(), written to LDS at commit(); a chunk at the edge by elements.
+template <typename T, bool OWN, int R, int THREADS, bool DMA>
+struct Stager {
+    typedef TileMap<OWN, R> Map;
+    typedef typename T::bits B;
+    static constexpr int kPieces = Map::kBytes / 16 / THREADS;
+    static_assert(kPieces >= 1 && Map::kBytes % (16 * THREADS) == 0, "whole pieces per thread");
+
+    const B *base;        // element (0, 0) of the current range, own offset included
+    int64_t ld;
+    int own_lim;          // values of the own index that exist from base on
+    int k_len;            // k values of the range
+    int tid;
+    uint32_t off[DMA ? kPieces : 1];
+    u32x4 held[DMA ? 1 : kPieces];
+
+    // Piece u of this thread: row r and chunk c (elements 8 c ..) it fetches.
+    __device__ __forceinline__ void piece(int u, int &r, int &c) const {
+        const int o = DMA ? (((tid >> 6) * kPieces + u) * 64 + (tid & 63)) : u * THREADS + tid;
+        r = o / Map::kChunks;
+        c = Map::chunk(r, o % Map::kChunks);
+    }
+    __device__ __forceinline__ void init(const void *p, int64_t stride, int own0, int own,
+                                         int64_t k0, int k_n, int thread) {
+        ld = stride;
+        tid = thread;
+        own_lim = own - own0;
+        k_len = k_n;
+        base = static_cast<const B *>(p) + (OWN ? k0 * stride + own0 : own0 * stride + k0);
+        if constexpr (DMA) {
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                int r, c;
+                piece(u, r, c);
+                if (OWN)
+                    off[u] = c * 8 < own_lim ? static_cast<uint32_t>(r * ld + c * 8) * 2u
+                                             : kOutOfRange;
+                else
+                    off[u] = static_cast<uint32_t>(min(r, own_lim - 1) * ld + c * 8) * 2u;
+            }
+        }
+    }
+    // FULL: the tile is known to hold kTileK values of k.
+    template <bool FULL>
+    __device__ __forceinline__ void issue(int t, uint8_t *stage) {
+        const B *src = base + static_cast<int64_t>(t) * (OWN ? kTileK * ld : kTileK);
+        const int k_left = k_len - t * kTileK;
+        if constexpr (DMA) {
+#if defined(__HIP_DEVICE_COMPILE__)
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<B *>(src), 0, 0x7fffffff, 0x00020000);
+            uint8_t *dst = stage + __builtin_amdgcn_readfirstlane(tid >> 6) * (kPieces * 1024);
+            if (FULL || k_left >= kTileK) {
+#pragma unroll
+                for (int u = 0; u < kPieces; ++u)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        rs, (KM_LDS void *)(dst + u * 1024), 16, off[u], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kPieces; ++u) {
+                    int r, c;
+                    piece(u, r, c);
+                    const uint32_t o = (OWN ? r : c * 8) < k_left ? off[u] : kOutOfRange;
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        rs, (KM_LDS void *)(dst + u * 1024), 16, o, 0, 0, 0);
+                }
+            }
+#endif
+        } else {
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                int r, c;
+                piece(u, r, c);
+                const int row_lim = OWN ? k_left : own_lim;
+                const int n = (OWN ? own_lim : k_left) - c * 8;   // elements that exist
+                const B *p = src + r * ld + c * 8;
+                u32x4 v = {0, 0, 0, 0};
+                if (r < row_lim) {
+                    if (n >= 8) {
+                        v = __builtin_bit_cast(u32x4, load_packed<B, 8>(p));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 7; ++e)
+                            if (e < n)
+                                v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+                    }
+                }
+                held[u] = v;
+            }
+        }
+    }
+    // The tile issued last is in LDS once this returned on every wave and
+    // they met at a barrier.
+    __device__ __forceinline__ void commit(uint8_t *stage) {
+        if constexpr (!DMA) {
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u)
+                *reinterpret_cast<u32x4 *>(stage + (u * THREADS + tid) * 16) = held[u];
+        }
+    }
+};
+
+// Fragments of one operand for the 16x16x32 matrix instruction: lane l holds
+// own index l % 16 of a 16-wide block, k = 8 (l / 16) .. + 7 of a k-step.
+template <typename T, bool OWN, int R, int BLOCKS>
+struct Reader {
+    typedef TileMap<OWN, R> Map;
+    uint32_t off[OWN ? BLOCKS : 2];
+
+    __device__ __forceinline__ void init(int own0, int lane) {
+        const int l = lane & 15, g = lane >> 4;
+        if constexpr (OWN) {
+            const int k = 8 * g + (l >> 2);
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b)
+                off[b] = k * Map::kRowBytes + ((own0 / 16 + b) ^ Map::spread(k)) * 32 + (l & 3) * 8;
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                off[s] = (own0 + l) * Map::kRowBytes + Map::chunk(l, 4 * s + g) * 16;
+        }
+    }
+    __device__ __forceinline__ typename T::mfma read(const uint8_t *stage, int b, int s) const {
+        if constexpr (OWN) {
+            // Lane l of a group of 16 addresses k row l / 4, values 4 (l % 4)
+            // .. + 3; it receives value l of k rows 0 .. 3.  Two such reads
+            // make a lane's eight k.
+#if defined(__HIP_DEVICE_COMPILE__)
+            struct { s16x4 lo, hi; } v;
+            const uint8_t *p = stage + off[b] + s * 32 * Map::kRowBytes;
+            v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KM_LDS s16x4 *)(p));
+            v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (KM_LDS s16x4 *)(p + 4 * Map::kRowBytes));
+            return __builtin_bit_cast(typename T::mfma, v);
+#else
+            return typename T::mfma{};
+#endif
+        } else {
+            return __builtin_bit_cast(typename T::mfma,
+                                      *reinterpret_cast<const u32x4 *>(
+                                          stage + off[s] + b * 16 * Map::kRowBytes));
+        }
+    }
+};
+
+// Output tile of workgroup b: XCD x = b % 8 takes a contiguous eighth of the
+// tiles (each XCD has its own L2), ordered in bands of 8 tile rows so that
+// the tiles in flight together share rows of both operands.
+__device__ __forceinline__ void tile_of(int b, int ni, int nj, int &ti, int &tj) {
+    constexpr int kBand = 8;
+    const int n = ni * nj;
+    const int x = b & 7, q = n >> 3, rem = n & 7;
+    const int t = x * q + min(x, rem) + (b >> 3);
+    const int band = t / (kBand * nj);
+    const int i0 = band * kBand;
+    const int h = min(kBand, ni - i0);
+    const int in = t - i0 * nj;
+    tj = in / h;
+    ti = i0 + in - tj * h;
+}
+
+// One workgroup of WI x WJ waves computes a tile of (WI 16 TI) x (WJ 16 TJ)
+// outputs over one split of k.  The matrix instruction's A operand is Q and B
+// is P, so that a lane's four accumulator values are four consecutive j of
+// one row i.
+//
+// Two LDS stages; while tile t is multiplied, tile t + 1 is on its way.  Each
+// k-step is worked in phases of four P blocks: a phase's fragments are read
+// one phase ahead (double-buffered registers).  The barrier between tiles
+// stands before the last phase of a tile, whose fragments are in registers by
+// then: behind it the next tile's first fragments are read and the copy of
+// the tile after it starts into the stage just freed, both under the last
+// phase's matrix instructions.  The stages are distinct arrays and the loop
+// is unrolled by two so that the compiler can tell an LDS read of one stage
+// from a copy into the other.
+template <typename T, bool POWN, bool QOWN, int WI, int WJ, int TI, int TJ, bool DMA>
+__global__ __launch_bounds__(WI * WJ * 64, 2)
+void linear_tile_kernel(const Product g) {
+    constexpr int kThreads = WI * WJ * 64;
+    constexpr int RI = WI * TI * 16, RJ = WJ * TJ * 16;
+    constexpr int HB = TI < 4 ? TI : 4;       // P blocks of one phase
+    constexpr int NH = TI / HB;               // phases per k-step
+    constexpr int NP = 2 * NH;                // phases per tile
+    static_assert(TI % HB == 0 && NP % 2 == 0, "phases alternate fragment buffers");
+    typedef typename T::mfma Frag;
+    __shared__ __attribute__((aligned(16))) uint8_t p0[TileMap<POWN, RI>::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t p1[TileMap<POWN, RI>::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t q0[TileMap<QOWN, RJ>::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t q1[TileMap<QOWN, RJ>::kBytes];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ni = (g.I + RI - 1) / RI, nj = (g.J + RJ - 1) / RJ;
+    int ti, tj;
+    tile_of(blockIdx.x, ni, nj, ti, tj);
+    const int i0 = ti * RI, j0 = tj * RJ;
+    const int wi = (wave % WI) * TI * 16, wj = (wave / WI) * TJ * 16;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.y) * g.k_chunk;
+    const int k_len = static_cast<int>(min(static_cast<int64_t>(g.k_chunk), g.K - k0));
+    const int tiles = (k_len + kTileK - 1) / kTileK;
+
+    Stager<T, POWN, RI, kThreads, DMA> ps;
+    Stager<T, QOWN, RJ, kThreads, DMA> qs;
+    ps.init(g.P, g.ldp, i0, g.I, k0, k_len, tid);
+    qs.init(g.Q, g.ldq, j0, g.J, k0, k_len, tid);
+    Reader<T, POWN, RI, TI> pr;
+    Reader<T, QOWN, RJ, TJ> qr;
+    pr.init(wi, lane);
+    qr.init(wj, lane);
+
+    f32x4 acc[TI][TJ];
+#pragma unroll
+    for (int a = 0; a < TI; ++a)
+#pragma unroll
+        for (int b = 0; b < TJ; ++b)
+            acc[a][b] = f32x4{0, 0, 0, 0};
+    Frag pf[2][HB], qf[2][TJ];
+
+    auto read_phase = [&](const uint8_t *pst, const uint8_t *qst, int ph) KM_INLINE {
+        const int s = ph / NH, h = ph % NH;
+        if (h == 0) {
+#pragma unroll
+            for (int b = 0; b < TJ; ++b)
+                qf[s][b] = qr.read(qst, b, s);
+        }
+#pragma unroll
+        for (int a = 0; a < HB; ++a)
+            pf[ph & 1][a] = pr.read(pst, h * HB + a, s);
+    };
+    auto multiply = [&](int ph) KM_INLINE {
+        const int s = ph / NH, h = ph % NH;
+#pragma unroll
+        for (int a = 0; a < HB; ++a)
+#pragma unroll
+            for (int b = 0; b < TJ; ++b)
+                acc[h * HB + a][b] = mfma(qf[s][b], pf[ph & 1][a], acc[h * HB + a][b]);
+    };
+    // FULL: tiles t + 1 and t + 2 exist and t + 2 is a whole one, so the step
+    // has no branches (a branch around the copies would cost the compiler its
+    // knowledge of which stage they write, and a wait before the next reads).
+    auto step = [&](auto full, int t, uint8_t *pc, uint8_t *qc, uint8_t *pn,
+                    uint8_t *qn) KM_INLINE {
+        constexpr bool FULL = decltype(full)::value;
+#pragma unroll
+        for (int ph = 0; ph + 1 < NP; ++ph) {
+            read_phase(pc, qc, ph + 1);
+            multiply(ph);
+            // Fragment reads one by one between the matrix instructions.
+            const int reads = (POWN ? 2 : 1) * HB + ((ph + 1) % NH == 0 ? (QOWN ? 2 : 1) * TJ : 0);
+#pragma unroll
+            for (int r = 0; r < reads; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (FULL || t + 1 < tiles) {
+            ps.commit(pn);
+            qs.commit(qn);
+            if (DMA)
+                wait_vmem();
+            __syncthreads();
+            read_phase(pn, qn, 0);
+            if (FULL || t + 2 < tiles) {
+                ps.template issue<FULL>(t + 2, pc);
+                qs.template issue<FULL>(t + 2, qc);
+            }
+        }
+        multiply(NP - 1);
+        if (FULL && DMA) {
+            constexpr int kReads = (POWN ? 2 : 1) * HB + (QOWN ? 2 : 1) * TJ;
+            constexpr int kCopies = decltype(ps)::kPieces + decltype(qs)::kPieces;
+#pragma unroll
+            for (int r = 0; r < kCopies; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, kReads / kCopies, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // one copy
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    ps.template issue<false>(0, p0);
+    qs.template issue<false>(0, q0);
+    ps.commit(p0);
+    qs.commit(q0);
+    if (DMA)
+        wait_vmem();
+    __syncthreads();
+    if (tiles > 1) {
+        ps.template issue<false>(1, p1);
+        qs.template issue<false>(1, q1);
+    }
+    read_phase(p0, q0, 0);
+    int t = 0;
+    if constexpr (DMA) {
+        for (const int whole = k_len / kTileK; t + 3 < whole; t += 2) {
+            step(std::true_type{}, t, p0, q0, p1, q1);
+            step(std::true_type{}, t + 1, p1, q1, p0, q0);
+        }
+    }
+    for (; t < tiles; t += 2) {
+        step(std::false_type{}, t, p0, q0, p1, q1);
+        if (t + 1 < tiles)
+            step(std::false_type{}, t + 1, p1, q1, p0, q0);
+    }
+
+    const int l = lane & 15, g4 = lane >> 4;
+    if (g.splits > 1) {
+        float *part = g.partial + static_cast<int64_t>(blockIdx.y) * g.I * g.J;
+#pragma unroll
+        for (int a = 0; a < TI; ++a) {
+            const int i = i0 + wi + a * 16 + l;
+            if (i >= g.I)
+                continue;
+#pragma unroll
+            for (int b = 0; b < TJ; ++b) {
+                const int j = j0 + wj + b * 16 + g4 * 4;
+                store_run<float, 4>(part + static_cast<int64_t>(i) * g.J + j, g.J - j,
+                                    __builtin_bit_cast(Packed<float, 4>, acc[a][b]));
+            }
+        }
+        return;
+    }
+    // The accumulators hold quads scattered over 16 rows.  Each wave passes
+    // them through its own 16 KiB of the stages (64 rows of 64 floats; chunk c
+    // of row r at chunk c ^ (r % 16), so neither side meets bank conflicts)
+    // and takes them back as runs of eight columns: a wave's loads and stores
+    // then cover whole 128-byte lines, and the epilogue exists once.
+    static_assert(TJ == 4 && TI % 4 == 0, "64 x 64 outputs pass at a time");
+    static_assert(WI * WJ * 16384 == 4 * sizeof(p0) && sizeof(p0) == sizeof(q0),
+                  "the stages hold 16 KiB per wave");
+    constexpr int kPerArray = WI * WJ / 4;
+    uint8_t *arrays[4] = {p0, p1, q0, q1};
+    uint8_t *mine = wave / kPerArray == 0 ? arrays[0] : wave / kPerArray == 1 ? arrays[1]
+                  : wave / kPerArray == 2 ? arrays[2] : arrays[3];
+    mine += (wave % kPerArray) * 16384;
+    __syncthreads();
+#pragma unroll
+    for (int half = 0; half < TI / 4; ++half) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                *reinterpret_cast<f32x4 *>(mine + (a * 16 + l) * 256 + ((b * 4 + g4) ^ l) * 16) =
+                    acc[half * 4 + a][b];
+        // One wave writes and reads the region, in program order; the fence
+        // keeps the compiler to it.
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int r8 = lane >> 3, c8 = lane & 7;
+        const int j = j0 + wj + c8 * 8;
+#pragma unroll 1
+        for (int r = r8; r < 64; r += 8) {
+            const int i = i0 + wi + half * 64 + r;
+            float v[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(
+                    mine + r * 256 + ((2 * c8 + h) ^ (r & 15)) * 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[4 * h + c] = x[c];
+            }
+            if (i < g.I && j < g.J)
+                finish_run<T>(g.epi, i, j, g.J, v);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// Joins the splits of a product: each run of eight outputs adds its partial
+// sums in split order and goes through the epilogue.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads)
+void linear_join_kernel(const Product g) {
+    const int runs = (g.J + 7) / 8;
+    const int64_t total = static_cast<int64_t>(g.I) * runs;
+    const int64_t plane = static_cast<int64_t>(g.I) * g.J;
+    for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; x < total;
+         x += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
+        const int i = static_cast<int>(x / runs), j = static_cast<int>(x % runs) * 8;
+        const float *p = g.partial + static_cast<int64_t>(i) * g.J + j;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int s = 0; s < g.splits; ++s) {
+            const Packed<float, 8> w = load_run<float, 8>(p + s * plane, g.J - j);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[c] += w.v[c];
+        }
+        finish_run<T>(g.epi, i, j, g.J, v);
+    }
+}
+
+// ---- dZ and the bias gradient ----------------------------------------------
+
+// dZ = dY * act'(Z), rounded once, rows ldz apart (a multiple of 8 elements,
+// 16-byte aligned), and the column sums of the unrounded dZ over this
+// workgroup's rows.  A lane owns eight columns; the workgroup's 256 lanes
+// cover `lanes` groups of eight columns (a power of two) and 256 / lanes rows
+// at a time.  The sums of the row groups meet in LDS in a fixed order.
+constexpr int kDzThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kDzThreads)
+void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp, int N, int F,
+                      int act, int lanes_log2, int rows_per_wg, void *dZ, int64_t ldz,
+                      float *col_partial) {
+    typedef typename T::bits B;
+    __shared__ float sums[kDzThreads][9];
+    const int tid = threadIdx.x;
+    const int lanes = 1 << lanes_log2;
+    const int groups = kDzThreads >> lanes_log2;
+    const int c0 = (blockIdx.y * lanes + (tid & (lanes - 1))) * 8;
+    const int r_first = blockIdx.x * rows_per_wg;
+    const int r_end = min(N, r_first + rows_per_wg);
+    const int n = F - c0;     // columns that exist (may be <= 0)
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n > 0) {
+        for (int r = r_first + (tid >> lanes_log2); r < r_end; r += groups) {
+            const B *y = static_cast<const B *>(dY) + r * ldy + c0;
+            const B *z = static_cast<const B *>(pre) + r * ldp + c0;
+            Packed<B, 8> d = {}, zz = {};
+            if (n >= 8) {
+                d = load_packed<B, 8>(y);
+                if (act != KMEANS_ACT_NONE)
+                    zz = load_packed<B, 8>(z);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (e < n) {
+                        d.v[e] = y[e];
+                        if (act != KMEANS_ACT_NONE)
+                            zz.v[e] = z[e];
+                    }
+            }
+            Packed<B, 8> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = activate_grad(act, T::widen(zz.v[e]), T::widen(d.v[e]));
+                s[e] += v;
+                o.v[e] = T::narrow(v);
+            }
+            if (dZ != nullptr) {
+                B *w = static_cast<B *>(dZ) + r * ldz + c0;   // the row's padding may be written
+                *reinterpret_cast<u32x4 *>(w) = __builtin_bit_cast(u32x4, o);
+            }
+        }
+    }
+    if (col_partial == nullptr)
+        return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        sums[tid][e] = s[e];
+    __syncthreads();
+    for (int x = tid; x < lanes * 8; x += kDzThreads) {
+        const int lane = x >> 3, e = x & 7;
+        float v = 0.0f;
+        for (int q = 0; q < groups; ++q)
+            v += sums[q * lanes + lane][e];
+        const int col = (blockIdx.y * lanes + lane) * 8 + e;
+        if (col < F)
+            col_partial[static_cast<int64_t>(blockIdx.x) * F + col] = v;
+    }
+}
+
+// db[j] = sum of the column partials: one workgroup per 16 columns, 16 threads
+// a column, each a fixed interleaved share of the rows, joined in LDS.
+constexpr int kBiasThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kBiasThreads)
+void linear_bias_kernel(const float *col_partial, int rows, int F, void *db) {
+    __shared__ float sums[16][17];
+    const int c = threadIdx.x & 15, w = threadIdx.x >> 4;
+    const int col = blockIdx.x * 16 + c;
+    float v = 0.0f;
+    if (col < F)
+        for (int r = w; r < rows; r += 16)
+            v += col_partial[static_cast<int64_t>(r) * F + col];
+    sums[w][c] = v;
+    __syncthreads();
+    if (w == 0 && col < F) {
+        for (int q = 1; q < 16; ++q)
+            v += sums[q][c];
+        static_cast<typename T::bits *>(db)[col] = T::narrow(v);
+    }
+}
+
+// Zeroes rows of 16-bit values (dW and db of an empty batch, dX of no features).
+__global__ __launch_bounds__(256)
+void linear_zero_kernel(uint16_t *p, int64_t rows, int cols, int64_t ld) {
+    const int64_t total = rows * cols;
+    for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < total;
+         x += static_cast<int64_t>(gridDim.x) * 256)
+        p[x / cols * ld + x % cols] = 0;
+}
+
+// ---- launch ----------------------------------------------------------------
+
+// Rows that DMA may read: 16-byte aligned base and stride.
+bool rows_aligned(const void *p, int64_t ld) {
+    return aligned(p, 16) && ld % 8 == 0;
+}
+
+// A product's workspace: its partial sums.
+size_t partial_bytes(const Product &g) {
+    return g.splits > 1 ? static_cast<size_t>(g.splits) * g.I * g.J * sizeof(float) : 0;
+}
+
+constexpr int kTile = 128;    // outputs per side of a workgroup's tile
+
+int64_t tile_count(const Product &g) {
+    return ((static_cast<int64_t>(g.I) + kTile - 1) / kTile) *
+           ((static_cast<int64_t>(g.J) + kTile - 1) / kTile);
+}
+
+// Splits k so that the tiles fill the CUs twice over (two workgroups share a
+// CU), each split at least four staged tiles long.
+void plan_product(Product &g, int compute_units) {
+    const int64_t tiles = tile_count(g);
+    const int64_t k_tiles = (g.K + kTileK - 1) / kTileK;
+    int64_t s = std::max<int64_t>(1, 2 * compute_units / tiles);
+    s = std::min<int64_t>({s, std::max<int64_t>(1, k_tiles / 4), kMaxKSplits});
+    const int64_t per = (k_tiles + s - 1) / s;
+    g.k_chunk = static_cast<int>(per * kTileK);
+    g.splits = static_cast<int>((k_tiles + per - 1) / per);
+}
+
+template <typename T, bool POWN, bool QOWN>
+hipError_t launch_product_modes(const Product &g, hipStream_t stream) {
+    const int64_t tiles = tile_count(g);
+    const dim3 grid(static_cast<unsigned>(tiles), g.splits);
+    const bool dma = rows_aligned(g.P, g.ldp) && rows_aligned(g.Q, g.ldq) &&
+                     (g.p_padded || (POWN ? g.I : g.K) % 8 == 0) &&
+                     (QOWN ? g.J : g.K) % 8 == 0;
+    if (dma)
+        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, true>), grid, dim3(256),
+                           0, stream, g);
+    else
+        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, false>), grid, dim3(256),
+                           0, stream, g);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && g.splits > 1) {
+        const int64_t runs = static_cast<int64_t>(g.I) * ((g.J + 7) / 8);
+        const unsigned wgs = static_cast<unsigned>(
+            std::min<int64_t>((runs + kJoinThreads - 1) / kJoinThreads, 4096));
+        hipLaunchKernelGGL((linear_join_kernel<T>), dim3(wgs), dim3(kJoinThreads), 0, stream, g);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+enum Modes { kForward, kInputGrad, kWeightGrad };
+
+template <typename T>
+hipError_t launch_product(const Product &g, Modes m, hipStream_t stream) {
+    switch (m) {
+    case kForward:
+        return launch_product_modes<T, false, false>(g, stream);
+    case kInputGrad:
+        return launch_product_modes<T, false, true>(g, stream);
+    default:
+        return launch_product_modes<T, true, true>(g, stream);
+    }
+}
+
+size_t align_up(size_t n) { return (n + 255) & ~size_t(255); }
+
+kmeans_status_t check_linear(int64_t N, int64_t D, int64_t F, int32_t dtype, int32_t activation) {
+    if (N < 0 || D < 1 || F < 1)
+        return fail(KMEANS_ERR_INVALID_ARG, "N=%lld must be >= 0, D=%lld and F=%lld >= 1",
+                    static_cast<long long>(N), static_cast<long long>(D),
+                    static_cast<long long>(F));
+    if (activation < KMEANS_ACT_NONE || activation > KMEANS_ACT_SILU)
+        return fail(KMEANS_ERR_INVALID_ARG, "activation=%d is not a kmeans_activation_t",
+                    activation);
+    if (dtype != KMEANS_BF16 && dtype != KMEANS_FP16)
+        return dtype == KMEANS_FP32
+                   ? fail(KMEANS_ERR_UNSUPPORTED, "fp32 is not supported: bf16 or fp16")
+                   : fail(KMEANS_ERR_INVALID_ARG, "dtype=%d is not a kmeans_dtype_t", dtype);
+    if (N > kMaxRows || D > kMaxWidth || F > kMaxWidth)
+        return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld, D=%lld or F=%lld too large (max %lld, "
+                    "%lld, %lld)", static_cast<long long>(N), static_cast<long long>(D),
+                    static_cast<long long>(F), static_cast<long long>(kMaxRows),
+                    static_cast<long long>(kMaxWidth), static_cast<long long>(kMaxWidth));
+    return KMEANS_OK;
+}
+
+// A matrix argument of 16-bit values: rows of `cols`, `ld` apart.
+kmeans_status_t check_rows(const char *name, const void *p, int64_t cols, int64_t ld) {
+    if (p == nullptr)
+        return fail(KMEANS_ERR_INVALID_ARG, "null pointer argument (%s)", name);
+    if (!aligned(p, 2))
+        return fail(KMEANS_ERR_ALIGNMENT, "%s must be 2-byte aligned", name);
+    if (ld < cols)
+        return fail(KMEANS_ERR_INVALID_ARG, "%s: row stride %lld below the row length %lld", name,
+                    static_cast<long long>(ld), static_cast<long long>(cols));
+    if (ld > kMaxWidth)
+        return fail(KMEANS_ERR_UNSUPPORTED, "%s: row stride %lld too large (max %lld)", name,
+                    static_cast<long long>(ld), static_cast<long long>(kMaxWidth));
+    return KMEANS_OK;
+}
+
+kmeans_status_t check_vector(const char *name, const void *p) {
+    if (!aligned(p, 2))
+        return fail(KMEANS_ERR_ALIGNMENT, "%s must be 2-byte aligned", name);
+    return KMEANS_OK;
+}
+
+template <typename T>
+hipError_t run_forward(const Product &g, hipStream_t stream) {
+    return launch_product<T>(g, kForward, stream);
+}
+
+// The launches of kmeans_linear_grad on workspace `ws`.
+struct GradPlan {
+    bool dz;                    // whether dZ is written (else dY stands for it)
+    int64_t ldz;
+    int lanes_log2, rows_per_wg, row_wgs, col_wgs;
+    size_t dz_at, col_at, part_at, bytes;
+    Product dx, dw;
+};
+
+template <typename T>
+hipError_t run_grad(const GradPlan &p, const void *dY, int64_t dy_stride, const void *pre,
+                    int64_t pre_stride, int N, int F, int act, bool want_dx, bool want_dw,
+                    void *dbias, char *ws, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    if (p.dz || dbias != nullptr) {
+        hipLaunchKernelGGL((linear_dz_kernel<T>), dim3(p.row_wgs, p.col_wgs), dim3(kDzThreads), 0,
+                           stream, dY, dy_stride, pre, pre_stride, N, F, act, p.lanes_log2,
+                           p.rows_per_wg, p.dz ? ws + p.dz_at : nullptr, p.ldz,
+                           dbias != nullptr ? reinterpret_cast<float *>(ws + p.col_at) : nullptr);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && dbias != nullptr) {
+        hipLaunchKernelGGL((linear_bias_kernel<T>), dim3((F + 15) / 16), dim3(kBiasThreads), 0,
+                           stream, reinterpret_cast<const float *>(ws + p.col_at), p.row_wgs, F,
+                           dbias);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && want_dx)
+        e = launch_product<T>(p.dx, kInputGrad, stream);
+    if (e == hipSuccess && want_dw)
+        e = launch_product<T>(p.dw, kWeightGrad, stream);
+    return e;
+}
+
+hipError_t zero_rows(void *p, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
+    if (p == nullptr)
+        return hipSuccess;
+    const unsigned wgs = static_cast<unsigned>(std::min<int64_t>((rows * cols + 255) / 256, 8192));
+    hipLaunchKernelGGL(linear_zero_kernel, dim3(wgs), dim3(256), 0, stream,
+                       static_cast<uint16_t *>(p), rows, static_cast<int>(cols), ld);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace kmeans
+
+// ---- C entry points --------------------------------------------------------
+
+extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const void *W,
+                                         int64_t w_stride, const void *bias, const void *residual,
+                                         int64_t residual_stride, int64_t N, int64_t D, int64_t F,
+                                         int32_t dtype, int32_t activation, void *Y,
+                                         int64_t y_stride, void *pre, int64_t pre_stride,
+                                         hipStream_t stream) {
+    using namespace kmeans;
+    kmeans_status_t st = check_linear(N, D, F, dtype, activation);
+    if (st != KMEANS_OK)
+        return st;
+    if (N == 0)
+        return ok();
+    if ((st = check_rows("X", X, D, x_stride)) != KMEANS_OK ||
+        (st = check_rows("W", W, D, w_stride)) != KMEANS_OK ||
+        (st = check_rows("Y", Y, F, y_stride)) != KMEANS_OK ||
+        (st = check_vector("bias", bias)) != KMEANS_OK ||
+        (residual && (st = check_rows("residual", residual, F, residual_stride)) != KMEANS_OK) ||
+        (pre && (st = check_rows("pre", pre, F, pre_stride)) != KMEANS_OK))
+        return st;
+
+    Product g{};
+    g.P = X;
+    g.ldp = x_stride;
+    g.Q = W;
+    g.ldq = w_stride;
+    g.I = static_cast<int>(N);
+    g.J = static_cast<int>(F);
+    g.K = static_cast<int>(D);
+    g.epi = {bias, residual, residual_stride, Y, y_stride, pre, pre_stride, activation};
+    if (tile_count(g) > kMaxRows)
+        return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x F=%lld: too many outputs",
+                    static_cast<long long>(N), static_cast<long long>(F));
+    plan_product(g, device_compute_units());
+    std::unique_ptr<WorkspaceLease> lease;
+    const size_t bytes = partial_bytes(g);
+    if (bytes > 0) {
+        lease = std::make_unique<WorkspaceLease>(stream, bytes);
+        if (lease->error() != hipSuccess)
+            return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", bytes,
+                        hipGetErrorString(lease->error()));
+        g.partial = static_cast<float *>(lease->ptr());
+    }
+    const hipError_t e = dtype == KMEANS_BF16 ? run_forward<Bf16>(g, stream)
+                                              : run_forward<Fp16>(g, stream);
+    if (e != hipSuccess)
+        return fail(KMEANS_ERR_HIP, "linear launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride, const void *X,
+                                              int64_t x_stride, const void *W, int64_t w_stride,
+                                              const void *pre, int64_t pre_stride, int64_t N,
+                                              int64_t D, int64_t F, int32_t dtype,
+                                              int32_t activation, void *dX, int64_t dx_stride,
+                                              void *dW, int64_t dw_stride, void *dbias,
+                                              hipStream_t stream) {
+    using namespace kmeans;
+    kmeans_status_t st = check_linear(N, D, F, dtype, activation);
+    if (st != KMEANS_OK)
+        return st;
+    if ((dW && (st = check_rows("dW", dW, D, dw_stride)) != KMEANS_OK) ||
+        (st = check_vector("dbias", dbias)) != KMEANS_OK)
+        return st;
+    if (N == 0) {
+        hipError_t e = zero_rows(dW, F, D, dw_stride, stream);
+        if (e == hipSuccess)
+            e = zero_rows(dbias, 1, F, F, stream);
+        if (e != hipSuccess)
+            return fail(KMEANS_ERR_HIP, "linear gradient launch failed: %s", hipGetErrorString(e));
+        return ok();
+    }
+    if ((st = check_rows("dY", dY, F, dy_stride)) != KMEANS_OK ||
+        (dW && (st = check_rows("X", X, D, x_stride)) != KMEANS_OK) ||
+        (dX && (st = check_rows("W", W, D, w_stride)) != KMEANS_OK) ||
+        (dX && (st = check_rows("dX", dX, D, dx_stride)) != KMEANS_OK) ||
+        (activation != KMEANS_ACT_NONE && (st = check_rows("pre", pre, F, pre_stride)) != KMEANS_OK))
+        return st;
+    if (!dX && !dW && !dbias)
+        return ok();
+
+    const int cus = device_compute_units();
+    GradPlan p{};
+    // dZ is dY itself without an activation, where its rows can be staged as
+    // they lie; otherwise it is written once with rows of whole chunks.
+    p.dz = (dX || dW) &&
+           (activation != KMEANS_ACT_NONE || !rows_aligned(dY, dy_stride) || F % 8 != 0);
+    p.ldz = (F + 7) / 8 * 8;
+    const int64_t col_groups = p.ldz / 8;
+    while (p.lanes_log2 < 8 && (1 << p.lanes_log2) < col_groups)
+        ++p.lanes_log2;
+    p.col_wgs = static_cast<int>((col_groups + (1 << p.lanes_log2) - 1) >> p.lanes_log2);
+    // About eight workgroups per CU, each at least four rounds of rows.
+    const int64_t rows_round = kDzThreads >> p.lanes_log2;
+    int64_t row_wgs = std::max<int64_t>(1, 8 * cus / p.col_wgs);
+    row_wgs = std::min<int64_t>(row_wgs, (N + 4 * rows_round - 1) / (4 * rows_round));
+    p.rows_per_wg = static_cast<int>((N + row_wgs - 1) / row_wgs);
+    p.row_wgs = static_cast<int>((N + p.rows_per_wg - 1) / p.rows_per_wg);
+
+    const void *z = dY;
+    int64_t ldz = dy_stride;
+    size_t at = 0;
+    if (p.dz) {
+        p.dz_at = at;
+        at += align_up(static_cast<size_t>(N) * p.ldz * 2);
+    }
+    if (dbias) {
+        p.col_at = at;
+        at += align_up(static_cast<size_t>(p.row_wgs) * F * sizeof(float));
+    }
+    p.part_at = at;
+    p.dx.ldq = w_stride;
+    p.dx.I = static_cast<int>(N);
+    p.dx.J = static_cast<int>(D);
+    p.dx.K = static_cast<int>(F);
+    p.dx.Q = W;
+    p.dx.epi = {nullptr, nullptr, 0, dX, dx_stride, nullptr, 0, KMEANS_ACT_NONE};
+    p.dw.ldq = x_stride;
+    p.dw.I = static_cast<int>(F);
+    p.dw.J = static_cast<int>(D);
+    p.dw.K = static_cast<int>(N);
+    p.dw.Q = X;
+    p.dw.epi = {nullptr, nullptr, 0, dW, dw_stride, nullptr, 0, KMEANS_ACT_NONE};
+    if (tile_count(p.dx) > kMaxRows || tile_count(p.dw) > kMaxRows)
+        return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x D=%lld: too many outputs",
+                    static_cast<long long>(N), static_cast<long long>(D));
+    size_t part = 0;
+    if (dX) {
+        plan_product(p.dx, cus);
+        part = std::max(part, partial_bytes(p.dx));
+    }
+    if (dW) {
+        plan_product(p.dw, cus);
+        part = std::max(part, partial_bytes(p.dw));
+    }
+    p.bytes = at + part;
+    std::unique_ptr<WorkspaceLease> lease;
+    char *ws = nullptr;
+    if (p.bytes > 0) {
+        lease = std::make_unique<WorkspaceLease>(stream, p.bytes);
+        if (lease->error() != hipSuccess)
+            return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", p.bytes,
+                        hipGetErrorString(lease->error()));
+        ws = static_cast<char *>(lease->ptr());
+    }
+    if (p.dz) {
+        z = ws + p.dz_at;
+        ldz = p.ldz;
+    }
+    p.dx.P = p.dw.P = z;
+    p.dx.ldp = p.dw.ldp = ldz;
+    p.dx.p_padded = p.dw.p_padded = p.dz;
+    p.dx.partial = p.dw.partial = reinterpret_cast<float *>(ws + p.part_at);
+    const hipError_t e =
+        dtype == KMEANS_BF16
+            ? run_grad<Bf16>(p, dY, dy_stride, pre, pre_stride, static_cast<int>(N),
+                             static_cast<int>(F), activation, dX != nullptr, dW != nullptr, dbias,
+                             ws, stream)
+            : run_grad<Fp16>(p, dY, dy_stride, pre, pre_stride, static_cast<int>(N),
+                             static_cast<int>(F), activation, dX != nullptr, dW != nullptr, dbias,
+                             ws, stream);
+    if (e != hipSuccess)
+        return fail(KMEANS_ERR_HIP, "linear gradient launch failed: %s", hipGetErrorString(e));
+    return ok();
+}

@@ -64,6 +64,12 @@ __device__ __forceinline__ int sort_key(int32_t label, int K) {
     return (label < 0 || label >= K) ? K : label;
 }
 
+// A label as int32 (one outside its range as -1, a stray label too).
+__device__ __forceinline__ int32_t label32(int32_t label) { return label; }
+__device__ __forceinline__ int32_t label32(int64_t label) {
+    return label < 0 || label > INT32_MAX ? -1 : static_cast<int32_t>(label);
+}
+
 __device__ __forceinline__ float widen(uint32_t b16) { return __uint_as_float(b16 << 16); }
 
 // fp32 -> bf16 bits, nearest with ties to even; NaN -> the quiet NaN 0x7FC0
@@ -80,11 +86,11 @@ __device__ __forceinline__ uint32_t bf16_rne(float f) {
 
 // Digit histogram of one tile for the pass on (key >> shift) & mask, written
 // digit-major ([digit][tile], all 256 rows; rows above mask count zero).
-// FIRST: keys come from the labels, and the launch also clears the cluster
-// bounds (clear, n_clear entries).
-template <bool FIRST>
+// FIRST: keys come from the labels (of type L), and the launch also clears
+// the cluster bounds (clear, n_clear entries).
+template <bool FIRST, typename L>
 __global__ __launch_bounds__(kSortThreads)
-void upd_hist_kernel(const int32_t *__restrict__ keys_in, int N, int K, int shift, int mask,
+void upd_hist_kernel(const L *__restrict__ keys_in, int N, int K, int shift, int mask,
                      int tile_log2, int tiles, int stride, int32_t *__restrict__ hist, int32_t *__restrict__ clear,
                      int64_t n_clear) {
     __shared__ int h[kRadix];
@@ -108,7 +114,7 @@ void upd_hist_kernel(const int32_t *__restrict__ keys_in, int N, int K, int shif
         int v[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            v[u] = keys_in[beg + min(rel0 + u * kSortThreads + tid, len - 1)];
+            v[u] = label32(keys_in[beg + min(rel0 + u * kSortThreads + tid, len - 1)]);
 #if defined(__HIP_DEVICE_COMPILE__)
         static_assert(kBatch == 8, "the asm below names eight values");
         asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]),
@@ -232,9 +238,9 @@ void upd_scan_kernel(int32_t *__restrict__ h, int M) {
 // lane records the count, tagged with the round, in wcnt[wave][digit]; the
 // owner thread of each digit then turns the 16 counts into per-wave starts
 // (its running position plus the counts of earlier waves).
-template <bool FIRST, bool SCANNED>
+template <bool FIRST, bool SCANNED, typename L>
 __global__ __launch_bounds__(kScatterThreads)
-void upd_scatter_kernel(const int32_t *__restrict__ keys_in, const int32_t *__restrict__ vals_in,
+void upd_scatter_kernel(const L *__restrict__ keys_in, const int32_t *__restrict__ vals_in,
                         int N, int K, int shift, int mask, int tile_log2, int tiles,
                         int stride, const int32_t *__restrict__ hist, int32_t *__restrict__ keys_out,
                         int32_t *__restrict__ vals_out) {
@@ -265,7 +271,7 @@ void upd_scatter_kernel(const int32_t *__restrict__ keys_in, const int32_t *__re
 #pragma unroll
         for (int r = 0; r < kBatchRounds; ++r) {
             const int i = beg + min(rel0 + r * kScatterThreads + tid, len - 1);
-            bkey[r] = keys_in[i];
+            bkey[r] = label32(keys_in[i]);
             bval[r] = FIRST ? i : vals_in[i];
         }
     };
@@ -1572,7 +1578,107 @@ hipError_t launch_sums(const UpdatePlan &pl, const uint16_t *X, const int32_t *k
     return hipGetLastError();
 }
 
+// The radix passes of one sort; *keys and *vals receive the sorted keys
+// (label, K for a stray one) and the point indices.
+template <typename L>
+hipError_t launch_radix(const LabelSort &so, const L *labels, int N, int K, char *base,
+                        int32_t *clear, int64_t n_clear, int32_t **keys, int32_t **vals,
+                        hipStream_t stream) {
+    auto *hist = reinterpret_cast<int32_t *>(base + so.hist);
+    const size_t hsz = static_cast<size_t>(kRadix) * so.stride;
+    const bool scan = so.tiles > kFusedScanTiles;
+    const dim3 grid(so.tiles), block(kSortThreads), sblock(kScatterThreads);
+    const int mask = (1 << so.digit_bits) - 1;
+    hipError_t e = hipSuccess;
+    for (int q = 0; q < so.passes && e == hipSuccess; ++q) {
+        const int sh = so.digit_bits * q;
+        int32_t *h = hist + hsz * q;
+        const auto *kin = reinterpret_cast<const int32_t *>(base + so.keys[(q - 1) & 1]);
+        const auto *vin = reinterpret_cast<const int32_t *>(base + so.vals[(q - 1) & 1]);
+        *keys = reinterpret_cast<int32_t *>(base + so.keys[q & 1]);
+        *vals = reinterpret_cast<int32_t *>(base + so.vals[q & 1]);
+        if (q == 0)
+            hipLaunchKernelGGL((upd_hist_kernel<true, L>), grid, block, 0, stream, labels, N, K, 0,
+                               mask, so.tile_log2, so.tiles, so.stride, h, clear, n_clear);
+        else
+            hipLaunchKernelGGL((upd_hist_kernel<false, int32_t>), grid, block, 0, stream, kin, N,
+                               K, sh, mask, so.tile_log2, so.tiles, so.stride, h, nullptr,
+                               int64_t(0));
+        if (scan)
+            hipLaunchKernelGGL(upd_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, h,
+                               static_cast<int>(hsz));
+        if (q == 0 && scan)
+            hipLaunchKernelGGL((upd_scatter_kernel<true, true, L>), grid, sblock, 0, stream,
+                               labels, nullptr, N, K, sh, mask, so.tile_log2, so.tiles, so.stride,
+                               h, *keys, *vals);
+        else if (q == 0)
+            hipLaunchKernelGGL((upd_scatter_kernel<true, false, L>), grid, sblock, 0, stream,
+                               labels, nullptr, N, K, sh, mask, so.tile_log2, so.tiles, so.stride,
+                               h, *keys, *vals);
+        else if (scan)
+            hipLaunchKernelGGL((upd_scatter_kernel<false, true, int32_t>), grid, sblock, 0, stream,
+                               kin, vin, N, K, sh, mask, so.tile_log2, so.tiles, so.stride, h,
+                               *keys, *vals);
+        else
+            hipLaunchKernelGGL((upd_scatter_kernel<false, false, int32_t>), grid, sblock, 0,
+                               stream, kin, vin, N, K, sh, mask, so.tile_log2, so.tiles,
+                               so.stride, h, *keys, *vals);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
 }  // namespace
+
+LabelSort make_label_sort(int64_t N, int64_t K) {
+    LabelSort p{};
+    int bits = 0;
+    while ((int64_t(1) << bits) <= K)
+        ++bits;                                   // keys run 0..K
+    p.passes = (bits + 7) / 8;
+    // Even digits (K = 4096: 7 + 6 bits, not 8 + 5) halve the histogram rows
+    // the first pass's scatter reads and cost the second pass little.
+    p.digit_bits = (bits + p.passes - 1) / p.passes;
+    // Sort tiles of 2^tl >= 1024 points: at most 128 tiles while tiles stay
+    // <= 16384 points (the scan then holds its histogram in registers), at
+    // most 4096 beyond.
+    int tl = 10;
+    while (tl < 14 && (int64_t(1) << tl) * 128 < N)
+        ++tl;
+    while ((int64_t(1) << tl) * 4096 < N)
+        ++tl;
+    p.tile_log2 = tl;
+    p.tiles = static_cast<int>((N + (int64_t(1) << tl) - 1) >> tl);
+    p.stride = (p.tiles + 3) & ~3;
+    size_t off = 0;
+    const size_t n4 = align_up(static_cast<size_t>(N) * 4);
+    for (int i = 0; i < 2; ++i) {
+        p.keys[i] = off;
+        off += n4;
+        p.vals[i] = off;
+        off += n4;
+    }
+    p.hist = off;
+    off += align_up(static_cast<size_t>(p.passes) * kRadix * p.stride * 4);
+    p.bytes = off;
+    return p;
+}
+
+hipError_t launch_label_sort(const LabelSort &sort, const void *labels, int32_t label_type, int N,
+                             int K, void *ws, const int32_t **keys, const int32_t **vals,
+                             hipStream_t stream) {
+    int32_t *k = nullptr, *v = nullptr;
+    auto *base = static_cast<char *>(ws);
+    const hipError_t e =
+        label_type == KMEANS_INT64
+            ? launch_radix(sort, static_cast<const int64_t *>(labels), N, K, base, nullptr, 0, &k,
+                           &v, stream)
+            : launch_radix(sort, static_cast<const int32_t *>(labels), N, K, base, nullptr, 0, &k,
+                           &v, stream);
+    *keys = k;
+    *vals = v;
+    return e;
+}
 
 // Below this many clusters there are too few buckets to fill the GPU (one
 // workgroup each), and the radix path is used.
@@ -1613,38 +1719,12 @@ UpdatePlan make_update_plan(int64_t N, int64_t D, int64_t K, int compute_units, 
         p.bytes = off;
         return p;
     }
-    int bits = 0;
-    while ((int64_t(1) << bits) <= K)
-        ++bits;                                   // keys run 0..K
-    p.passes = (bits + 7) / 8;
-    // Even digits (K = 4096: 7 + 6 bits, not 8 + 5) halve the histogram rows
-    // the first pass's scatter reads and cost the second pass little.
-    p.digit_bits = (bits + p.passes - 1) / p.passes;
-    // Sort tiles of 2^tl >= 1024 points: at most 128 tiles while tiles stay
-    // <= 16384 points (the scan then holds its histogram in registers), at
-    // most 4096 beyond.
-    int tl = 10;
-    while (tl < 14 && (int64_t(1) << tl) * 128 < N)
-        ++tl;
-    while ((int64_t(1) << tl) * 4096 < N)
-        ++tl;
-    p.tile_log2 = tl;
-    p.tiles = static_cast<int>((N + (int64_t(1) << tl) - 1) >> tl);
-    p.stride = (p.tiles + 3) & ~3;
+    p.sort = make_label_sort(N, K);
     p.chunk = static_cast<int>(min(static_cast<int64_t>(kMaxChunk), kStageBytes / (2 * D)));
     p.chunks = static_cast<int>((N + p.chunk - 1) / p.chunk);
     if (N == 0)
         return p;
-    size_t off = 0;
-    const size_t n4 = align_up(static_cast<size_t>(N) * 4);
-    for (int i = 0; i < 2; ++i) {
-        p.keys[i] = off;
-        off += n4;
-        p.vals[i] = off;
-        off += n4;
-    }
-    p.hist = off;
-    off += align_up(static_cast<size_t>(p.passes) * kRadix * p.stride * 4);
+    size_t off = p.sort.bytes;
     p.start = off;
     off += align_up(static_cast<size_t>(K) * 4);
     p.end = off;
@@ -1687,44 +1767,10 @@ hipError_t launch_update(const UpdatePlan &pl, const uint16_t *X, const int32_t 
         start = reinterpret_cast<int32_t *>(base + pl.start);
         end = reinterpret_cast<int32_t *>(base + pl.end);
         partial = reinterpret_cast<float *>(base + pl.partial);
-        auto *hist = reinterpret_cast<int32_t *>(base + pl.hist);
-        const size_t hsz = static_cast<size_t>(kRadix) * pl.stride;
-        const bool scan = pl.tiles > kFusedScanTiles;
-        const dim3 grid(pl.tiles), block(kSortThreads);
-        hipError_t e = hipSuccess;
-        const int mask = (1 << pl.digit_bits) - 1;
-        for (int q = 0; q < pl.passes && e == hipSuccess; ++q) {
-            const int sh = pl.digit_bits * q;
-            int32_t *h = hist + hsz * q;
-            const int32_t *kin = q == 0 ? labels : reinterpret_cast<int32_t *>(base + pl.keys[(q - 1) & 1]);
-            const int32_t *vin = q == 0 ? nullptr : reinterpret_cast<int32_t *>(base + pl.vals[(q - 1) & 1]);
-            keys = reinterpret_cast<int32_t *>(base + pl.keys[q & 1]);
-            vals = reinterpret_cast<int32_t *>(base + pl.vals[q & 1]);
-            if (q == 0)   // also clears start and end (adjacent in the workspace)
-                hipLaunchKernelGGL(upd_hist_kernel<true>, grid, block, 0, stream, kin, N, K, 0,
-                                   mask, pl.tile_log2, pl.tiles, pl.stride, h, start,
-                                   static_cast<int64_t>((pl.partial - pl.start) / 4));
-            else
-                hipLaunchKernelGGL(upd_hist_kernel<false>, grid, block, 0, stream, kin, N, K, sh,
-                                   mask, pl.tile_log2, pl.tiles, pl.stride, h, nullptr, int64_t(0));
-            if (scan)
-                hipLaunchKernelGGL(upd_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, h,
-                                   static_cast<int>(hsz));
-            const dim3 sblock(kScatterThreads);
-            if (q == 0 && scan)
-                hipLaunchKernelGGL((upd_scatter_kernel<true, true>), grid, sblock, 0, stream, kin,
-                                   vin, N, K, sh, mask, pl.tile_log2, pl.tiles, pl.stride, h, keys, vals);
-            else if (q == 0)
-                hipLaunchKernelGGL((upd_scatter_kernel<true, false>), grid, sblock, 0, stream, kin,
-                                   vin, N, K, sh, mask, pl.tile_log2, pl.tiles, pl.stride, h, keys, vals);
-            else if (scan)
-                hipLaunchKernelGGL((upd_scatter_kernel<false, true>), grid, sblock, 0, stream, kin,
-                                   vin, N, K, sh, mask, pl.tile_log2, pl.tiles, pl.stride, h, keys, vals);
-            else
-                hipLaunchKernelGGL((upd_scatter_kernel<false, false>), grid, sblock, 0, stream, kin,
-                                   vin, N, K, sh, mask, pl.tile_log2, pl.tiles, pl.stride, h, keys, vals);
-            e = hipGetLastError();
-        }
+        // The first pass also clears start and end (adjacent in the workspace).
+        const hipError_t e = launch_radix(pl.sort, labels, N, K, base, start,
+                                          static_cast<int64_t>((pl.partial - pl.start) / 4),
+                                          &keys, &vals, stream);
         if (e != hipSuccess)
             return e;
     }

@@ -6,6 +6,29 @@
 
 namespace kmeans {
 
+// Workspace layout and launch shape of one stable radix sort of N labels in
+// [0, K), stray ones last (the update's sort path, the lookup's gradient).
+struct LabelSort {
+    int passes;        // radix passes over the keys 0..K (K = stray label)
+    int digit_bits;    // bits per pass (<= 8): the key bits split evenly
+    int tile_log2;     // sort tile of 2^tile_log2 points (>= 1024)
+    int tiles;         // sort tiles
+    int stride;        // histogram row length: tiles rounded up to 4
+    size_t keys[2], vals[2];   // byte offsets of the ping-pong sort buffers
+    size_t hist;       // [passes][256][stride] int32
+    size_t bytes;      // total workspace
+};
+
+// Requires 1 <= N < 2^31, 1 <= K < 2^31.
+LabelSort make_label_sort(int64_t N, int64_t K);
+
+// The sort's launches on `stream`, scratch of sort.bytes at ws; labels are
+// int32 or int64 (kmeans_label_t).  *keys receives the sorted keys (the
+// label, or K for one outside [0, K)) and *vals their positions, both in ws.
+hipError_t launch_label_sort(const LabelSort &sort, const void *labels, int32_t label_type, int N,
+                             int K, void *ws, const int32_t **keys, const int32_t **vals,
+                             hipStream_t stream);
+
 // Workspace layout and launch shape of one kmeans_update call.
 struct UpdatePlan {
     int path;          // 1: radix sort + chunked reduce + finish; 2: buckets
@@ -16,15 +39,9 @@ struct UpdatePlan {
     int bucket_log2, buckets, bin_tile_log2, bin_tiles;
     size_t sidx, dir;
     // path 1
-    int passes;        // radix passes over the keys 0..K (K = stray label)
-    int digit_bits;    // bits per pass (<= 8): the key bits split evenly
-    int tile_log2;     // sort tile of 2^tile_log2 points (>= 1024)
-    int tiles;         // sort tiles
-    int stride;        // histogram row length: tiles rounded up to 4
+    LabelSort sort;    // its workspace comes first
     int chunk;         // sorted positions per reduce chunk (32 KiB of rows, <= 240)
     int chunks;        // reduce chunks
-    size_t keys[2], vals[2];   // byte offsets of the ping-pong sort buffers
-    size_t hist;       // [passes][256][stride] int32
     size_t start, end; // [K] int32 each
     size_t partial;    // [chunks][2][D] fp32
     size_t bytes;      // total workspace (0 when N == 0)
