@@ -129,7 +129,8 @@ struct Product {
     const void *P, *Q;
     int64_t ldp, ldq;       // elements between rows as they lie in memory
     int I, J, K;
-    bool p_padded;          // P's rows may be read up to a whole chunk of 8 (zeros past the end)
+    bool dma;               // both operands' rows are 16-byte aligned and of whole chunks of 8
+    int shape;              // Shape
     int k_chunk;            // k per split, a multiple of kTileK
     int splits;
     float *partial;         // [splits][I][J] fp32 when splits > 1
@@ -165,31 +166,31 @@ __device__ __forceinline__ void store_run(B *p, int n, const Packed<B, V> &q) {
             p[c] = q.v[c];
 }
 
-template <int ACT>
-__device__ __forceinline__ void activate_run(float (&v)[8]) {
+template <int ACT, int V>
+__device__ __forceinline__ void activate_run(float (&v)[V]) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int c = 0; c < V; ++c)
         v[c] = activate(ACT, v[c]);
 }
 
-// Eight consecutive outputs of row i from column j on (those below J): bias,
+// V consecutive outputs of row i from column j on (those below J): bias,
 // activation, residual, one rounding.
-template <typename T>
-__device__ __forceinline__ void finish_run(const Epilogue &e, int i, int j, int J, float (&v)[8]) {
+template <typename T, int V>
+__device__ __forceinline__ void finish_run(const Epilogue &e, int i, int j, int J, float (&v)[V]) {
     typedef typename T::bits B;
     const int n = J - j;
-    Packed<B, 8> q;
+    Packed<B, V> q;
     if (e.bias != nullptr) {
-        q = load_run<B, 8>(static_cast<const B *>(e.bias) + j, n);
+        q = load_run<B, V>(static_cast<const B *>(e.bias) + j, n);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < V; ++c)
             v[c] += T::widen(q.v[c]);
     }
     if (e.pre != nullptr) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < V; ++c)
             q.v[c] = T::narrow(v[c]);
-        store_run<B, 8>(static_cast<B *>(e.pre) + static_cast<int64_t>(i) * e.ldp + j, n, q);
+        store_run<B, V>(static_cast<B *>(e.pre) + static_cast<int64_t>(i) * e.ldp + j, n, q);
     }
     switch (e.act) {
     case KMEANS_ACT_RELU: activate_run<KMEANS_ACT_RELU>(v); break;
@@ -199,16 +200,16 @@ __device__ __forceinline__ void finish_run(const Epilogue &e, int i, int j, int 
     default: break;
     }
     if (e.residual != nullptr) {
-        q = load_run<B, 8>(static_cast<const B *>(e.residual) + static_cast<int64_t>(i) * e.ldr + j,
+        q = load_run<B, V>(static_cast<const B *>(e.residual) + static_cast<int64_t>(i) * e.ldr + j,
                            n);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < V; ++c)
             v[c] += T::widen(q.v[c]);
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int c = 0; c < V; ++c)
         q.v[c] = T::narrow(v[c]);
-    store_run<B, 8>(static_cast<B *>(e.out) + static_cast<int64_t>(i) * e.ldo + j, n, q);
+    store_run<B, V>(static_cast<B *>(e.out) + static_cast<int64_t>(i) * e.ldo + j, n, q);
 }
 
 __device__ __forceinline__ f32x4 mfma(Bf16::mfma a, Bf16::mfma b, f32x4 c) {
@@ -226,9 +227,23 @@ __device__ __forceinline__ f32x4 mfma(Fp16::mfma a, Fp16::mfma b, f32x4 c) {
 #endif
 }
 
-// s_waitcnt vmcnt(0): this wave's global-to-LDS copies have landed (a
-// workgroup barrier does not imply it).
-__device__ __forceinline__ void wait_vmem() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+// s_waitcnt vmcnt(N): all but the last N global-to-LDS copies of this wave
+// have landed (a workgroup barrier does not imply it).
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+    static_assert(N < 64, "vmcnt has six bits");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier for LDS traffic alone: this wave's LDS reads and writes are
+// done, its copies may still be on their way (__syncthreads would wait for
+// every copy).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 // One operand's tile of kTileK values of k by R values of its own index, as
 // it is staged in LDS.
@@ -262,13 +277,15 @@ struct TileMap {
 
 // Copies tiles of one operand from global memory into LDS, THREADS threads
 // together; tile t covers k in [t * 64, t * 64 + 64) of the workgroup's range.
-// Rows and columns past the operand's end read as zero where they are k
-// (so they add nothing), and as anything where they are the own index (their
-// outputs are not stored).
+// Values past the range of k are zero (so they add nothing); values past the
+// own index are anything (their outputs are not stored), but nothing outside
+// the operand is read.
 //
-// DMA (16-byte aligned rows): buffer loads straight into LDS, nothing held in
-// registers.  Else: loads of 8 elements at any alignment into registers at
-// issue(), written to LDS at commit(); a chunk at the edge by elements.
+// DMA (16-byte aligned rows of whole chunks): buffer loads straight into LDS,
+// nothing held in registers.  Else: 16-byte buffer loads at the rows' own
+// alignment into registers at issue(), written to LDS at commit().  Such a load
+// may run past the end of its row, into the next one; in the operand's last
+// rows, and where k ends, the values are loaded one by one instead.
 template <typename T, bool OWN, int R, int THREADS, bool DMA>
 struct Stager {
     typedef TileMap<OWN, R> Map;
@@ -281,7 +298,7 @@ struct Stager {
     int own_lim;          // values of the own index that exist from base on
     int k_len;            // k values of the range
     int tid;
-    uint32_t off[DMA ? kPieces : 1];
+    uint32_t off[kPieces];
     u32x4 held[DMA ? 1 : kPieces];
 
     // Piece u of this thread: row r and chunk c (elements 8 c ..) it fetches.
@@ -297,28 +314,26 @@ struct Stager {
         own_lim = own - own0;
         k_len = k_n;
         base = static_cast<const B *>(p) + (OWN ? k0 * stride + own0 : own0 * stride + k0);
-        if constexpr (DMA) {
 #pragma unroll
-            for (int u = 0; u < kPieces; ++u) {
-                int r, c;
-                piece(u, r, c);
-                if (OWN)
-                    off[u] = c * 8 < own_lim ? static_cast<uint32_t>(r * ld + c * 8) * 2u
-                                             : kOutOfRange;
-                else
-                    off[u] = static_cast<uint32_t>(min(r, own_lim - 1) * ld + c * 8) * 2u;
-            }
+        for (int u = 0; u < kPieces; ++u) {
+            int r, c;
+            piece(u, r, c);
+            if (OWN)
+                off[u] = c * 8 < own_lim ? static_cast<uint32_t>(r * ld + c * 8) * 2u
+                                         : kOutOfRange;
+            else
+                off[u] = static_cast<uint32_t>(min(r, own_lim - 1) * ld + c * 8) * 2u;
         }
     }
-    // FULL: the tile is known to hold kTileK values of k.
+    // FULL: the tile is known to hold kTileK values of k, and k goes on after it.
     template <bool FULL>
     __device__ __forceinline__ void issue(int t, uint8_t *stage) {
+#if defined(__HIP_DEVICE_COMPILE__)
         const B *src = base + static_cast<int64_t>(t) * (OWN ? kTileK * ld : kTileK);
         const int k_left = k_len - t * kTileK;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<B *>(src), 0, 0x7fffffff, 0x00020000);
         if constexpr (DMA) {
-#if defined(__HIP_DEVICE_COMPILE__)
-            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<B *>(src), 0, 0x7fffffff, 0x00020000);
             uint8_t *dst = stage + __builtin_amdgcn_readfirstlane(tid >> 6) * (kPieces * 1024);
             if (FULL || k_left >= kTileK) {
 #pragma unroll
@@ -335,29 +350,33 @@ struct Stager {
                         rs, (KM_LDS void *)(dst + u * 1024), 16, o, 0, 0, 0);
                 }
             }
-#endif
-        } else {
+        } else if (FULL || k_left > kTileK) {
 #pragma unroll
+            for (int u = 0; u < kPieces; ++u)
+                held[u] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off[u], 0, 0));
+        } else {
+#pragma unroll 1
             for (int u = 0; u < kPieces; ++u) {
                 int r, c;
                 piece(u, r, c);
-                const int row_lim = OWN ? k_left : own_lim;
-                const int n = (OWN ? own_lim : k_left) - c * 8;   // elements that exist
-                const B *p = src + r * ld + c * 8;
-                u32x4 v = {0, 0, 0, 0};
-                if (r < row_lim) {
-                    if (n >= 8) {
-                        v = __builtin_bit_cast(u32x4, load_packed<B, 8>(p));
-                    } else {
+                const bool row = OWN ? r < k_left : true;
+                const int n = row ? (OWN ? own_lim : k_left) - c * 8 : 0;   // that exist
+                const uint32_t at = static_cast<uint32_t>((OWN ? r : min(r, own_lim - 1)) * ld +
+                                                          c * 8) * 2u;
+                uint32_t e[8];
 #pragma unroll
-                        for (int e = 0; e < 7; ++e)
-                            if (e < n)
-                                v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
-                    }
-                }
-                held[u] = v;
+                for (int x = 0; x < 8; ++x)
+                    e[x] = __builtin_amdgcn_raw_buffer_load_b16(
+                        rs, x < n ? at + 2 * x : kOutOfRange, 0, 0);
+                const u32x4 v = {e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
+                                 e[6] | e[7] << 16};
+#pragma unroll
+                for (int x = 0; x < kPieces; ++x)      // keeps held[] in registers
+                    held[x] = x == u ? v : held[x];
             }
         }
+#endif
     }
     // The tile issued last is in LDS once this returned on every wave and
     // they met at a barrier.
@@ -434,17 +453,20 @@ __device__ __forceinline__ void tile_of(int b, int ni, int nj, int &ti, int &tj)
 // is P, so that a lane's four accumulator values are four consecutive j of
 // one row i.
 //
-// Two LDS stages; while tile t is multiplied, tile t + 1 is on its way.  Each
-// k-step is worked in phases of four P blocks: a phase's fragments are read
-// one phase ahead (double-buffered registers).  The barrier between tiles
-// stands before the last phase of a tile, whose fragments are in registers by
-// then: behind it the next tile's first fragments are read and the copy of
-// the tile after it starts into the stage just freed, both under the last
-// phase's matrix instructions.  The stages are distinct arrays and the loop
-// is unrolled by two so that the compiler can tell an LDS read of one stage
-// from a copy into the other.
-template <typename T, bool POWN, bool QOWN, int WI, int WJ, int TI, int TJ, bool DMA>
-__global__ __launch_bounds__(WI * WJ * 64, 2)
+// S LDS stages; while tile t is multiplied, tiles t + 1 .. t + S - 1 are on
+// their way.  Each k-step is worked in phases of four P blocks: a phase's
+// fragments are read one phase ahead (double-buffered registers).  The
+// barrier between tiles stands before the last phase of a tile, whose
+// fragments are in registers by then: behind it the next tile's first
+// fragments are read and the copy of tile t + S starts into the stage just
+// freed, both under the last phase's matrix instructions.  The stages are
+// distinct arrays and the loop is unrolled by S so that the compiler can tell
+// an LDS read of one stage from a copy into another.
+template <int I>
+using Index = std::integral_constant<int, I>;
+
+template <typename T, bool POWN, bool QOWN, int WI, int WJ, int TI, int TJ, int S, bool DMA>
+__global__ __launch_bounds__(WI * WJ * 64, DMA ? 2 : 4)
 void linear_tile_kernel(const Product g) {
     constexpr int kThreads = WI * WJ * 64;
     constexpr int RI = WI * TI * 16, RJ = WJ * TJ * 16;
@@ -452,11 +474,26 @@ void linear_tile_kernel(const Product g) {
     constexpr int NH = TI / HB;               // phases per k-step
     constexpr int NP = 2 * NH;                // phases per tile
     static_assert(TI % HB == 0 && NP % 2 == 0, "phases alternate fragment buffers");
+    static_assert(S == 2 || (S == 4 && DMA), "registers hold one tile on its way");
     typedef typename T::mfma Frag;
-    __shared__ __attribute__((aligned(16))) uint8_t p0[TileMap<POWN, RI>::kBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t p1[TileMap<POWN, RI>::kBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t q0[TileMap<QOWN, RJ>::kBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t q1[TileMap<QOWN, RJ>::kBytes];
+    typedef TileMap<POWN, RI> PMap;
+    typedef TileMap<QOWN, RJ> QMap;
+    __shared__ __attribute__((aligned(16))) uint8_t p0[PMap::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t q0[QMap::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t p1[PMap::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t q1[QMap::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t p2[S > 2 ? PMap::kBytes : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t q2[S > 2 ? QMap::kBytes : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t p3[S > 2 ? PMap::kBytes : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t q3[S > 2 ? QMap::kBytes : 16];
+    auto p_stage = [&](auto i) KM_INLINE -> uint8_t * {
+        constexpr int n = decltype(i)::value % S;
+        return n == 0 ? p0 : n == 1 ? p1 : n == 2 ? p2 : p3;
+    };
+    auto q_stage = [&](auto i) KM_INLINE -> uint8_t * {
+        constexpr int n = decltype(i)::value % S;
+        return n == 0 ? q0 : n == 1 ? q1 : n == 2 ? q2 : q3;
+    };
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -505,12 +542,17 @@ void linear_tile_kernel(const Product g) {
             for (int b = 0; b < TJ; ++b)
                 acc[h * HB + a][b] = mfma(qf[s][b], pf[ph & 1][a], acc[h * HB + a][b]);
     };
-    // FULL: tiles t + 1 and t + 2 exist and t + 2 is a whole one, so the step
-    // has no branches (a branch around the copies would cost the compiler its
-    // knowledge of which stage they write, and a wait before the next reads).
-    auto step = [&](auto full, int t, uint8_t *pc, uint8_t *qc, uint8_t *pn,
-                    uint8_t *qn) KM_INLINE {
+    constexpr int kReads = (POWN ? 2 : 1) * HB + (QOWN ? 2 : 1) * TJ;
+    constexpr int kCopies = decltype(ps)::kPieces + decltype(qs)::kPieces;
+    // Tile t, in stage at % S.  FULL: tiles t + 1 .. t + S exist and t + S is a
+    // whole one (and not the last, without DMA), so the step has no branches (a branch around the copies would
+    // cost the compiler its knowledge of which stage they write, and a wait
+    // before the next reads).
+    auto step = [&](auto full, auto at, int t) KM_INLINE {
         constexpr bool FULL = decltype(full)::value;
+        uint8_t *pc = p_stage(at), *qc = q_stage(at);
+        uint8_t *pn = p_stage(Index<decltype(at)::value + 1>{});
+        uint8_t *qn = q_stage(Index<decltype(at)::value + 1>{});
 #pragma unroll
         for (int ph = 0; ph + 1 < NP; ++ph) {
             read_phase(pc, qc, ph + 1);
@@ -527,19 +569,17 @@ void linear_tile_kernel(const Product g) {
         if (FULL || t + 1 < tiles) {
             ps.commit(pn);
             qs.commit(qn);
-            if (DMA)
-                wait_vmem();
-            __syncthreads();
+            if constexpr (DMA)
+                wait_vmem<FULL ? (S - 2) * kCopies : 0>();
+            lds_barrier();
             read_phase(pn, qn, 0);
-            if (FULL || t + 2 < tiles) {
-                ps.template issue<FULL>(t + 2, pc);
-                qs.template issue<FULL>(t + 2, qc);
+            if (FULL || t + S < tiles) {
+                ps.template issue<FULL>(t + S, pc);
+                qs.template issue<FULL>(t + S, qc);
             }
         }
         multiply(NP - 1);
-        if (FULL && DMA) {
-            constexpr int kReads = (POWN ? 2 : 1) * HB + (QOWN ? 2 : 1) * TJ;
-            constexpr int kCopies = decltype(ps)::kPieces + decltype(qs)::kPieces;
+        if (FULL) {
 #pragma unroll
             for (int r = 0; r < kCopies; ++r) {
                 __builtin_amdgcn_sched_group_barrier(0x100, kReads / kCopies, 0);
@@ -549,30 +589,49 @@ void linear_tile_kernel(const Product g) {
         }
         __builtin_amdgcn_sched_barrier(0);
     };
+    auto start = [&](auto at) KM_INLINE {
+        constexpr int n = decltype(at)::value;
+        if (n < tiles) {
+            ps.template issue<false>(n, p_stage(at));
+            qs.template issue<false>(n, q_stage(at));
+        }
+    };
 
-    ps.template issue<false>(0, p0);
-    qs.template issue<false>(0, q0);
+    start(Index<0>{});
     ps.commit(p0);
     qs.commit(q0);
-    if (DMA)
-        wait_vmem();
-    __syncthreads();
-    if (tiles > 1) {
-        ps.template issue<false>(1, p1);
-        qs.template issue<false>(1, q1);
+    start(Index<1>{});
+    if constexpr (S > 2) {
+        start(Index<2>{});
+        start(Index<3>{});
     }
+    if constexpr (DMA)
+        // All stages were started: only the first need have landed.
+        if (tiles >= S)
+            wait_vmem<(S - 1) * kCopies>();
+        else
+            wait_vmem<0>();
+    lds_barrier();
     read_phase(p0, q0, 0);
     int t = 0;
-    if constexpr (DMA) {
-        for (const int whole = k_len / kTileK; t + 3 < whole; t += 2) {
-            step(std::true_type{}, t, p0, q0, p1, q1);
-            step(std::true_type{}, t + 1, p1, q1, p0, q0);
+    for (const int whole = DMA ? k_len / kTileK : tiles - 1; t + 2 * S - 1 < whole; t += S) {
+        step(std::true_type{}, Index<0>{}, t);
+        step(std::true_type{}, Index<1>{}, t + 1);
+        if constexpr (S > 2) {
+            step(std::true_type{}, Index<2>{}, t + 2);
+            step(std::true_type{}, Index<3>{}, t + 3);
         }
     }
-    for (; t < tiles; t += 2) {
-        step(std::false_type{}, t, p0, q0, p1, q1);
+    for (; t < tiles; t += S) {
+        step(std::false_type{}, Index<0>{}, t);
         if (t + 1 < tiles)
-            step(std::false_type{}, t + 1, p1, q1, p0, q0);
+            step(std::false_type{}, Index<1>{}, t + 1);
+        if constexpr (S > 2) {
+            if (t + 2 < tiles)
+                step(std::false_type{}, Index<2>{}, t + 2);
+            if (t + 3 < tiles)
+                step(std::false_type{}, Index<3>{}, t + 3);
+        }
     }
 
     const int l = lane & 15, g4 = lane >> 4;
@@ -593,73 +652,144 @@ void linear_tile_kernel(const Product g) {
         return;
     }
     // The accumulators hold quads scattered over 16 rows.  Each wave passes
-    // them through its own 16 KiB of the stages (64 rows of 64 floats; chunk c
-    // of row r at chunk c ^ (r % 16), so neither side meets bank conflicts)
-    // and takes them back as runs of eight columns: a wave's loads and stores
-    // then cover whole 128-byte lines, and the epilogue exists once.
-    static_assert(TJ == 4 && TI % 4 == 0, "64 x 64 outputs pass at a time");
-    static_assert(WI * WJ * 16384 == 4 * sizeof(p0) && sizeof(p0) == sizeof(q0),
-                  "the stages hold 16 KiB per wave");
-    constexpr int kPerArray = WI * WJ / 4;
-    uint8_t *arrays[4] = {p0, p1, q0, q1};
-    uint8_t *mine = wave / kPerArray == 0 ? arrays[0] : wave / kPerArray == 1 ? arrays[1]
-                  : wave / kPerArray == 2 ? arrays[2] : arrays[3];
-    mine += (wave % kPerArray) * 16384;
+    // them, 64 rows at a time, through its own part of the first two stages
+    // (rows of 16 TJ floats; chunk c of row r at a place that spreads both
+    // sides' accesses over the banks) and takes them back as runs of eight
+    // columns: a wave's loads and stores then cover whole rows, and the
+    // epilogue's code exists once.
+    constexpr int kRowFloats = TJ * 16;
+    constexpr int kPass = 64 * kRowFloats * 4;          // bytes of one wave's pass
+    constexpr int kPerArray = WI * WJ / 4;              // waves sharing one stage array
+    static_assert((TJ == 4 || TJ == 2) && TI % 4 == 0, "64-row passes");
+    static_assert(WI * WJ % 4 == 0 && kPerArray * kPass <= sizeof(p0) && sizeof(p0) == sizeof(q0),
+                  "the first two stages hold a pass of every wave");
+    auto spot = [](int r, int c) KM_INLINE {
+        return r * kRowFloats * 4 + (c ^ (TJ == 4 ? r & 15 : (r >> 1) & 7)) * 16;
+    };
+    uint8_t *mine = wave / kPerArray == 0 ? p0 : wave / kPerArray == 1 ? p1
+                  : wave / kPerArray == 2 ? q0 : q1;
+    mine += (wave % kPerArray) * kPass;
     __syncthreads();
 #pragma unroll
     for (int half = 0; half < TI / 4; ++half) {
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                *reinterpret_cast<f32x4 *>(mine + (a * 16 + l) * 256 + ((b * 4 + g4) ^ l) * 16) =
+            for (int b = 0; b < TJ; ++b)
+                *reinterpret_cast<f32x4 *>(mine + spot(a * 16 + l, b * 4 + g4)) =
                     acc[half * 4 + a][b];
         // One wave writes and reads the region, in program order; the fence
         // keeps the compiler to it.
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const int r8 = lane >> 3, c8 = lane & 7;
+        constexpr int kRuns = TJ * 2;                   // runs of eight columns per row
+        const int c8 = lane % kRuns;
         const int j = j0 + wj + c8 * 8;
 #pragma unroll 1
-        for (int r = r8; r < 64; r += 8) {
+        for (int r = lane / kRuns; r < 64; r += 64 / kRuns) {
             const int i = i0 + wi + half * 64 + r;
             float v[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(
-                    mine + r * 256 + ((2 * c8 + h) ^ (r & 15)) * 16);
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(mine + spot(r, 2 * c8 + h));
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     v[4 * h + c] = x[c];
             }
             if (i < g.I && j < g.J)
-                finish_run<T>(g.epi, i, j, g.J, v);
+                finish_run<T, 8>(g.epi, i, j, g.J, v);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
-// Joins the splits of a product: each run of eight outputs adds its partial
-// sums in split order and goes through the epilogue.
+// Joins the splits of a product: each run of four outputs adds its partial
+// sums in split order (kJoinBatch loads in flight) and goes through the
+// epilogue.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;
 template <typename T>
 __global__ __launch_bounds__(kJoinThreads)
 void linear_join_kernel(const Product g) {
-    const int runs = (g.J + 7) / 8;
+    const int runs = (g.J + 3) / 4;
     const int64_t total = static_cast<int64_t>(g.I) * runs;
     const int64_t plane = static_cast<int64_t>(g.I) * g.J;
     for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; x < total;
          x += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
-        const int i = static_cast<int>(x / runs), j = static_cast<int>(x % runs) * 8;
+        const int i = static_cast<int>(x / runs), j = static_cast<int>(x % runs) * 4;
         const float *p = g.partial + static_cast<int64_t>(i) * g.J + j;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int s = 0; s < g.splits; ++s) {
-            const Packed<float, 8> w = load_run<float, 8>(p + s * plane, g.J - j);
+        float v[4] = {0, 0, 0, 0};
+        for (int s0 = 0; s0 < g.splits; s0 += kJoinBatch) {
+            Packed<float, 4> w[kJoinBatch];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                v[c] += w.v[c];
+            for (int u = 0; u < kJoinBatch; ++u)
+                w[u] = load_run<float, 4>(p + min(s0 + u, g.splits - 1) * plane, g.J - j);
+#pragma unroll
+            for (int u = 0; u < kJoinBatch; ++u)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[c] += s0 + u < g.splits ? w[u].v[c] : 0.0f;
         }
-        finish_run<T>(g.epi, i, j, g.J, v);
+        finish_run<T, 4>(g.epi, i, j, g.J, v);
     }
+}
+
+// Few rows: the weights are read once, straight into fragments, and that is
+// the whole cost.  One workgroup takes 16 features and all (at most 16) rows;
+// its WAVES waves split D between them in runs of kRowsStep values (each wave
+// every WAVES-th run, so that together they read along the rows of W) and add
+// their sums in LDS in wave order.  kRowsUnroll matrix instructions' operands
+// are in flight per wave.  Loads are 16 bytes per lane at the rows' own
+// alignment; the last values of a row that is no multiple of 8 are loaded one
+// by one.  Against the tile kernels: 1 x 4096 x 4096 8.5 us per call (the
+// host's time) instead of 11.5, 16 rows 9.3 instead of 11.6, but 32 rows (two
+// row blocks) 12.9 instead of 12.7, so it stops at 16.
+constexpr int kRowsUnroll = 4;
+constexpr int kRowsStep = 32 * kRowsUnroll;
+template <typename T, int WAVES>
+__global__ __launch_bounds__(WAVES * 64)
+void linear_rows_kernel(const Product g) {
+    typedef typename T::bits B;
+    typedef typename T::mfma Frag;
+    __shared__ f32x4 sums[WAVES][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l = lane & 15, q = lane >> 4;
+    const int j0 = blockIdx.x * 16;
+    const B *w = static_cast<const B *>(g.Q) + min(j0 + l, g.J - 1) * g.ldq + q * 8;
+    const B *x = static_cast<const B *>(g.P) + min(l, g.I - 1) * g.ldp + q * 8;
+    f32x4 acc = {0, 0, 0, 0};
+    int k = wave * kRowsStep;
+    for (; k + kRowsStep <= g.K; k += WAVES * kRowsStep) {
+        Packed<B, 8> wf[kRowsUnroll], xf[kRowsUnroll];
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u)
+            wf[u] = load_packed<B, 8>(w + k + u * 32);
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u)
+            xf[u] = load_packed<B, 8>(x + k + u * 32);
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u)
+            acc = mfma(__builtin_bit_cast(Frag, wf[u]), __builtin_bit_cast(Frag, xf[u]), acc);
+    }
+    // The one run that D cuts short, if it is this wave's.
+    for (int e = min(g.K, k + kRowsStep); k < e; k += 32) {
+        const int n = e - k - q * 8;
+        acc = mfma(__builtin_bit_cast(Frag, load_run<B, 8>(w + k, n)),
+                   __builtin_bit_cast(Frag, load_run<B, 8>(x + k, n)), acc);
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    // Four features of one row per lane: element c of lane (l, q) is feature
+    // 4 q + c of row l.
+    const int j = j0 + q * 4;
+    if (tid >= 64 || l >= g.I || j >= g.J)
+        return;
+    f32x4 s = sums[0][lane];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v)
+        s += sums[v][lane];
+    float v[4] = {s[0], s[1], s[2], s[3]};
+    finish_run<T, 4>(g.epi, l, j, g.J, v);
 }
 
 // ---- dZ and the bias gradient ----------------------------------------------
@@ -776,41 +906,92 @@ size_t partial_bytes(const Product &g) {
     return g.splits > 1 ? static_cast<size_t>(g.splits) * g.I * g.J * sizeof(float) : 0;
 }
 
-constexpr int kTile = 128;    // outputs per side of a workgroup's tile
+// How one product is tiled and split.  Rates of the shapes on an MI355X, bf16,
+// as the whole call (the library's product beside it):
+//   8192 x 4096 x 4096   kWide 1310-1440 TFLOP/s by operand order, kPaired
+//                        1110-1200, kDeep 1020-1100 (library 1440, 1260, 1140)
+//   2048 x 2048 x 2048   kDeep 21.5 us, kPaired 24.6-27.4, kWide 45 (21.4-25.3)
+//   65536 x 512 x 128    kPaired 18.1 us, kWide 22.6, kDeep 22.0 (18.6)
+// kWide halves the LDS reads per flop; kDeep keeps three tiles on their way
+// where one workgroup per CU is all there is; kPaired overlaps one workgroup's
+// epilogue with the other's products where k is short.
+enum Shape {
+    kWide,      // 256 x 256 tiles, two stages, one workgroup of eight waves per CU
+    kDeep,      // 128 x 128, four stages, one workgroup of eight waves per CU
+    kPaired,    // 128 x 128, two stages, two workgroups of four waves per CU
+    kRows,      // at most kMaxFewRows rows: weights straight into fragments (forward only)
+    kUnaligned  // 128 x 128, two stages through registers, two of eight waves per CU
+};
 
-int64_t tile_count(const Product &g) {
-    return ((static_cast<int64_t>(g.I) + kTile - 1) / kTile) *
-           ((static_cast<int64_t>(g.J) + kTile - 1) / kTile);
+constexpr int kMaxFewRows = 16;
+
+int64_t tiles_of(const Product &g, int side) {
+    return ((static_cast<int64_t>(g.I) + side - 1) / side) *
+           ((static_cast<int64_t>(g.J) + side - 1) / side);
 }
 
-// Splits k so that the tiles fill the CUs twice over (two workgroups share a
-// CU), each split at least four staged tiles long.
+// Chooses the shape and the splits of k with the least estimated time.
 void plan_product(Product &g, int compute_units) {
-    const int64_t tiles = tile_count(g);
     const int64_t k_tiles = (g.K + kTileK - 1) / kTileK;
-    int64_t s = std::max<int64_t>(1, 2 * compute_units / tiles);
-    s = std::min<int64_t>({s, std::max<int64_t>(1, k_tiles / 4), kMaxKSplits});
-    const int64_t per = (k_tiles + s - 1) / s;
-    g.k_chunk = static_cast<int>(per * kTileK);
-    g.splits = static_cast<int>((k_tiles + per - 1) / per);
+    struct Cost {
+        Shape shape;
+        int side, per_cu;
+        double round;     // us per staged tile of a full round of workgroups
+        double single;    // the same with one workgroup per CU
+        double fixed;     // us per round: first copies, epilogue
+    };
+    static constexpr Cost kAligned[] = {{kWide, 256, 1, 1.50, 1.50, 4.0},
+                                        {kDeep, 128, 1, 0.50, 0.50, 2.0},
+                                        {kPaired, 128, 2, 0.92, 0.65, 1.5}};
+    static constexpr Cost kOther[] = {{kUnaligned, 128, 2, 1.2, 0.8, 2.0}};
+    const Cost *costs = g.dma ? kAligned : kOther;
+    const int kinds = g.dma ? 3 : 1;
+    double best = 1e30;
+    for (int c = 0; c < kinds; ++c) {
+        const Cost &k = costs[c];
+        const int64_t tiles = tiles_of(g, k.side);
+        for (int64_t s = 1; s <= std::min<int64_t>(kMaxKSplits, k_tiles); s *= 2) {
+            const int64_t per = (k_tiles + s - 1) / s;
+            const int64_t wgs = tiles * ((k_tiles + per - 1) / per);
+            const int64_t slots = static_cast<int64_t>(compute_units) * k.per_cu;
+            const double step = wgs <= compute_units ? k.single : k.round;
+            double t = static_cast<double>((wgs + slots - 1) / slots) * (per * step + k.fixed);
+            if (s > 1)    // the join's launch, and the partial sums written and read
+                t += 4.5 + static_cast<double>(s) * g.I * g.J * 8e-6 / 4.0;
+            if (t < best) {
+                best = t;
+                g.shape = k.shape;
+                g.k_chunk = static_cast<int>(per * kTileK);
+                g.splits = static_cast<int>((k_tiles + per - 1) / per);
+            }
+        }
+    }
 }
 
 template <typename T, bool POWN, bool QOWN>
 hipError_t launch_product_modes(const Product &g, hipStream_t stream) {
-    const int64_t tiles = tile_count(g);
-    const dim3 grid(static_cast<unsigned>(tiles), g.splits);
-    const bool dma = rows_aligned(g.P, g.ldp) && rows_aligned(g.Q, g.ldq) &&
-                     (g.p_padded || (POWN ? g.I : g.K) % 8 == 0) &&
-                     (QOWN ? g.J : g.K) % 8 == 0;
-    if (dma)
-        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, true>), grid, dim3(256),
-                           0, stream, g);
-    else
-        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, false>), grid, dim3(256),
-                           0, stream, g);
+    const dim3 grid(static_cast<unsigned>(tiles_of(g, g.shape == kWide ? 256 : 128)), g.splits);
+    switch (g.shape) {
+    case kWide:
+        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 8, 4, 2, true>), grid,
+                           dim3(512), 0, stream, g);
+        break;
+    case kDeep:
+        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 4, 2, 4, true>), grid,
+                           dim3(512), 0, stream, g);
+        break;
+    case kPaired:
+        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, 2, true>), grid,
+                           dim3(256), 0, stream, g);
+        break;
+    default:
+        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 4, 2, 2, false>), grid,
+                           dim3(512), 0, stream, g);
+        break;
+    }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && g.splits > 1) {
-        const int64_t runs = static_cast<int64_t>(g.I) * ((g.J + 7) / 8);
+        const int64_t runs = static_cast<int64_t>(g.I) * ((g.J + 3) / 4);
         const unsigned wgs = static_cast<unsigned>(
             std::min<int64_t>((runs + kJoinThreads - 1) / kJoinThreads, 4096));
         hipLaunchKernelGGL((linear_join_kernel<T>), dim3(wgs), dim3(kJoinThreads), 0, stream, g);
@@ -877,8 +1058,21 @@ kmeans_status_t check_vector(const char *name, const void *p) {
 }
 
 template <typename T>
-hipError_t run_forward(const Product &g, hipStream_t stream) {
-    return launch_product<T>(g, kForward, stream);
+hipError_t run_forward(const Product &g, int compute_units, hipStream_t stream) {
+    if (g.shape != kRows)
+        return launch_product<T>(g, kForward, stream);
+    // As many waves as D gives work to, while the CUs hold them (32 each).
+    const dim3 grid((g.J + 15) / 16);
+    int64_t waves = 4;
+    while (waves < 16 && waves * kRowsStep < g.K && grid.x * waves * 2 <= 16 * compute_units)
+        waves *= 2;
+    if (waves == 16)
+        hipLaunchKernelGGL((linear_rows_kernel<T, 16>), grid, dim3(1024), 0, stream, g);
+    else if (waves == 8)
+        hipLaunchKernelGGL((linear_rows_kernel<T, 8>), grid, dim3(512), 0, stream, g);
+    else
+        hipLaunchKernelGGL((linear_rows_kernel<T, 4>), grid, dim3(256), 0, stream, g);
+    return hipGetLastError();
 }
 
 // The launches of kmeans_linear_grad on workspace `ws`.
@@ -958,10 +1152,17 @@ extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const 
     g.J = static_cast<int>(F);
     g.K = static_cast<int>(D);
     g.epi = {bias, residual, residual_stride, Y, y_stride, pre, pre_stride, activation};
-    if (tile_count(g) > kMaxRows)
+    g.dma = rows_aligned(X, x_stride) && rows_aligned(W, w_stride) && D % 8 == 0;
+    if (tiles_of(g, 128) > kMaxRows)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x F=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(F));
-    plan_product(g, device_compute_units());
+    const int cus = device_compute_units();
+    if (N <= kMaxFewRows) {
+        g.shape = kRows;
+        g.splits = 1;
+    } else {
+        plan_product(g, cus);
+    }
     std::unique_ptr<WorkspaceLease> lease;
     const size_t bytes = partial_bytes(g);
     if (bytes > 0) {
@@ -971,8 +1172,8 @@ extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const 
                         hipGetErrorString(lease->error()));
         g.partial = static_cast<float *>(lease->ptr());
     }
-    const hipError_t e = dtype == KMEANS_BF16 ? run_forward<Bf16>(g, stream)
-                                              : run_forward<Fp16>(g, stream);
+    const hipError_t e = dtype == KMEANS_BF16 ? run_forward<Bf16>(g, cus, stream)
+                                              : run_forward<Fp16>(g, cus, stream);
     if (e != hipSuccess)
         return fail(KMEANS_ERR_HIP, "linear launch failed: %s", hipGetErrorString(e));
     return ok();
@@ -1051,7 +1252,11 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
     p.dw.K = static_cast<int>(N);
     p.dw.Q = X;
     p.dw.epi = {nullptr, nullptr, 0, dW, dw_stride, nullptr, 0, KMEANS_ACT_NONE};
-    if (tile_count(p.dx) > kMaxRows || tile_count(p.dw) > kMaxRows)
+    // dZ's rows may be read up to a whole chunk where they are the workspace's
+    // (zeros past F); W and X are read with D contiguous.
+    p.dx.dma = rows_aligned(W, w_stride) && D % 8 == 0;
+    p.dw.dma = rows_aligned(X, x_stride) && D % 8 == 0;
+    if (tiles_of(p.dx, 128) > kMaxRows || tiles_of(p.dw, 128) > kMaxRows)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x D=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(D));
     size_t part = 0;
@@ -1079,7 +1284,6 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
     }
     p.dx.P = p.dw.P = z;
     p.dx.ldp = p.dw.ldp = ldz;
-    p.dx.p_padded = p.dw.p_padded = p.dz;
     p.dx.partial = p.dw.partial = reinterpret_cast<float *>(ws + p.part_at);
     const hipError_t e =
         dtype == KMEANS_BF16
