@@ -96,7 +96,7 @@ __device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c,
         Packed<B, V> v[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            v[u] = *reinterpret_cast<const Packed<B, V> *>(p + (u * kClipThreads + threadIdx.x) * V);
+            v[u] = load_packed<B, V>(p + (u * kClipThreads + threadIdx.x) * V);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
             add(v[u]);
@@ -104,7 +104,7 @@ __device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c,
     }
     for (int at = threadIdx.x * V; at < left; at += kClipThreads * V) {
         if (at + V <= left) {
-            add(*reinterpret_cast<const Packed<B, V> *>(p + at));
+            add(load_packed<B, V>(p + at));
         } else {
             for (int e = at; e < left; ++e) {
                 const double x = static_cast<double>(T::widen(p[e]));
@@ -125,16 +125,17 @@ __device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t 
     const B *p = static_cast<const B *>(src) + beg;
     B *o = static_cast<B *>(dst) + beg;
     auto put = [&](int at, Packed<B, V> v) __attribute__((always_inline)) {
+        float x[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            v.v[e] = T::narrow(T::widen(v.v[e]) * factor);
-        *reinterpret_cast<Packed<B, V> *>(o + at) = v;
+            x[e] = T::widen(v.v[e]) * factor;
+        store_packed<B, V>(o + at, narrow_run<T, V>(x));
     };
     if (left == E) {
         Packed<B, V> v[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            v[u] = *reinterpret_cast<const Packed<B, V> *>(p + (u * kClipThreads + threadIdx.x) * V);
+            v[u] = load_packed<B, V>(p + (u * kClipThreads + threadIdx.x) * V);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
             put((u * kClipThreads + threadIdx.x) * V, v[u]);
@@ -142,7 +143,7 @@ __device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t 
     }
     for (int at = threadIdx.x * V; at < left; at += kClipThreads * V) {
         if (at + V <= left)
-            put(at, *reinterpret_cast<const Packed<B, V> *>(p + at));
+            put(at, load_packed<B, V>(p + at));
         else
             for (int e = at; e < left; ++e)
                 o[e] = T::narrow(T::widen(p[e]) * factor);

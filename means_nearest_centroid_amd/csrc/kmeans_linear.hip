@@ -137,40 +137,22 @@ struct Product {
     Epilogue epi;
 };
 
-template <typename B, int n>
-__device__ __forceinline__ Packed<B, n> load_packed(const B *p) {
-    return *reinterpret_cast<const Packed<B, n> *>(p);
-}
-
-// Up to V elements at any alignment: one access where all V exist.
-template <typename B, int V>
-__device__ __forceinline__ Packed<B, V> load_run(const B *p, int n) {
-    if (n >= V)
-        return load_packed<B, V>(p);
-    Packed<B, V> q = {};
-#pragma unroll
-    for (int c = 0; c < V - 1; ++c)
-        if (c < n)
-            q.v[c] = p[c];
-    return q;
-}
-template <typename B, int V>
-__device__ __forceinline__ void store_run(B *p, int n, const Packed<B, V> &q) {
-    if (n >= V) {
-        *reinterpret_cast<Packed<B, V> *>(p) = q;
-        return;
-    }
-#pragma unroll
-    for (int c = 0; c < V - 1; ++c)
-        if (c < n)
-            p[c] = q.v[c];
-}
-
 template <int ACT, int V>
 __device__ __forceinline__ void activate_run(float (&v)[V]) {
 #pragma unroll
     for (int c = 0; c < V; ++c)
         v[c] = activate(ACT, v[c]);
+}
+
+template <int V>
+__device__ __forceinline__ void activate_run(int act, float (&v)[V]) {
+    switch (act) {
+    case KMEANS_ACT_RELU: activate_run<KMEANS_ACT_RELU>(v); break;
+    case KMEANS_ACT_GELU: activate_run<KMEANS_ACT_GELU>(v); break;
+    case KMEANS_ACT_GELU_TANH: activate_run<KMEANS_ACT_GELU_TANH>(v); break;
+    case KMEANS_ACT_SILU: activate_run<KMEANS_ACT_SILU>(v); break;
+    default: break;
+    }
 }
 
 // V consecutive outputs of row i from column j on (those below J): bias,
@@ -179,37 +161,22 @@ template <typename T, int V>
 __device__ __forceinline__ void finish_run(const Epilogue &e, int i, int j, int J, float (&v)[V]) {
     typedef typename T::bits B;
     const int n = J - j;
-    Packed<B, V> q;
     if (e.bias != nullptr) {
-        q = load_run<B, V>(static_cast<const B *>(e.bias) + j, n);
+        const Packed<B, V> q = load_run<B, V>(static_cast<const B *>(e.bias) + j, n);
 #pragma unroll
         for (int c = 0; c < V; ++c)
             v[c] += T::widen(q.v[c]);
     }
-    if (e.pre != nullptr) {
-#pragma unroll
-        for (int c = 0; c < V; ++c)
-            q.v[c] = T::narrow(v[c]);
-        store_run<B, V>(static_cast<B *>(e.pre) + static_cast<int64_t>(i) * e.ldp + j, n, q);
-    }
-    switch (e.act) {
-    case KMEANS_ACT_RELU: activate_run<KMEANS_ACT_RELU>(v); break;
-    case KMEANS_ACT_GELU: activate_run<KMEANS_ACT_GELU>(v); break;
-    case KMEANS_ACT_GELU_TANH: activate_run<KMEANS_ACT_GELU_TANH>(v); break;
-    case KMEANS_ACT_SILU: activate_run<KMEANS_ACT_SILU>(v); break;
-    default: break;
-    }
+    if (e.pre != nullptr)
+        store_run<B, V>(static_cast<B *>(e.pre) + i * e.ldp + j, n, narrow_run<T, V>(v));
+    activate_run(e.act, v);
     if (e.residual != nullptr) {
-        q = load_run<B, V>(static_cast<const B *>(e.residual) + static_cast<int64_t>(i) * e.ldr + j,
-                           n);
+        const Packed<B, V> q = load_run<B, V>(static_cast<const B *>(e.residual) + i * e.ldr + j, n);
 #pragma unroll
         for (int c = 0; c < V; ++c)
             v[c] += T::widen(q.v[c]);
     }
-#pragma unroll
-    for (int c = 0; c < V; ++c)
-        q.v[c] = T::narrow(v[c]);
-    store_run<B, V>(static_cast<B *>(e.out) + static_cast<int64_t>(i) * e.ldo + j, n, q);
+    store_run<B, V>(static_cast<B *>(e.out) + i * e.ldo + j, n, narrow_run<T, V>(v));
 }
 
 __device__ __forceinline__ f32x4 mfma(Bf16::mfma a, Bf16::mfma b, f32x4 c) {
@@ -605,12 +572,13 @@ void linear_tile_kernel(const Product g) {
         start(Index<2>{});
         start(Index<3>{});
     }
-    if constexpr (DMA)
+    if constexpr (DMA) {
         // All stages were started: only the first need have landed.
         if (tiles >= S)
             wait_vmem<(S - 1) * kCopies>();
         else
             wait_vmem<0>();
+    }
     lds_barrier();
     read_phase(p0, q0, 0);
     int t = 0;
@@ -670,8 +638,48 @@ void linear_tile_kernel(const Product g) {
                   : wave / kPerArray == 2 ? q0 : q1;
     mine += (wave % kPerArray) * kPass;
     __syncthreads();
+    constexpr int kRuns = TJ * 2;                       // runs of eight columns per row
+    constexpr int kSteps = kRuns;                       // a wave's steps over 64 rows
+    typedef typename T::bits B;
+    const Epilogue &e = g.epi;
+    const int c8 = lane % kRuns;
+    const int j = j0 + wj + c8 * 8;
+    const int n = g.J - j;                              // columns that exist
+    const int i_first = i0 + wi + lane / kRuns;
+    // Tiles whose columns all exist (nearly all) take whole-run accesses without
+    // a branch each; a tile at the right edge goes run by run.
+    const bool whole = j0 + RJ <= g.J;
+    float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (!QOWN && e.bias != nullptr && whole) {
+        const Packed<B, 8> q = load_packed<B, 8>(static_cast<const B *>(e.bias) + j);
 #pragma unroll
-    for (int half = 0; half < TI / 4; ++half) {
+        for (int c = 0; c < 8; ++c)
+            bias[c] = T::widen(q.v[c]);
+    }
+    auto take = [&](int r, float (&v)[8]) KM_INLINE {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(mine + spot(r, 2 * c8 + h));
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                v[4 * h + c] = x[c];
+        }
+    };
+    auto pass = [&](auto which) KM_INLINE {
+        constexpr int half = decltype(which)::value;
+        const int i_pass = i_first + half * 64;
+        // All residual loads of the pass are in flight while the accumulators
+        // go through LDS.
+        Packed<B, 8> res[kSteps];
+        if (!QOWN && e.residual != nullptr && whole) {
+            const B *p = static_cast<const B *>(e.residual) + i_pass * e.ldr + j;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                res[s] = Packed<B, 8>{};
+                if (i_pass + s * (64 / kRuns) < g.I)
+                    res[s] = load_packed<B, 8>(p + s * (64 / kRuns) * e.ldr);
+            }
+        }
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -681,25 +689,56 @@ void linear_tile_kernel(const Product g) {
         // One wave writes and reads the region, in program order; the fence
         // keeps the compiler to it.
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        constexpr int kRuns = TJ * 2;                   // runs of eight columns per row
-        const int c8 = lane % kRuns;
-        const int j = j0 + wj + c8 * 8;
-#pragma unroll 1
-        for (int r = lane / kRuns; r < 64; r += 64 / kRuns) {
-            const int i = i0 + wi + half * 64 + r;
-            float v[8];
+        auto finish = [&](auto act) KM_INLINE {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(mine + spot(r, 2 * c8 + h));
+            for (int s = 0; s < kSteps; ++s) {
+                const int i = i_pass + s * (64 / kRuns);
+                float v[8];
+                take(lane / kRuns + s * (64 / kRuns), v);
+                if (i >= g.I)
+                    continue;
+                if constexpr (!QOWN) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    v[4 * h + c] = x[c];
+                    for (int c = 0; c < 8; ++c)
+                        v[c] += bias[c];
+                    if (e.pre != nullptr)
+                        store_packed(static_cast<B *>(e.pre) + i * e.ldp + j, narrow_run<T, 8>(v));
+                    activate_run<decltype(act)::value>(v);
+                    if (e.residual != nullptr) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            v[c] += T::widen(res[s].v[c]);
+                    }
+                }
+                store_packed(static_cast<B *>(e.out) + i * e.ldo + j, narrow_run<T, 8>(v));
             }
-            if (i < g.I && j < g.J)
-                finish_run<T, 8>(g.epi, i, j, g.J, v);
+        };
+        if (!whole) {
+#pragma unroll 1
+            for (int s = 0; s < kSteps; ++s) {
+                const int i = i_pass + s * (64 / kRuns);
+                float v[8];
+                take(lane / kRuns + s * (64 / kRuns), v);
+                if (i < g.I && n > 0)
+                    finish_run<T, 8>(e, i, j, g.J, v);
+            }
+        } else if constexpr (QOWN) {
+            finish(Index<KMEANS_ACT_NONE>{});
+        } else {
+            switch (e.act) {
+            case KMEANS_ACT_RELU: finish(Index<KMEANS_ACT_RELU>{}); break;
+            case KMEANS_ACT_GELU: finish(Index<KMEANS_ACT_GELU>{}); break;
+            case KMEANS_ACT_GELU_TANH: finish(Index<KMEANS_ACT_GELU_TANH>{}); break;
+            case KMEANS_ACT_SILU: finish(Index<KMEANS_ACT_SILU>{}); break;
+            default: finish(Index<KMEANS_ACT_NONE>{}); break;
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
+    };
+    pass(Index<0>{});
+    if constexpr (TI > 4)
+        pass(Index<1>{});
+    static_assert(TI <= 8, "two passes");
 }
 
 // Joins the splits of a product: each run of four outputs adds its partial
@@ -819,30 +858,19 @@ void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp,
         for (int r = r_first + (tid >> lanes_log2); r < r_end; r += groups) {
             const B *y = static_cast<const B *>(dY) + r * ldy + c0;
             const B *z = static_cast<const B *>(pre) + r * ldp + c0;
-            Packed<B, 8> d = {}, zz = {};
-            if (n >= 8) {
-                d = load_packed<B, 8>(y);
-                if (act != KMEANS_ACT_NONE)
-                    zz = load_packed<B, 8>(z);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 7; ++e)
-                    if (e < n) {
-                        d.v[e] = y[e];
-                        if (act != KMEANS_ACT_NONE)
-                            zz.v[e] = z[e];
-                    }
-            }
-            Packed<B, 8> o;
+            const Packed<B, 8> d = load_run<B, 8>(y, n);
+            Packed<B, 8> zz = {};
+            if (act != KMEANS_ACT_NONE)
+                zz = load_run<B, 8>(z, n);
+            float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = activate_grad(act, T::widen(zz.v[e]), T::widen(d.v[e]));
-                s[e] += v;
-                o.v[e] = T::narrow(v);
+                v[e] = activate_grad(act, T::widen(zz.v[e]), T::widen(d.v[e]));
+                s[e] += v[e];
             }
             if (dZ != nullptr) {
                 B *w = static_cast<B *>(dZ) + r * ldz + c0;   // the row's padding may be written
-                *reinterpret_cast<u32x4 *>(w) = __builtin_bit_cast(u32x4, o);
+                *reinterpret_cast<u32x4 *>(w) = __builtin_bit_cast(u32x4, narrow_run<T, 8>(v));
             }
         }
     }

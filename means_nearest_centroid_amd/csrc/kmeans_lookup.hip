@@ -36,15 +36,6 @@ __device__ __forceinline__ int table_row(L label, int K) {
     return label < 0 || label >= K ? -1 : static_cast<int>(label);
 }
 
-template <typename B, int n>
-__device__ __forceinline__ Packed<B, n> load_packed(const B *p) {
-    return *reinterpret_cast<const Packed<B, n> *>(p);
-}
-template <typename B, int n>
-__device__ __forceinline__ void store_packed(B *p, const Packed<B, n> &v) {
-    *reinterpret_cast<Packed<B, n> *>(p) = v;
-}
-
 // ---- lookup ----------------------------------------------------------------
 
 // Pieces of V elements (16 bytes), `pieces` per row; the last piece of a row
@@ -82,11 +73,12 @@ void lookup_kernel(const typename T::bits *__restrict__ C, int64_t ldc, const L 
             v[u] = from[u] >= 0 ? load_packed<B, V>(C + from[u] * ldc + col[u]) : Packed<B, V>{};
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
+            float x[V];
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                v[u].v[e] = from[u] >= 0 ? T::narrow(scale * T::widen(v[u].v[e])) : B(0);
+                x[e] = from[u] >= 0 ? scale * T::widen(v[u].v[e]) : 0.0f;
             if (row[u] < N)
-                store_packed(Y + row[u] * ldy + col[u], v[u]);
+                store_packed<B, V>(Y + row[u] * ldy + col[u], narrow_run<T, V>(x));
         }
     } else {
 #pragma unroll
@@ -127,50 +119,23 @@ __device__ __forceinline__ void finish_row(const GradArgs &g, int k, int c0, int
                                            const float (&sum)[V]) {
     typedef typename O::bits B;
     B *o = static_cast<B *>(g.dC) + k * g.ldc + c0;
-    if (n >= V) {
-        Packed<B, V> v = {};
-        if (g.accumulate)
-            v = load_packed<B, V>(o);
+    float v[V];
+    if (g.accumulate) {
+        const Packed<B, V> old = load_run<B, V>(o, n);
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            v.v[e] = O::narrow(g.accumulate ? fmaf(g.scale, sum[e], O::widen(v.v[e]))
-                                            : g.scale * sum[e]);
-        store_packed(o, v);
+            v[e] = fmaf(g.scale, sum[e], O::widen(old.v[e]));
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            if (e < n)
-                o[e] = O::narrow(g.accumulate ? fmaf(g.scale, sum[e], O::widen(o[e]))
-                                              : g.scale * sum[e]);
+            v[e] = g.scale * sum[e];
     }
+    store_run<B, V>(o, n, narrow_run<O, V>(v));
 }
 
 template <int V>
 __device__ __forceinline__ void store_partial(float *p, int n, const float (&sum)[V]) {
-    if (n >= V) {
-        Packed<float, V> v;
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            v.v[e] = sum[e];
-        store_packed(p, v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (e < n)
-                p[e] = sum[e];
-    }
-}
-
-template <typename B, int V>
-__device__ __forceinline__ Packed<B, V> load_columns(const B *p, int n) {
-    if (n >= V)
-        return load_packed<B, V>(p);
-    Packed<B, V> v = {};
-#pragma unroll
-    for (int e = 0; e < V - 1; ++e)
-        if (e < n)
-            v.v[e] = p[e];
-    return v;
+    store_run<float, V>(p, n, narrow_run<Fp32, V>(sum));
 }
 
 // First position whose key is at least `key` (lower) or greater (upper).
@@ -233,7 +198,7 @@ void lookup_sum_kernel(const GradArgs g, int sum_wgs) {
         for (int u = 0; u < kBatch; ++u) {
             const int p = min(p0 + u, end - 1);
             key[u] = p0 + u < end ? g.keys[p] : -1;
-            row[u] = load_columns<B, V>(src + g.vals[p] * g.ldy, n);
+            row[u] = load_run<B, V>(src + g.vals[p] * g.ldy, n);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -309,14 +274,14 @@ void lookup_join_kernel(const GradArgs g) {
         if (m == 0 || m >= kLongRun || n <= 0)
             continue;
         const float *p = g.partial + static_cast<int64_t>(first + x) * 2 * g.D + c0;
-        const Packed<float, V> head = load_columns<float, V>(p + g.D, n);
+        const Packed<float, V> head = load_run<float, V>(p + g.D, n);
         float sum[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
             sum[e] = head.v[e];
         for (int s = 1; s <= m; ++s) {
             const Packed<float, V> w =
-                load_columns<float, V>(p + static_cast<int64_t>(s) * 2 * g.D, n);
+                load_run<float, V>(p + static_cast<int64_t>(s) * 2 * g.D, n);
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 sum[e] += w.v[e];
@@ -331,7 +296,7 @@ void lookup_join_kernel(const GradArgs g) {
         float sum[V] = {};
         if (n > 0)
             for (int s = q; s <= m; s += groups) {
-                const Packed<float, V> w = load_columns<float, V>(
+                const Packed<float, V> w = load_run<float, V>(
                     s == 0 ? p + g.D : p + static_cast<int64_t>(s) * 2 * g.D, n);
 #pragma unroll
                 for (int e = 0; e < V; ++e)
