@@ -6,17 +6,37 @@
 // Both move rows and compute next to nothing: the bound is the bytes of the
 // rows, read once and written once.
 //
-// Gradient.  The positions are sorted by label (the stable radix sort of the
-// centroid update), so that a label's rows are one run of sorted positions.
+// Gradient.  Two paths, by a rule on N and K alone.  In neither are there
+// floating-point atomics: the order of every sum follows from the labels.
+//
+// Buckets (K from 256 to 65536 and at most 1024 positions per bucket on
+// average): each tile of positions is sorted by bucket of up to 64 rows, as in
+// the centroid update.
+//  1. lookup_bucket_kernel: one workgroup per bucket gathers its positions,
+//     sorts them by row in LDS (stably) and sums them; groups of lanes that
+//     together hold one row's columns each take an equal share of the sorted
+//     positions, and the sums of runs cut between groups meet in LDS.  The
+//     workgroup owns its rows, so it zeroes those without a position too.
+//  2. A bucket of more positions than one workgroup should sum (a frequent
+//     label) is put on a list instead, in parts of `cap` positions.
+//     lookup_part_kernel does the same for each part, leaving partial sums,
+//     and lookup_part_join_kernel adds them in order: work per workgroup is
+//     bounded whatever the frequencies.  Both end at once when the list is
+//     empty (about 2 us each).  Workgroups of the first launch taking parts
+//     themselves once done with their buckets, without further launches, was
+//     700 us instead of 160 at 16384 x 4096 of 32768 tokens: the fences that
+//     hand partial sums from one XCD to another inside a launch empty its L2.
+//
+// Sort (every other shape): the positions are sorted by label (the stable
+// radix sort of the centroid update), so that a label's rows are one run of
+// sorted positions.
 //  1. lookup_sum_kernel walks fixed chunks of sorted positions; a group of
-//     lanes that together hold one row's columns owns one chunk and sums each
-//     run in position order.  A run inside the chunk is finished there (one
-//     rounding); a run cut by a chunk edge leaves its partial sum.  Work per
-//     group is bounded whatever the label frequencies are.  Further
-//     workgroups of the same launch zero the rows that no label names.
+//     lanes owns one chunk and sums each run in position order.  A run inside
+//     the chunk is finished there (one rounding); a run cut by a chunk edge
+//     leaves its partial sum.  Further workgroups of the same launch zero the
+//     rows that no label names.
 //  2. lookup_join_kernel adds the partial sums of the runs that were cut, in
 //     an order fixed by the chunks.
-// No atomics: the order of every sum follows from the labels alone.
 #include <stdint.h>
 
 #include <algorithm>
@@ -112,16 +132,46 @@ struct GradArgs {
     int slabs;                    // column slabs of (lanes V) columns
 };
 
-// Columns c0 .. c0 + n - 1 of row k from the sums: scaled, added to the row
-// where asked, rounded once.
+// The V columns that a lane holds in column slab `slab`.  The last lane of a
+// row of D >= V columns that are no multiple of V starts at D - V, so that
+// every load is a whole one; it shares its first `skip` columns with the lane
+// before it and leaves them to that lane.  (D < V: V = 1.)
+template <int V>
+struct Columns {
+    int first, skip;
+    bool any;
+    __device__ __forceinline__ Columns(int slab, int lanes, int l, int D) {
+        const int c = (slab * lanes + l) * V;
+        any = c < D;
+        first = min(c, max(D - V, 0));
+        skip = c - first;
+    }
+};
+
+// A lane's columns of a row of dC (o), without the first `skip`.
 template <typename O, int V>
-__device__ __forceinline__ void finish_row(const GradArgs &g, int k, int c0, int n,
+__device__ __forceinline__ void store_columns(typename O::bits *o, int skip,
+                                              const Packed<typename O::bits, V> &v) {
+    if (skip == 0) {
+        store_packed(o, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 1; e < V; ++e)
+        if (e >= skip)
+            o[e] = v.v[e];
+}
+
+// A lane's columns of row k from the sums: scaled, added to the row where
+// asked, rounded once.
+template <typename O, int V>
+__device__ __forceinline__ void finish_row(const GradArgs &g, int k, const Columns<V> &c,
                                            const float (&sum)[V]) {
     typedef typename O::bits B;
-    B *o = static_cast<B *>(g.dC) + k * g.ldc + c0;
+    B *o = static_cast<B *>(g.dC) + k * g.ldc + c.first;
     float v[V];
     if (g.accumulate) {
-        const Packed<B, V> old = load_run<B, V>(o, n);
+        const Packed<B, V> old = load_packed<B, V>(o);
 #pragma unroll
         for (int e = 0; e < V; ++e)
             v[e] = fmaf(g.scale, sum[e], O::widen(old.v[e]));
@@ -130,12 +180,21 @@ __device__ __forceinline__ void finish_row(const GradArgs &g, int k, int c0, int
         for (int e = 0; e < V; ++e)
             v[e] = g.scale * sum[e];
     }
-    store_run<B, V>(o, n, narrow_run<O, V>(v));
+    store_columns<O, V>(o, c.skip, narrow_run<O, V>(v));
 }
 
+// The same columns of a row that no label names.
+template <typename O, int V>
+__device__ __forceinline__ void zero_row(const GradArgs &g, int k, const Columns<V> &c) {
+    if (!g.accumulate)
+        store_columns<O, V>(static_cast<typename O::bits *>(g.dC) + k * g.ldc + c.first, c.skip,
+                            Packed<typename O::bits, V>{});
+}
+
+// Partial sums are written whole: lanes that share columns hold the same sums.
 template <int V>
-__device__ __forceinline__ void store_partial(float *p, int n, const float (&sum)[V]) {
-    store_run<float, V>(p, n, narrow_run<Fp32, V>(sum));
+__device__ __forceinline__ void store_partial(float *p, const float (&sum)[V]) {
+    store_packed(p, narrow_run<Fp32, V>(sum));
 }
 
 // First position whose key is at least `key` (lower) or greater (upper).
@@ -168,26 +227,23 @@ void lookup_sum_kernel(const GradArgs g, int sum_wgs) {
             named[tid] = p < g.N && g.keys[p] == k;
         }
         __syncthreads();
-        const float zero[V] = {};
-        const int c0 = (blockIdx.y * lanes + l) * V;
-        const int n = g.D - c0;
-        if (n <= 0)
+        const Columns<V> cols(blockIdx.y, lanes, l, g.D);
+        if (!cols.any)
             return;
         for (int r = tid >> g.lanes_log2; r < kFillRows; r += kRowThreads >> g.lanes_log2)
             if (r0 + r < g.K && !named[r])
-                finish_row<O, V>(g, r0 + r, c0, n, zero);
+                zero_row<O, V>(g, r0 + r, cols);
         return;
     }
     const int c = blockIdx.x * (kRowThreads >> g.lanes_log2) + (tid >> g.lanes_log2);
-    const int c0 = (blockIdx.y * lanes + l) * V;
-    const int n = g.D - c0;
-    if (c >= g.chunks || n <= 0)
+    const Columns<V> cols(blockIdx.y, lanes, l, g.D);
+    if (c >= g.chunks || !cols.any)
         return;
     const int beg = c * g.chunk;
     const int end = static_cast<int>(min(static_cast<int64_t>(g.N),
                                          static_cast<int64_t>(beg) + g.chunk));
-    const B *src = static_cast<const B *>(g.dY) + c0;
-    float *part = g.partial + static_cast<int64_t>(c) * 2 * g.D + c0;
+    const B *src = static_cast<const B *>(g.dY) + cols.first;
+    float *part = g.partial + static_cast<int64_t>(c) * 2 * g.D + cols.first;
     int cur = g.keys[beg];
     bool open_left = beg > 0 && g.keys[beg - 1] == cur;
     float sum[V] = {};
@@ -198,7 +254,7 @@ void lookup_sum_kernel(const GradArgs g, int sum_wgs) {
         for (int u = 0; u < kBatch; ++u) {
             const int p = min(p0 + u, end - 1);
             key[u] = p0 + u < end ? g.keys[p] : -1;
-            row[u] = load_run<B, V>(src + g.vals[p] * g.ldy, n);
+            row[u] = load_packed<B, V>(src + g.vals[p] * g.ldy);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -207,9 +263,9 @@ void lookup_sum_kernel(const GradArgs g, int sum_wgs) {
             if (key[u] != cur) {
                 if (cur < g.K) {
                     if (open_left)
-                        store_partial<V>(part, n, sum);
+                        store_partial<V>(part, sum);
                     else
-                        finish_row<O, V>(g, cur, c0, n, sum);
+                        finish_row<O, V>(g, cur, cols, sum);
                 }
                 open_left = false;
                 cur = key[u];
@@ -226,11 +282,11 @@ void lookup_sum_kernel(const GradArgs g, int sum_wgs) {
         return;
     const bool open_right = end < g.N && g.keys[end] == cur;
     if (open_left)
-        store_partial<V>(part, n, sum);
+        store_partial<V>(part, sum);
     else if (open_right)
-        store_partial<V>(part + g.D, n, sum);
+        store_partial<V>(part + g.D, sum);
     else
-        finish_row<O, V>(g, cur, c0, n, sum);
+        finish_row<O, V>(g, cur, cols, sum);
 }
 
 // A run that was cut began in some chunk c (slot 1 of c) and went on through
@@ -267,71 +323,494 @@ void lookup_join_kernel(const GradArgs g) {
         more[tid] = m;
     }
     __syncthreads();
-    const int c0 = (blockIdx.y * lanes + l) * V;
-    const int n = g.D - c0;
+    const Columns<V> cols(blockIdx.y, lanes, l, g.D);
     for (int x = q; x < kJoinChunks; x += groups) {
         const int m = more[x];
-        if (m == 0 || m >= kLongRun || n <= 0)
+        if (m == 0 || m >= kLongRun || !cols.any)
             continue;
-        const float *p = g.partial + static_cast<int64_t>(first + x) * 2 * g.D + c0;
-        const Packed<float, V> head = load_run<float, V>(p + g.D, n);
+        const float *p = g.partial + static_cast<int64_t>(first + x) * 2 * g.D + cols.first;
+        const Packed<float, V> head = load_packed<float, V>(p + g.D);
         float sum[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
             sum[e] = head.v[e];
-        for (int s = 1; s <= m; ++s) {
-            const Packed<float, V> w =
-                load_run<float, V>(p + static_cast<int64_t>(s) * 2 * g.D, n);
+        for (int s0 = 1; s0 <= m; s0 += 4) {
+            Packed<float, V> w[4];
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                sum[e] += w.v[e];
+            for (int u = 0; u < 4; ++u)
+                w[u] = load_packed<float, V>(p + static_cast<int64_t>(min(s0 + u, m)) * 2 * g.D);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    sum[e] += s0 + u <= m ? w[u].v[e] : 0.0f;
         }
-        finish_row<O, V>(g, key_of[x], c0, n, sum);
+        finish_row<O, V>(g, key_of[x], cols, sum);
     }
     for (int x = 0; x < kJoinChunks; ++x) {
         const int m = more[x];
         if (m < kLongRun)
             continue;
-        const float *p = g.partial + static_cast<int64_t>(first + x) * 2 * g.D + c0;
+        const float *p = g.partial + static_cast<int64_t>(first + x) * 2 * g.D + cols.first;
         float sum[V] = {};
-        if (n > 0)
-            for (int s = q; s <= m; s += groups) {
-                const Packed<float, V> w = load_run<float, V>(
-                    s == 0 ? p + g.D : p + static_cast<int64_t>(s) * 2 * g.D, n);
+        if (cols.any)
+            for (int s0 = q; s0 <= m; s0 += kBatch * groups) {
+                Packed<float, V> w[kBatch];
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    sum[e] += w.v[e];
+                for (int u = 0; u < kBatch; ++u) {
+                    const int s = min(s0 + u * groups, m);
+                    w[u] = load_packed<float, V>(
+                        s == 0 ? p + g.D : p + static_cast<int64_t>(s) * 2 * g.D);
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        sum[e] += s0 + u * groups <= m ? w[u].v[e] : 0.0f;
             }
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < V; ++e)
             sums[tid][e] = sum[e];
         __syncthreads();
-        if (q == 0 && n > 0) {
+        if (q == 0 && cols.any) {
             for (int r = 1; r < groups; ++r)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     sum[e] += sums[r * lanes + l][e];
-            finish_row<O, V>(g, key_of[x], c0, n, sum);
+            finish_row<O, V>(g, key_of[x], cols, sum);
         }
+    }
+}
+
+// ---- gradient by buckets ---------------------------------------------------
+
+constexpr int kBucketCap = 2048;       // most positions one workgroup sorts and sums
+constexpr int kMaxBucketRows = 64;
+constexpr int kMaxTiles = 512;         // of positions (make_label_bins)
+constexpr int kWaves = kRowThreads / 64;
+
+// One bucket of more than `cap` positions.
+struct Heavy {
+    int bucket, first_part, parts;
+};
+
+struct BucketArgs {
+    const int32_t *sidx, *dir;   // slot words and directory (launch_label_bins)
+    int bucket_log2, buckets, tile_log2, tiles;
+    int cap;                     // positions of a part; from more on a bucket is heavy
+    int col_groups_log2;         // groups of lanes side by side on columns (the others
+                                 // divide the positions)
+    int *counts;                 // heavy buckets, parts
+    Heavy *heavy;
+    int *run_len;                // [parts][S]: positions of each row in the part
+    float *partial;              // [parts][S][D]
+};
+
+struct BucketShared {
+    int words[kBucketCap], sorted[kBucketCap];
+    int off[kMaxTiles + 1], src[kMaxTiles];
+    int cnt[kWaves][kMaxBucketRows], start[kMaxBucketRows + 1];
+    int wave_total[kWaves];
+    int found;                   // by one thread, for all
+    float edge[2][kRowThreads * 8];
+};
+
+// Positions (slots, in tile order) of bucket b: their first slots per tile in
+// sh.off, where each tile's lie in sidx in sh.src; returns their number.
+__device__ __forceinline__ int find_segments(const BucketArgs &bk, int b, BucketShared &sh) {
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const size_t row = bk.buckets + 1;
+    int len[2] = {0, 0}, base[2] = {0, 0};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int t = min(2 * tid + u, bk.tiles - 1);
+        const int32_t *d = bk.dir + t * row + b;
+        const int lo = d[0], hi = d[1];
+        len[u] = 2 * tid + u < bk.tiles ? hi - lo : 0;
+        base[u] = (t << bk.tile_log2) + lo;
+    }
+    const int x = wave_inclusive_sum(len[0] + len[1]);
+    if (lane == 63)
+        sh.wave_total[w] = x;
+    __syncthreads();
+    int ex = x - len[0] - len[1], total = 0;
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) {
+        ex += v < w ? sh.wave_total[v] : 0;
+        total += sh.wave_total[v];
+    }
+    if (2 * tid < bk.tiles) {
+        sh.off[2 * tid] = ex;
+        sh.src[2 * tid] = base[0];
+    }
+    if (2 * tid + 1 < bk.tiles) {
+        sh.off[2 * tid + 1] = ex + len[0];
+        sh.src[2 * tid + 1] = base[1];
+    }
+    __syncthreads();
+    return total;
+}
+
+// Slot words of slots [s0, s0 + n) into sh.words (n <= kBucketCap): each slot
+// finds its tile by binary search, eight slots of a thread at a time.
+__device__ __forceinline__ void gather_words(const BucketArgs &bk, int s0, int n,
+                                             BucketShared &sh) {
+    constexpr int kPer = kBucketCap / kRowThreads;
+    int v[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int p = min(u * kRowThreads + static_cast<int>(threadIdx.x), n - 1);
+        int lo = 0, hi = bk.tiles - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sh.off[mid] <= s0 + p)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        if (u * kRowThreads < n)         // uniform: small buckets load once
+            v[u] = bk.sidx[sh.src[lo] + (s0 + p - sh.off[lo])];
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+        if (u * kRowThreads + static_cast<int>(threadIdx.x) < n)
+            sh.words[u * kRowThreads + threadIdx.x] = v[u];
+}
+
+__device__ __forceinline__ int row_of(int word) {
+    return static_cast<int>(static_cast<uint32_t>(word) >> kSlotIdxBits);
+}
+
+// Stable sort of sh.words[0, n) by row in the bucket into sh.sorted, and the
+// first position of each row in sh.start[0 .. S].  Each wave owns a quarter;
+// lanes of equal row are found by one ballot per row bit.
+__device__ __forceinline__ void sort_by_row(int n, int s_log2, BucketShared &sh) {
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int S = 1 << s_log2;
+    const int quarter = (n + kRowThreads - 1) / kRowThreads * 64;
+    const int beg = min(n, w * quarter), end = min(n, beg + quarter);
+    for (int x = tid; x < kWaves * kMaxBucketRows; x += kRowThreads)
+        sh.cnt[x / kMaxBucketRows][x % kMaxBucketRows] = 0;
+    __syncthreads();
+    for (int i = beg + lane; i < end; i += 64)
+        atomicAdd(&sh.cnt[w][row_of(sh.words[i])], 1);
+    __syncthreads();
+    if (w == 0) {
+        int c[kWaves], sum = 0;
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            c[v] = sh.cnt[v][lane];
+            sum += c[v];
+        }
+        int run = wave_inclusive_sum(sum) - sum;
+        if (lane < S)
+            sh.start[lane] = run;
+        if (lane == 0)
+            sh.start[S] = n;
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            sh.cnt[v][lane] = run;
+            run += c[v];
+        }
+    }
+    __syncthreads();
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    for (int i0 = beg; i0 < end; i0 += 64) {
+        const bool in = i0 + lane < end;
+        const int word = in ? sh.words[i0 + lane] : 0;
+        const int r = row_of(word);
+        uint64_t same = __ballot(in);
+        for (int b = 0; b < s_log2; ++b) {
+            const bool bit = (r >> b) & 1;
+            const uint64_t m = __ballot(in && bit);
+            same &= bit ? m : ~m;
+        }
+        if (in) {
+            const int at = sh.cnt[w][r] + __popcll(same & below);
+            if ((same >> lane) == 1)     // the last lane of its row
+                sh.cnt[w][r] = at + 1;
+            sh.sorted[at] = word;
+        }
+    }
+    __syncthreads();
+}
+
+// A thread's place: its lane in a group, the group's share of the positions
+// (qp of gp) and its columns.
+template <int V>
+struct Place {
+    int l, qp, gp;
+    Columns<V> cols;
+    __device__ __forceinline__ Place(const GradArgs &g, const BucketArgs &bk)
+        : l(threadIdx.x & ((1 << g.lanes_log2) - 1)),
+          qp(threadIdx.x >> (g.lanes_log2 + bk.col_groups_log2)),
+          gp(kRowThreads >> (g.lanes_log2 + bk.col_groups_log2)),
+          cols((blockIdx.y << bk.col_groups_log2) +
+                   ((threadIdx.x >> g.lanes_log2) & ((1 << bk.col_groups_log2) - 1)),
+               1 << g.lanes_log2, l, g.D) {}
+};
+
+// Sums sh.sorted[0, n) (rows of bucket b) over this workgroup's columns.  PART:
+// into the partial sums of part `part`; else into dC, rows without a position
+// zeroed.  Ends with a barrier.
+template <typename T, typename O, int V, bool PART>
+__device__ __forceinline__ void sum_sorted(const GradArgs &g, const BucketArgs &bk,
+                                           const Place<V> &at, int b, int part, int n,
+                                           BucketShared &sh) {
+    typedef typename T::bits B;
+    const int S = 1 << bk.bucket_log2;
+    const int lo = n * at.qp / at.gp, hi = n * (at.qp + 1) / at.gp;
+    const bool any = at.cols.any;
+    auto edge = [&](int side, int thread) __attribute__((always_inline)) {
+        return sh.edge[side] + thread * V;
+    };
+    auto put = [&](int r, const float (&sum)[V]) __attribute__((always_inline)) {
+        if (PART)
+            store_partial<V>(
+                bk.partial + (static_cast<int64_t>(part) * S + r) * g.D + at.cols.first, sum);
+        else
+            finish_row<O, V>(g, (b << bk.bucket_log2) + r, at.cols, sum);
+    };
+    // The zeros need no positions: their stores go first and drain meanwhile.
+    if (!PART && any)
+        for (int r = at.qp; r < S; r += at.gp)
+            if (sh.start[r] == sh.start[r + 1] && (b << bk.bucket_log2) + r < g.K)
+                zero_row<O, V>(g, (b << bk.bucket_log2) + r, at.cols);
+    if (any && lo < hi) {
+        const B *src = static_cast<const B *>(g.dY) + at.cols.first;
+        int row = row_of(sh.sorted[lo]), first = lo;
+        float sum[V] = {};
+        // The run [first, end) of `row` is over: finished if it is the whole
+        // row, else an edge (0: it began in an earlier group).
+        auto close = [&](int end) __attribute__((always_inline)) {
+            if (first == sh.start[row] && end == sh.start[row + 1]) {
+                put(row, sum);
+            } else {
+                float *e = edge(first == sh.start[row] ? 1 : 0, threadIdx.x);
+#pragma unroll
+                for (int x = 0; x < V; ++x)
+                    e[x] = sum[x];
+            }
+        };
+        int word[kBatch];
+        Packed<B, V> val[kBatch];
+        for (int p0 = lo; p0 < hi; p0 += kBatch) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                word[u] = sh.sorted[min(p0 + u, hi - 1)];
+                const int64_t i = word[u] & ((1 << kSlotIdxBits) - 1);
+                val[u] = load_packed<B, V>(src + i * g.ldy);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (p0 + u >= hi)
+                    break;
+                const int r = row_of(word[u]);
+                if (r != row) {
+                    close(p0 + u);
+                    row = r;
+                    first = p0 + u;
+#pragma unroll
+                    for (int x = 0; x < V; ++x)
+                        sum[x] = 0.0f;
+                }
+#pragma unroll
+                for (int x = 0; x < V; ++x)
+                    sum[x] += T::widen(val[u].v[x]);
+            }
+        }
+        close(hi);
+    }
+    __syncthreads();
+    // The group in which a cut run began adds its pieces, in order.
+    if (any && lo < hi) {
+        const int r = row_of(sh.sorted[hi - 1]);
+        const int end = sh.start[r + 1];
+        if (sh.start[r] >= lo && end > hi) {
+            float sum[V];
+#pragma unroll
+            for (int x = 0; x < V; ++x)
+                sum[x] = edge(1, threadIdx.x)[x];
+            for (int o = at.qp + 1; o < at.gp && n * o / at.gp < end; ++o) {
+                if (n * o / at.gp == n * (o + 1) / at.gp)
+                    continue;
+                const float *e =
+                    edge(0, threadIdx.x + ((o - at.qp) << (g.lanes_log2 + bk.col_groups_log2)));
+#pragma unroll
+                for (int x = 0; x < V; ++x)
+                    sum[x] += e[x];
+            }
+            put(r, sum);
+        }
+    }
+    __syncthreads();
+}
+
+template <typename T, typename O, int V>
+__global__ __launch_bounds__(kRowThreads, 4)
+void lookup_bucket_kernel(const GradArgs g, const BucketArgs bk) {
+    __shared__ BucketShared sh;
+    const int b = blockIdx.x;
+    const int n = find_segments(bk, b, sh);
+    if (n > bk.cap) {
+        if (blockIdx.y == 0 && threadIdx.x == 0) {
+            const int parts = (n + bk.cap - 1) / bk.cap;
+            bk.heavy[atomicAdd(&bk.counts[0], 1)] = {b, atomicAdd(&bk.counts[1], parts), parts};
+        }
+        return;
+    }
+    if (n > 0)
+        gather_words(bk, 0, n, sh);
+    __syncthreads();
+    sort_by_row(n, bk.bucket_log2, sh);
+    sum_sorted<T, O, V, false>(g, bk, Place<V>(g, bk), b, 0, n, sh);
+}
+
+template <typename T, typename O, int V>
+__global__ __launch_bounds__(kRowThreads, 4)
+void lookup_part_kernel(const GradArgs g, const BucketArgs bk) {
+    __shared__ BucketShared sh;
+    const int entries = bk.counts[0], parts = bk.counts[1];
+    const int S = 1 << bk.bucket_log2;
+    for (int t = blockIdx.x; t < parts; t += gridDim.x) {
+        for (int e = threadIdx.x; e < entries; e += kRowThreads)
+            if (t >= bk.heavy[e].first_part && t < bk.heavy[e].first_part + bk.heavy[e].parts)
+                sh.found = e;                // exactly one
+        __syncthreads();
+        const Heavy h = bk.heavy[sh.found];
+        const int s0 = (t - h.first_part) * bk.cap;
+        const int n = min(find_segments(bk, h.bucket, sh) - s0, bk.cap);
+        gather_words(bk, s0, n, sh);
+        __syncthreads();
+        sort_by_row(n, bk.bucket_log2, sh);
+        if (blockIdx.y == 0 && static_cast<int>(threadIdx.x) < S)
+            bk.run_len[t * S + threadIdx.x] = sh.start[threadIdx.x + 1] - sh.start[threadIdx.x];
+        sum_sorted<T, O, V, true>(g, bk, Place<V>(g, bk), h.bucket, t, n, sh);
+    }
+}
+
+// Rows of heavy buckets, one workgroup a row at a time: its groups of lanes
+// take every groups-th part, and their sums are added in group order.
+template <typename O, int V>
+__global__ __launch_bounds__(kRowThreads)
+void lookup_part_join_kernel(const GradArgs g, const BucketArgs bk) {
+    __shared__ float sums[kRowThreads][V + 1];
+    __shared__ int total[kRowThreads];
+    const int S = 1 << bk.bucket_log2;
+    const int items = bk.counts[0] << bk.bucket_log2;
+    const Place<V> at(g, bk);
+    for (int x = blockIdx.x; x < items; x += gridDim.x) {
+        const Heavy h = bk.heavy[x >> bk.bucket_log2];
+        const int r = x & (S - 1), k = (h.bucket << bk.bucket_log2) + r;
+        float sum[V] = {};
+        int positions = 0;
+        for (int t0 = at.qp; t0 < h.parts; t0 += kBatch * at.gp) {
+            int len[kBatch];
+            Packed<float, V> v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const bool in = t0 + u * at.gp < h.parts;
+                const int64_t t = h.first_part + (in ? t0 + u * at.gp : t0);
+                len[u] = in ? bk.run_len[t * S + r] : 0;
+                if (at.cols.any)
+                    v[u] = load_packed<float, V>(bk.partial + (t * S + r) * g.D + at.cols.first);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (len[u] > 0) {                // else nothing was written there
+                    positions += len[u];
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        sum[e] += v[u].v[e];
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            sums[threadIdx.x][e] = sum[e];
+        total[threadIdx.x] = positions;
+        __syncthreads();
+        if (at.qp == 0 && at.cols.any && k < g.K) {
+            for (int o = 1; o < at.gp; ++o) {
+                const int other = threadIdx.x + (o << g.lanes_log2);
+                positions += total[other];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    sum[e] += sums[other][e];
+            }
+            if (positions > 0)
+                finish_row<O, V>(g, k, at.cols, sum);
+            else
+                zero_row<O, V>(g, k, at.cols);
+        }
+        __syncthreads();
     }
 }
 
 // ---- launch ----------------------------------------------------------------
 
 struct GradPlan {
+    int lanes_log2, slabs;
+    bool by_buckets;
+    // buckets
+    LabelBins bins;
+    int cap, col_groups_log2, column_groups;
+    int max_parts;
+    size_t counts, heavy, run_len;
+    // sort
     LabelSort sort;
-    int chunk, chunks, lanes_log2, slabs;
+    int chunk, chunks;
     size_t partial, bytes;
 };
+
+size_t align_up(size_t n) { return (n + 255) & ~size_t(255); }
+
+constexpr int64_t kMinBucketRows = 256;                 // fewer buckets leave CUs idle
+constexpr int64_t kMaxBucketTable = int64_t(1024) * kMaxBucketRows;
+constexpr int64_t kMaxMeanBucket = 1024;                // positions
+constexpr int64_t kMinCap = 128;
 
 GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_units) {
     GradPlan p{};
     while (p.lanes_log2 < 6 && (int64_t(V) << p.lanes_log2) < D)
         ++p.lanes_log2;
-    p.slabs = static_cast<int>((D + (int64_t(V) << p.lanes_log2) - 1) / (int64_t(V) << p.lanes_log2));
+    const int64_t slab = int64_t(V) << p.lanes_log2;    // columns of one group of lanes
+    p.slabs = static_cast<int>((D + slab - 1) / slab);
     if (N == 0)
         return p;
+    if (K >= kMinBucketRows && K <= kMaxBucketTable && N <= kMaxMeanBucket * 1024) {
+        p.bins = make_label_bins(N, K);
+        p.by_buckets = N <= kMaxMeanBucket * p.bins.buckets;
+    }
+    if (p.by_buckets) {
+        // Few positions per bucket and wide rows: the groups of a workgroup
+        // take columns side by side, so that none waits for the others and
+        // the gathering serves them all.  Else they divide the positions.
+        if (N <= 64 * static_cast<int64_t>(p.bins.buckets))
+            while ((1 << (p.lanes_log2 + p.col_groups_log2)) < kRowThreads &&
+                   (1 << p.col_groups_log2) < p.slabs)
+                ++p.col_groups_log2;
+        p.column_groups = (p.slabs + (1 << p.col_groups_log2) - 1) >> p.col_groups_log2;
+        // A part is 1024 positions of 256 bytes, fewer for wider slabs, and
+        // at least twice the mean bucket; larger where the partial sums would
+        // take more than 256 MiB.  A heavy bucket has more than `cap`
+        // positions, so its parts hold half of that each on average at least.
+        const int64_t bytes = std::min(D, slab) * (V == 8 ? 2 : 4);
+        int64_t cap = std::max<int64_t>((int64_t(1) << 26) / (bytes * bytes),
+                                        2 * N / p.bins.buckets);
+        cap = std::min<int64_t>(std::max(cap, kMinCap), kBucketCap);
+        auto rows = [&] { return static_cast<size_t>(2 * N / cap + 1) << p.bins.bucket_log2; };
+        while (cap < kBucketCap && rows() * D * sizeof(float) > (size_t(256) << 20))
+            cap = std::min<int64_t>(2 * cap, kBucketCap);
+        p.cap = static_cast<int>(cap);
+        p.max_parts = static_cast<int>(2 * N / cap + 1);
+        p.counts = align_up(p.bins.bytes);
+        p.heavy = p.counts + 256;
+        p.run_len = p.heavy + align_up((N / cap + 1) * sizeof(Heavy));
+        p.partial = p.run_len + align_up(rows() * sizeof(int));
+        p.bytes = p.partial + rows() * D * sizeof(float);
+        return p;
+    }
     // Chunks of at least 8 positions, more when that leaves eight waves or
     // more per CU.
     const int64_t waves_at_1 = ((N << p.lanes_log2) + 63) / 64 * p.slabs;
@@ -341,13 +820,32 @@ GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_unit
     p.chunk = static_cast<int>(chunk);
     p.chunks = static_cast<int>((N + chunk - 1) / chunk);
     p.sort = make_label_sort(N, K);
-    p.partial = (p.sort.bytes + 255) & ~size_t(255);
+    p.partial = align_up(p.sort.bytes);
     p.bytes = p.partial + static_cast<size_t>(p.chunks) * 2 * D * sizeof(float);
     return p;
 }
 
 template <typename T, typename O, int V>
-hipError_t launch_grad(const GradPlan &p, const GradArgs &g, hipStream_t stream) {
+hipError_t launch_grad(const GradPlan &p, const GradArgs &g, const BucketArgs &bk,
+                       int compute_units, hipStream_t stream) {
+    if (p.by_buckets) {
+        hipLaunchKernelGGL((lookup_bucket_kernel<T, O, V>),
+                           dim3(p.bins.buckets, p.column_groups), dim3(kRowThreads), 0, stream, g,
+                           bk);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess || g.N <= p.cap)            // no bucket can be heavy
+            return e;
+        BucketArgs pk = bk;
+        pk.col_groups_log2 = 0;
+        hipLaunchKernelGGL((lookup_part_kernel<T, O, V>),
+                           dim3(std::min(p.max_parts, 2 * compute_units), p.slabs),
+                           dim3(kRowThreads), 0, stream, g, pk);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+        hipLaunchKernelGGL((lookup_part_join_kernel<O, V>), dim3(compute_units, p.slabs),
+                           dim3(kRowThreads), 0, stream, g, pk);
+        return hipGetLastError();
+    }
     const int per_wg = kRowThreads >> p.lanes_log2;
     const int sum_wgs = (p.chunks + per_wg - 1) / per_wg;
     const int fill_wgs = g.accumulate ? 0 : (g.K + kFillRows - 1) / kFillRows;
@@ -475,8 +973,11 @@ extern "C" kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride,
         return st;
     if (N == 0 && accumulate)
         return ok();
-    const int V = 16 / static_cast<int>(dtype_size(dtype));
-    const GradPlan p = make_grad_plan(N, D, K, V, device_compute_units());
+    // 16 bytes of a row per lane, single values where a row is shorter.
+    const int V = D * static_cast<int64_t>(dtype_size(dtype)) >= 16
+                      ? 16 / static_cast<int>(dtype_size(dtype)) : 1;
+    const int cus = device_compute_units();
+    const GradPlan p = make_grad_plan(N, D, K, V, cus);
     if (p.slabs > 65535)
         return fail(KMEANS_ERR_UNSUPPORTED, "D=%lld too large", static_cast<long long>(D));
     GradArgs g{};
@@ -493,6 +994,7 @@ extern "C" kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride,
     g.chunks = p.chunks;
     g.lanes_log2 = p.lanes_log2;
     g.slabs = p.slabs;
+    BucketArgs bk{};
     std::unique_ptr<WorkspaceLease> lease;
     hipError_t e = hipSuccess;
     if (N > 0) {
@@ -501,18 +1003,32 @@ extern "C" kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride,
             return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", p.bytes,
                         hipGetErrorString(lease->error()));
         auto *ws = static_cast<char *>(lease->ptr());
+        auto ints = [&](size_t at) { return reinterpret_cast<int *>(ws + at); };
         g.partial = reinterpret_cast<float *>(ws + p.partial);
-        e = launch_label_sort(p.sort, labels, label_type, g.N, g.K, ws, &g.keys, &g.vals, stream);
+        if (p.by_buckets) {
+            bk = {ints(p.bins.sidx), ints(p.bins.dir), p.bins.bucket_log2, p.bins.buckets,
+                  p.bins.tile_log2, p.bins.tiles, p.cap, p.col_groups_log2, ints(p.counts),
+                  reinterpret_cast<Heavy *>(ws + p.heavy), ints(p.run_len), g.partial};
+            e = launch_label_bins(p.bins, labels, label_type, g.N, g.K, ws, bk.counts, 2, stream);
+        } else {
+            e = launch_label_sort(p.sort, labels, label_type, g.N, g.K, ws, &g.keys, &g.vals,
+                                  stream);
+        }
     }
     if (e == hipSuccess) {
+        auto launch = [&](auto type, auto out) {
+            using T = decltype(type);
+            using O = decltype(out);
+            constexpr int kWide = 16 / sizeof(typename T::bits);
+            return V == 1 ? launch_grad<T, O, 1>(p, g, bk, cus, stream)
+                          : launch_grad<T, O, kWide>(p, g, bk, cus, stream);
+        };
         if (dtype == KMEANS_BF16)
-            e = out_dtype == dtype ? launch_grad<Bf16, Bf16, 8>(p, g, stream)
-                                   : launch_grad<Bf16, Fp32, 8>(p, g, stream);
+            e = out_dtype == dtype ? launch(Bf16{}, Bf16{}) : launch(Bf16{}, Fp32{});
         else if (dtype == KMEANS_FP16)
-            e = out_dtype == dtype ? launch_grad<Fp16, Fp16, 8>(p, g, stream)
-                                   : launch_grad<Fp16, Fp32, 8>(p, g, stream);
+            e = out_dtype == dtype ? launch(Fp16{}, Fp16{}) : launch(Fp16{}, Fp32{});
         else
-            e = launch_grad<Fp32, Fp32, 4>(p, g, stream);
+            e = launch(Fp32{}, Fp32{});
     }
     if (e != hipSuccess)
         return fail(KMEANS_ERR_HIP, "lookup gradient launch failed: %s", hipGetErrorString(e));

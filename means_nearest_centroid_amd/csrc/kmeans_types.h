@@ -70,8 +70,10 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 template <typename B, int n>
 __device__ __forceinline__ Packed<B, n> load_packed(const B *p) {
     constexpr size_t bytes = sizeof(B) * n;
-    static_assert(bytes == 8 || bytes == 16 || bytes == 32, "vector accesses");
-    if constexpr (bytes == 8) {
+    static_assert(n == 1 || bytes == 8 || bytes == 16 || bytes == 32, "vector accesses");
+    if constexpr (n == 1) {
+        return Packed<B, n>{{*p}};
+    } else if constexpr (bytes == 8) {
         return __builtin_bit_cast(Packed<B, n>, *reinterpret_cast<const u32x2_any *>(p));
     } else if constexpr (bytes == 16) {
         return __builtin_bit_cast(Packed<B, n>, *reinterpret_cast<const u32x4_any *>(p));
@@ -85,8 +87,10 @@ __device__ __forceinline__ Packed<B, n> load_packed(const B *p) {
 template <typename B, int n>
 __device__ __forceinline__ void store_packed(B *p, const Packed<B, n> &q) {
     constexpr size_t bytes = sizeof(B) * n;
-    static_assert(bytes == 8 || bytes == 16 || bytes == 32, "vector accesses");
-    if constexpr (bytes == 8) {
+    static_assert(n == 1 || bytes == 8 || bytes == 16 || bytes == 32, "vector accesses");
+    if constexpr (n == 1) {
+        *p = q.v[0];
+    } else if constexpr (bytes == 8) {
         *reinterpret_cast<u32x2_any *>(p) = __builtin_bit_cast(u32x2_any, q);
     } else if constexpr (bytes == 16) {
         *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4_any, q);
@@ -125,8 +129,7 @@ __device__ __forceinline__ void store_run(B *p, int m, const Packed<B, n> &q) {
 // n values rounded to T.
 template <typename T, int n>
 __device__ __forceinline__ Packed<typename T::bits, n> narrow_run(const float (&v)[n]) {
-    if constexpr (sizeof(typename T::bits) == 2) {
-        static_assert(n % 2 == 0, "pairs");
+    if constexpr (sizeof(typename T::bits) == 2 && n % 2 == 0) {
         Packed<uint32_t, n / 2> q;
 #pragma unroll
         for (int c = 0; c < n / 2; ++c)

@@ -64,12 +64,6 @@ __device__ __forceinline__ int sort_key(int32_t label, int K) {
     return (label < 0 || label >= K) ? K : label;
 }
 
-// A label as int32 (one outside its range as -1, a stray label too).
-__device__ __forceinline__ int32_t label32(int32_t label) { return label; }
-__device__ __forceinline__ int32_t label32(int64_t label) {
-    return label < 0 || label > INT32_MAX ? -1 : static_cast<int32_t>(label);
-}
-
 __device__ __forceinline__ float widen(uint32_t b16) { return __uint_as_float(b16 << 16); }
 
 // fp32 -> bf16 bits, nearest with ties to even; NaN -> the quiet NaN 0x7FC0
@@ -142,21 +136,6 @@ void upd_hist_kernel(const L *__restrict__ keys_in, int N, int K, int shift, int
         for (int64_t j = static_cast<int64_t>(t) * kSortThreads + tid; j < n_clear; j += step)
             clear[j] = 0;
     }
-}
-
-// Inclusive prefix sum over the 64 lanes of a wave by DPP: shifts right by
-// 1, 2, 4 and 8 lanes within each row of 16 (lanes shifted in from outside
-// the row read 0), then each row adds the last lane of the rows before it
-// (row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3).
-__device__ __forceinline__ int wave_inclusive_sum(int x) {
-    constexpr int kRowShr = 0x110, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
-    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 1, 0xf, 0xf, true);
-    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 2, 0xf, 0xf, true);
-    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 4, 0xf, 0xf, true);
-    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 8, 0xf, 0xf, true);
-    x += __builtin_amdgcn_update_dpp(0, x, kRowBcast15, 0xa, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, kRowBcast31, 0xc, 0xf, false);
-    return x;
 }
 
 // Exclusive scan of h[0..M) in place (M a multiple of 4), one workgroup:
@@ -803,7 +782,6 @@ constexpr int kBucketThreads = 256;  // 4 waves
 constexpr int kBucketWaves = kBucketThreads / 64;
 constexpr int kBucketChunk = 512;    // slots summed per round
 constexpr int kBucketSlots = 2048;   // a bucket up to this size has all its slot words in LDS
-constexpr int kSlotIdxBits = 24;     // a slot word: point index | cluster in bucket << 24
 static_assert(kMaxBinPoints <= (int64_t(1) << kSlotIdxBits), "point indices fit the slot word");
 static_assert(kSlotIdxBits + kMaxBucketLog2 <= 31, "the cluster in its bucket fits the slot word");
 
@@ -827,9 +805,12 @@ static_assert(kSlotIdxBits + kMaxBucketLog2 <= 31, "the cluster in its bucket fi
 // flight together (unconditional loads clamped to the wave's last point,
 // taken by an empty asm); a wave holding one batch (tiles up to 4096) keeps
 // it in registers from the counts to the ranks.
+// Workgroup 0 also clears `clear` (n_clear entries).
+template <typename L>
 __global__ __launch_bounds__(kBinThreads)
-void upd_bin_kernel(const int32_t *__restrict__ labels, int N, int K, int s_log2, int nb,
-                    int tl, int32_t *__restrict__ sidx, int32_t *__restrict__ dir) {
+void upd_bin_kernel(const L *__restrict__ labels, int N, int K, int s_log2, int nb,
+                    int tl, int32_t *__restrict__ sidx, int32_t *__restrict__ dir,
+                    int32_t *__restrict__ clear, int n_clear) {
     typedef int32_t i4 __attribute__((ext_vector_type(4)));
     __shared__ __attribute__((aligned(16))) int cnt[kBinWaves * kMaxBuckets];
     __shared__ int wtot[kBinWaves];
@@ -852,7 +833,7 @@ void upd_bin_kernel(const int32_t *__restrict__ labels, int N, int K, int s_log2
     auto load_batch = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            v[u] = labels[beg + min(i0 + u * 64 + lane, we - 1)];
+            v[u] = label32(labels[beg + min(i0 + u * 64 + lane, we - 1)]);
 #if defined(__HIP_DEVICE_COMPILE__)
         static_assert(kBatch == 8, "the asm below names eight values");
         asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]),
@@ -866,6 +847,9 @@ void upd_bin_kernel(const int32_t *__restrict__ labels, int N, int K, int s_log2
     const bool one_batch = we - wb <= kBatch * 64;
     if (wb < we)
         load_batch(wb);
+    if (t == 0)
+        for (int i = tid; i < n_clear; i += kBinThreads)
+            clear[i] = 0;
     __syncthreads();                               // cnt cleared
     int *mine = cnt + w * NR;
 
@@ -1680,6 +1664,42 @@ hipError_t launch_label_sort(const LabelSort &sort, const void *labels, int32_t 
     return e;
 }
 
+LabelBins make_label_bins(int64_t N, int64_t K) {
+    // Buckets of S = 2^s clusters, at most 1024 of them (one round of bucket
+    // workgroups on 256 CUs); tiles of 2^tl >= 1024 points, at most 512 of
+    // them (each bucket workgroup reads two directory entries per tile).
+    LabelBins p{};
+    while ((K + (int64_t(1) << p.bucket_log2) - 1) >> p.bucket_log2 > kMaxBuckets)
+        ++p.bucket_log2;
+    p.buckets = static_cast<int>((K + (int64_t(1) << p.bucket_log2) - 1) >> p.bucket_log2);
+    p.tile_log2 = kMinBinTileLog2;
+    while (((N + (int64_t(1) << p.tile_log2) - 1) >> p.tile_log2) > kMaxBinTiles)
+        ++p.tile_log2;
+    p.tiles = static_cast<int>((N + (int64_t(1) << p.tile_log2) - 1) >> p.tile_log2);
+    if (N > 0) {
+        p.sidx = 0;
+        p.dir = align_up(static_cast<size_t>(N) * 4);
+        p.bytes = p.dir + align_up(static_cast<size_t>(p.buckets + 1) * p.tiles * 4);
+    }
+    return p;
+}
+
+hipError_t launch_label_bins(const LabelBins &bins, const void *labels, int32_t label_type, int N,
+                             int K, void *ws, int32_t *clear, int n_clear, hipStream_t stream) {
+    auto *base = static_cast<char *>(ws);
+    auto *sidx = reinterpret_cast<int32_t *>(base + bins.sidx);
+    auto *dir = reinterpret_cast<int32_t *>(base + bins.dir);
+    if (label_type == KMEANS_INT64)
+        hipLaunchKernelGGL(upd_bin_kernel<int64_t>, dim3(bins.tiles), dim3(kBinThreads), 0, stream,
+                           static_cast<const int64_t *>(labels), N, K, bins.bucket_log2,
+                           bins.buckets, bins.tile_log2, sidx, dir, clear, n_clear);
+    else
+        hipLaunchKernelGGL(upd_bin_kernel<int32_t>, dim3(bins.tiles), dim3(kBinThreads), 0, stream,
+                           static_cast<const int32_t *>(labels), N, K, bins.bucket_log2,
+                           bins.buckets, bins.tile_log2, sidx, dir, clear, n_clear);
+    return hipGetLastError();
+}
+
 // Below this many clusters there are too few buckets to fill the GPU (one
 // workgroup each), and the radix path is used.
 constexpr int64_t kMinBucketPathK = 256;
@@ -1694,29 +1714,14 @@ UpdatePlan make_update_plan(int64_t N, int64_t D, int64_t K, int compute_units, 
     p.path = force_path != 0 ? force_path
                              : (K >= kMinBucketPathK && bucket_path_fits(N, K) ? 2 : 1);
     if (p.path == 2) {
-        // Buckets of S = 2^s clusters, at most 1024 of them (one round of
-        // bucket workgroups on 256 CUs); tiles of 2^tl >= 1024 points, at
-        // most 512 of them (each bucket workgroup reads two directory
-        // entries per tile).
-        int sl = 0;
-        while ((K + (int64_t(1) << sl) - 1) >> sl > kMaxBuckets)
-            ++sl;
-        p.bucket_log2 = sl;
-        p.buckets = static_cast<int>((K + (int64_t(1) << sl) - 1) >> sl);
-        int tl = kMinBinTileLog2;
-        while (((N + (int64_t(1) << tl) - 1) >> tl) > kMaxBinTiles)
-            ++tl;
-        p.bin_tile_log2 = tl;
-        p.bin_tiles = static_cast<int>((N + (int64_t(1) << tl) - 1) >> tl);
-        size_t off = 0;
-        if (N > 0) {
-            const size_t n4 = align_up(static_cast<size_t>(N) * 4);
-            p.sidx = off;
-            off += n4;
-            p.dir = off;
-            off += align_up(static_cast<size_t>(p.buckets + 1) * p.bin_tiles * 4);
-        }
-        p.bytes = off;
+        const LabelBins bins = make_label_bins(N, K);
+        p.bucket_log2 = bins.bucket_log2;
+        p.buckets = bins.buckets;
+        p.bin_tile_log2 = bins.tile_log2;
+        p.bin_tiles = bins.tiles;
+        p.sidx = bins.sidx;
+        p.dir = bins.dir;
+        p.bytes = bins.bytes;
         return p;
     }
     p.sort = make_label_sort(N, K);
@@ -1745,9 +1750,9 @@ hipError_t launch_update(const UpdatePlan &pl, const uint16_t *X, const int32_t 
         if (N > 0) {
             sidx = reinterpret_cast<int32_t *>(base + pl.sidx);
             dir = reinterpret_cast<int32_t *>(base + pl.dir);
-            hipLaunchKernelGGL(upd_bin_kernel, dim3(pl.bin_tiles), dim3(kBinThreads), 0, stream,
-                               labels, N, K, pl.bucket_log2, pl.buckets, pl.bin_tile_log2, sidx,
-                               dir);
+            hipLaunchKernelGGL(upd_bin_kernel<int32_t>, dim3(pl.bin_tiles), dim3(kBinThreads), 0,
+                               stream, labels, N, K, pl.bucket_log2, pl.buckets,
+                               pl.bin_tile_log2, sidx, dir, nullptr, 0);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess)
                 return e;

@@ -29,6 +29,47 @@ hipError_t launch_label_sort(const LabelSort &sort, const void *labels, int32_t 
                              int K, void *ws, const int32_t **keys, const int32_t **vals,
                              hipStream_t stream);
 
+// Labels grouped into at most 1024 buckets of 2^bucket_log2 clusters: each tile
+// of 2^tile_log2 points is sorted by bucket, stably, into slot words (the point
+// index, its cluster in the bucket above bit kSlotIdxBits) at sidx, and its
+// directory row holds the first slot of each bucket and, last, the number of
+// points with a label in [0, K): dir[tile][buckets + 1].  Offsets are relative
+// to the workspace.
+struct LabelBins {
+    int bucket_log2, buckets, tile_log2, tiles;
+    size_t sidx, dir, bytes;
+};
+constexpr int kSlotIdxBits = 24;
+
+// At most 2^24 points, 512 tiles, and buckets of at most 128 clusters
+// (K <= 2^17).
+LabelBins make_label_bins(int64_t N, int64_t K);
+
+// The one launch; it also zeroes n_clear entries of clear.
+hipError_t launch_label_bins(const LabelBins &bins, const void *labels, int32_t label_type, int N,
+                             int K, void *ws, int32_t *clear, int n_clear, hipStream_t stream);
+
+// A label as int32 (one outside its range as -1, a stray label too).
+__device__ __forceinline__ int32_t label32(int32_t label) { return label; }
+__device__ __forceinline__ int32_t label32(int64_t label) {
+    return label < 0 || label > INT32_MAX ? -1 : static_cast<int32_t>(label);
+}
+
+// Inclusive prefix sum over the 64 lanes of a wave by DPP: shifts right by
+// 1, 2, 4 and 8 lanes within each row of 16 (lanes shifted in from outside
+// the row read 0), then each row adds the last lane of the rows before it
+// (row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3).
+__device__ __forceinline__ int wave_inclusive_sum(int x) {
+    constexpr int kRowShr = 0x110, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 1, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 2, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 4, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, kRowShr + 8, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, kRowBcast15, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, kRowBcast31, 0xc, 0xf, false);
+    return x;
+}
+
 // Workspace layout and launch shape of one kmeans_update call.
 struct UpdatePlan {
     int path;          // 1: radix sort + chunked reduce + finish; 2: buckets

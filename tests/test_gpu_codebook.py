@@ -145,8 +145,31 @@ def test_lookup_grad_of_one_label(N, D):
     ref.check(got, want, bound)
 
 
+@pytest.mark.parametrize("N,K,D,kind", [
+    (2049, 256, 8, "one"),       # one position past a workgroup's share, one run over all
+    (40000, 300, 64, "one"), (70001, 5000, 130, "zipf"), (30000, 65536, 24, "zipf"),
+    (262144, 257, 16, "uniform"), (100000, 256, 12, "zipf"), (9000, 4096, 1100, "one"),
+    (5000, 65537, 40, "zipf"), (300000, 256, 8, "uniform")])    # the sort path again
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_lookup_grad_of_frequent_labels(N, K, D, kind, accumulate):
+    """Buckets holding more positions than one workgroup sorts, several of
+    them, with absent rows beside the frequent ones; and the limits between
+    the two paths."""
+    dY = rand((N, D), BF, 31)
+    lab = some_labels(N, K, 32, torch.int32, kind)
+    into = rand((K, D), F32, 33)
+    before = into.clone()
+    want, bound = ref.lookup_grad(dY, lab, K, 0.75, F32, into=before if accumulate else None)
+    km.kmeans_lookup_grad(dY, lab, K, scale=0.75, out=into, accumulate=accumulate)
+    ref.check(into, want, bound, f"{N} {K} {D} {kind}")
+    again = before.clone()
+    km.kmeans_lookup_grad(dY, lab, K, scale=0.75, out=again, accumulate=accumulate)
+    assert torch.equal(again, into)
+
+
 @pytest.mark.parametrize("dtype,out_dtype", [(BF, BF), (BF, F32), (FP, F32), (F32, F32)])
-@pytest.mark.parametrize("N,K,D", [(1000, 37, 16), (777, 300, 129), (3000, 2, 64), (50, 9, 515)])
+@pytest.mark.parametrize("N,K,D", [(1000, 37, 16), (777, 300, 129), (3000, 2, 64), (50, 9, 515),
+                                   (900, 270, 515), (40, 300, 5)])
 def test_lookup_grad_accumulates(N, K, D, dtype, out_dtype):
     dY = rand((N, D), dtype, 11)
     lab = some_labels(N, K, 12)
