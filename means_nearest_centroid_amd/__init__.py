@@ -26,6 +26,7 @@ its gradient and the clipping also fp32):
 
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -63,12 +64,6 @@ _STATUS_NAMES = {
 }
 
 _lib = None
-
-
-class _Gradient(ctypes.Structure):
-    """kmeans_gradient_t."""
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class KmeansError(RuntimeError):
@@ -330,6 +325,7 @@ def kmeans_update(X, labels, C_old, C_new=None, norms=None, counts=None, means=N
 # ---- training a codebook by gradients ----
 
 _DTYPES = None
+_CURRENT_DEVICE = None
 
 
 def _dtype(t, name):
@@ -344,26 +340,52 @@ def _dtype(t, name):
     return code
 
 
+def _launch(call, device, stream, *args):
+    """``call(*args, stream handle)`` under ``device``, a non-OK status
+    raised.  These calls are often a few microseconds of GPU time, so the
+    common case (the tensors' device is the current one) does no more than
+    look."""
+    global _CURRENT_DEVICE
+    if _CURRENT_DEVICE is None:
+        import torch
+        _CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    handle = _stream_handle(stream, device)
+    if device.index == _CURRENT_DEVICE():
+        status = call(*args, handle)
+    else:
+        import torch
+        with torch.cuda.device(device):
+            status = call(*args, handle)
+    if status != KMEANS_OK:
+        _check(_lib, status)
+
+
 def _rows(t, name, like=None, shape=None):
     """Check a 2-D CUDA tensor with unit column stride; its row stride.  A
     tensor of one row or less, or one column, may report any stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2 or not t.is_cuda:
+    try:
+        rows, cols = t.shape
+        row_stride, col_stride = t.stride()
+        on_gpu = t.is_cuda
+    except (AttributeError, ValueError):
+        import torch
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor") from None
+        on_gpu = False
+    if not on_gpu:
         raise ValueError(f"{name} must be a 2-D CUDA tensor (got {tuple(t.shape)}, {t.device})")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if cols > 1 and col_stride != 1:
         raise ValueError(f"{name} must have unit column stride (strides {t.stride()})")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be {like.dtype} on {like.device} "
                          f"(got {t.dtype} on {t.device})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    stride = t.stride(0) if rows > 1 else max(cols, 1)
-    if stride < cols:
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must have shape {shape} (got {(rows, cols)})")
+    if rows <= 1:
+        return cols or 1
+    if row_stride < cols:
         raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return stride
+    return row_stride
 
 
 def _flat(t, name):
@@ -382,38 +404,38 @@ def _flat(t, name):
                          "evenly spaced; make it contiguous") from None
 
 
-def _labels(labels, device):
+def _labels(labels, index):
+    """kmeans_label_t of a labels tensor on GPU ``index``."""
     import torch
-    if (not isinstance(labels, torch.Tensor) or labels.dtype not in (torch.int32, torch.int64)
-            or labels.device != device or not labels.is_contiguous()):
-        got = (f"{labels.dtype}, {labels.device}, contiguous={labels.is_contiguous()}"
-               if isinstance(labels, torch.Tensor) else type(labels).__name__)
-        raise ValueError(f"labels must be a contiguous int32 or int64 tensor on {device} "
-                         f"(got {got})")
-    return INT64 if labels.dtype == torch.int64 else INT32
+    if isinstance(labels, torch.Tensor) and labels.get_device() == index and labels.is_contiguous():
+        if labels.dtype is torch.int64:
+            return INT64
+        if labels.dtype is torch.int32:
+            return INT32
+    got = (f"{labels.dtype}, {labels.device}, contiguous={labels.is_contiguous()}"
+           if isinstance(labels, torch.Tensor) else type(labels).__name__)
+    raise ValueError(f"labels must be a contiguous int32 or int64 tensor on cuda:{index} "
+                     f"(got {got})")
 
 
 def kmeans_lookup(C, labels, scale: float = 1.0, out=None, stream=None):
     """``out[i] = scale * C[labels[i]]``, a row of zeros for a label outside
     ``[0, K)``.  ``C``: ``[K, D]`` bf16, fp16 or fp32, any row stride;
     ``labels``: int32 or int64 of any shape; ``out``: ``[*labels.shape, D]``."""
-    import torch
     c_stride = _rows(C, "C")
     code = _dtype(C, "C")
     K, D = C.shape
-    kind = _labels(labels, C.device)
+    kind = _labels(labels, C.get_device())
     if out is None:
-        out = torch.empty((*labels.shape, D), dtype=C.dtype, device=C.device)
+        out = C.new_empty((*labels.shape, D))
         y_stride = D
     else:
         if tuple(out.shape) != (*labels.shape, D):
             raise ValueError(f"out must have shape {(*labels.shape, D)} (got {tuple(out.shape)})")
         y_stride = _rows(_flat(out, "out") if out.dim() != 1 else out.view(1, D), "out", like=C)
     lib = load_library()
-    with _on(C.device):
-        _check(lib, lib.kmeans_lookup(_ptr(C), c_stride, _ptr(labels), kind, labels.numel(), D, K,
-                                      code, scale, _ptr(out), y_stride,
-                                      _stream_handle(stream, C.device)))
+    _launch(lib.kmeans_lookup, C.device, stream, C.data_ptr(), c_stride, labels.data_ptr(), kind,
+            labels.numel(), D, K, code, scale, out.data_ptr(), y_stride)
     return out
 
 
@@ -430,22 +452,21 @@ def kmeans_lookup_grad(dY, labels, K: int, scale: float = 1.0, out=None,
     y_stride = _rows(dY, "dY")
     code = _dtype(dY, "dY")
     N, D = dY.shape
-    kind = _labels(labels, dY.device)
+    kind = _labels(labels, dY.get_device())
     if labels.numel() != N:
         raise ValueError(f"dY has {N} rows but there are {labels.numel()} labels")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((K, D), dtype=dY.dtype, device=dY.device)
+        out = dY.new_empty((K, D))
     c_stride = _rows(out, "out", shape=(K, D))
-    if out.device != dY.device or out.dtype not in (dY.dtype, torch.float32):
+    if out.get_device() != dY.get_device() or out.dtype not in (dY.dtype, torch.float32):
         raise ValueError(f"out must be {dY.dtype} or float32 on {dY.device} "
                          f"(got {out.dtype} on {out.device})")
     lib = load_library()
-    with _on(dY.device):
-        _check(lib, lib.kmeans_lookup_grad(_ptr(dY), y_stride, _ptr(labels), kind, N, D, K, code,
-                                           scale, int(accumulate), _ptr(out), _dtype(out, "out"),
-                                           c_stride, _stream_handle(stream, dY.device)))
+    _launch(lib.kmeans_lookup_grad, dY.device, stream, dY.data_ptr(), y_stride, labels.data_ptr(),
+            kind, N, D, K, code, scale, int(accumulate), out.data_ptr(), _dtype(out, "out"),
+            c_stride)
     return out
 
 
@@ -458,8 +479,8 @@ def _activation(name) -> int:
 
 def _bias(t, F, like):
     import torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != like.dtype or t.device != like.device
-            or t.numel() != F or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not like.dtype
+            or t.get_device() != like.get_device() or t.numel() != F or not t.is_contiguous()):
         raise ValueError(f"bias must be a contiguous {like.dtype} tensor of {F} elements on "
                          f"{like.device}")
     return t
@@ -471,40 +492,39 @@ def kmeans_linear(X, W, bias=None, residual=None, activation: str = "none",
     ``[..., D]``, ``W``: ``[F, D]``, bf16 or fp16; ``activation``: a key of
     ``ACTIVATIONS``.  Returns ``Y``, or ``(Y, Z)`` with ``save_pre`` (or
     ``pre`` given), which ``kmeans_linear_grad`` needs."""
-    import torch
     lead = X.shape[:-1]
     X = _flat(X, "X")
     x_stride = _rows(X, "X")
     code = _dtype(X, "X")
     N, D = X.shape
     w_stride = _rows(W, "W", like=X)
-    F = W.shape[0]
-    if W.shape[1] != D:
-        raise ValueError(f"X has D={D} but W has D={W.shape[1]}")
+    F, d = W.shape
+    if d != D:
+        raise ValueError(f"X has D={D} but W has D={d}")
     act = _activation(activation)
     if bias is not None:
-        _bias(bias, F, X)
+        bias = _bias(bias, F, X).data_ptr()
     r_stride = 0
     if residual is not None:
         residual = _flat(residual, "residual")
         r_stride = _rows(residual, "residual", like=X, shape=(N, F))
+        residual = residual.data_ptr()
     if out is None:
-        out = torch.empty((*lead, F), dtype=X.dtype, device=X.device)
+        out = X.new_empty((*lead, F))
         y_stride = F
     else:
         y_stride = _rows(_flat(out, "out"), "out", like=X, shape=(N, F))
-    z_stride = 0
+    z_stride, z = 0, None
     if pre is not None:
         z_stride = _rows(_flat(pre, "pre"), "pre", like=X, shape=(N, F))
     elif save_pre:
-        pre = torch.empty((*lead, F), dtype=X.dtype, device=X.device)
+        pre = X.new_empty((*lead, F))
         z_stride = F
+    if pre is not None:
+        z = pre.data_ptr()
     lib = load_library()
-    with _on(X.device):
-        _check(lib, lib.kmeans_linear(_ptr(X), x_stride, _ptr(W), w_stride, _ptr(bias),
-                                      _ptr(residual), r_stride, N, D, F, code, act, _ptr(out),
-                                      y_stride, _ptr(pre), z_stride,
-                                      _stream_handle(stream, X.device)))
+    _launch(lib.kmeans_linear, X.device, stream, X.data_ptr(), x_stride, W.data_ptr(), w_stride,
+            bias, residual, r_stride, N, D, F, code, act, out.data_ptr(), y_stride, z, z_stride)
     return out if pre is None else (out, pre)
 
 
@@ -535,39 +555,37 @@ def kmeans_linear_grad(dY, X, W, Z=None, activation: str = "none", bias: bool = 
     else:
         Z = _flat(Z, "Z")
         z_stride = _rows(Z, "Z", like=X, shape=(N, F))
-    dX = torch.empty(x_shape, dtype=X.dtype, device=X.device) if need_dx else None
-    dW = torch.empty((F, D), dtype=X.dtype, device=X.device) if need_dw else None
-    db = torch.empty(F, dtype=X.dtype, device=X.device) if bias else None
+    dX = X.new_empty(x_shape) if need_dx else None
+    dW = X.new_empty((F, D)) if need_dw else None
+    db = X.new_empty(F) if bias else None
     lib = load_library()
-    with _on(X.device):
-        _check(lib, lib.kmeans_linear_grad(_ptr(dY), y_stride, _ptr(X), x_stride, _ptr(W),
-                                           w_stride, _ptr(Z), z_stride, N, D, F, code, act,
-                                           _ptr(dX), D, _ptr(dW), D, _ptr(db),
-                                           _stream_handle(stream, X.device)))
+    _launch(lib.kmeans_linear_grad, X.device, stream, dY.data_ptr(), y_stride, X.data_ptr(),
+            x_stride, W.data_ptr(), w_stride, _ptr(Z), z_stride, N, D, F, code, act, _ptr(dX), D,
+            _ptr(dW), D, _ptr(db))
     return dX, dW, db
 
 
 def _gradient_list(grads, out, device):
-    items = (_Gradient * max(len(grads), 1))()
-    for item, g, o in zip(items, grads, grads if out is None else out):
-        if not g.is_cuda or g.device != device or not g.is_contiguous():
+    """The list as kmeans_gradient_t entries: four 64-bit words each, the
+    last one the type (and the reserved half, zero)."""
+    index = device.index
+    words = []
+    for g, o in zip(grads, grads if out is None else out):
+        if g.get_device() != index or not g.is_contiguous():
             raise ValueError(f"gradients must be contiguous tensors on one GPU "
                              f"(got {g.device}, strides {g.stride()})")
-        if o is not g and (o.dtype != g.dtype or o.device != device or o.shape != g.shape
+        n = g.numel()
+        if o is not g and (o.dtype is not g.dtype or o.get_device() != index or o.numel() != n
                            or not o.is_contiguous()):
-            raise ValueError(f"out must match the gradients: {g.dtype}, {tuple(g.shape)}, "
+            raise ValueError(f"out must match the gradients: {g.dtype}, {n} elements, "
                              f"contiguous, on {device}")
-        item.src = g.data_ptr()
-        item.dst = o.data_ptr()
-        item.numel = g.numel()
-        item.dtype = _dtype(g, "gradients")
-    return items
+        words += (g.data_ptr(), o.data_ptr(), n, _dtype(g, "gradients"))
+    return array.array("q", words)
 
 
-def _norm_of(grads, norm, device):
+def _norm_of(grads, norm):
     import torch
-    if device is None:
-        device = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
+    device = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=device)
     return _vector(norm, "norm", torch.float32, 1, device), device
@@ -576,12 +594,11 @@ def _norm_of(grads, norm, device):
 def kmeans_gradient_norm(grads, norm=None, stream=None):
     """Global 2-norm of a list of contiguous gradients (bf16, fp16 and fp32
     mixed as they come): fp32 tensor of one element."""
-    norm, device = _norm_of(grads, norm, None)
+    norm, device = _norm_of(grads, norm)
     items = _gradient_list(grads, None, device)
     lib = load_library()
-    with _on(device):
-        _check(lib, lib.kmeans_gradient_norm(ctypes.byref(items), len(grads), _ptr(norm),
-                                             _stream_handle(stream, device)))
+    _launch(lib.kmeans_gradient_norm, device, stream, items.buffer_info()[0], len(grads),
+            norm.data_ptr())
     return norm
 
 
@@ -591,12 +608,11 @@ def kmeans_clip_gradients(grads, max_norm: float, out=None, norm=None, stream=No
     ``out``.  Returns ``(norm, clipped)``."""
     if out is not None and len(out) != len(grads):
         raise ValueError(f"out has {len(out)} tensors for {len(grads)} gradients")
-    norm, device = _norm_of(grads, norm, None)
+    norm, device = _norm_of(grads, norm)
     items = _gradient_list(grads, out, device)
     lib = load_library()
-    with _on(device):
-        _check(lib, lib.kmeans_clip_gradients(ctypes.byref(items), len(grads), max_norm,
-                                              _ptr(norm), _stream_handle(stream, device)))
+    _launch(lib.kmeans_clip_gradients, device, stream, items.buffer_info()[0], len(grads),
+            max_norm, norm.data_ptr())
     return norm, list(grads if out is None else out)
 
 

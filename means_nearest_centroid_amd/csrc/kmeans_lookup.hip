@@ -453,29 +453,33 @@ __device__ __forceinline__ int find_segments(const BucketArgs &bk, int b, Bucket
 }
 
 // Slot words of slots [s0, s0 + n) into sh.words (n <= kBucketCap): each slot
-// finds its tile by binary search, eight slots of a thread at a time.
+// finds its tile by binary search.  Most buckets need one slot a thread; the
+// loads of larger ones overlap four at a time.
 __device__ __forceinline__ void gather_words(const BucketArgs &bk, int s0, int n,
                                              BucketShared &sh) {
-    constexpr int kPer = kBucketCap / kRowThreads;
-    int v[kPer];
+    constexpr int kPer = 4;
+    for (int p0 = threadIdx.x; p0 < n; p0 += kPer * kRowThreads) {
+        int v[kPer];
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-        const int p = min(u * kRowThreads + static_cast<int>(threadIdx.x), n - 1);
-        int lo = 0, hi = bk.tiles - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sh.off[mid] <= s0 + p)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        if (u * kRowThreads < n)         // uniform: small buckets load once
+        for (int u = 0; u < kPer; ++u) {
+            const int p = p0 + u * kRowThreads;
+            if (p >= n)
+                break;
+            int lo = 0, hi = bk.tiles - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (sh.off[mid] <= s0 + p)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
             v[u] = bk.sidx[sh.src[lo] + (s0 + p - sh.off[lo])];
-    }
+        }
 #pragma unroll
-    for (int u = 0; u < kPer; ++u)
-        if (u * kRowThreads + static_cast<int>(threadIdx.x) < n)
-            sh.words[u * kRowThreads + threadIdx.x] = v[u];
+        for (int u = 0; u < kPer; ++u)
+            if (p0 + u * kRowThreads < n)
+                sh.words[p0 + u * kRowThreads] = v[u];
+    }
 }
 
 __device__ __forceinline__ int row_of(int word) {
@@ -651,7 +655,9 @@ template <typename T, typename O, int V>
 __global__ __launch_bounds__(kRowThreads, 4)
 void lookup_bucket_kernel(const GradArgs g, const BucketArgs bk) {
     __shared__ BucketShared sh;
-    const int b = blockIdx.x;
+    // Each XCD takes a contiguous range of buckets: its directory entries and
+    // slot words are neighbours in memory.
+    const int b = xcd_contiguous(blockIdx.x, bk.buckets);
     const int n = find_segments(bk, b, sh);
     if (n > bk.cap) {
         if (blockIdx.y == 0 && threadIdx.x == 0) {
@@ -711,19 +717,22 @@ void lookup_part_join_kernel(const GradArgs g, const BucketArgs bk) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const bool in = t0 + u * at.gp < h.parts;
-                const int64_t t = h.first_part + (in ? t0 + u * at.gp : t0);
-                len[u] = in ? bk.run_len[t * S + r] : 0;
-                if (at.cols.any)
-                    v[u] = load_packed<float, V>(bk.partial + (t * S + r) * g.D + at.cols.first);
+                len[u] = in ? bk.run_len[(h.first_part + t0 + u * at.gp) * S + r] : 0;
+                v[u] = Packed<float, V>{};
             }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (len[u] > 0) {                // else nothing was written there
-                    positions += len[u];
+            for (int u = 0; u < kBatch; ++u)     // else nothing was written there
+                if (len[u] > 0 && at.cols.any)
+                    v[u] = load_packed<float, V>(
+                        bk.partial + (static_cast<int64_t>(h.first_part + t0 + u * at.gp) * S + r) * g.D +
+                        at.cols.first);
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        sum[e] += v[u].v[e];
-                }
+            for (int u = 0; u < kBatch; ++u) {
+                positions += len[u];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    sum[e] += v[u].v[e];
+            }
         }
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -791,12 +800,12 @@ GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_unit
                    (1 << p.col_groups_log2) < p.slabs)
                 ++p.col_groups_log2;
         p.column_groups = (p.slabs + (1 << p.col_groups_log2) - 1) >> p.col_groups_log2;
-        // A part is 1024 positions of 256 bytes, fewer for wider slabs, and
+        // A part is 512 positions of 256 bytes, fewer for wider slabs, and
         // at least twice the mean bucket; larger where the partial sums would
         // take more than 256 MiB.  A heavy bucket has more than `cap`
         // positions, so its parts hold half of that each on average at least.
         const int64_t bytes = std::min(D, slab) * (V == 8 ? 2 : 4);
-        int64_t cap = std::max<int64_t>((int64_t(1) << 26) / (bytes * bytes),
+                int64_t cap = std::max<int64_t>((int64_t(1) << 25) / (bytes * bytes),
                                         2 * N / p.bins.buckets);
         cap = std::min<int64_t>(std::max(cap, kMinCap), kBucketCap);
         auto rows = [&] { return static_cast<size_t>(2 * N / cap + 1) << p.bins.bucket_log2; };
@@ -812,7 +821,7 @@ GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_unit
         return p;
     }
     // Chunks of at least 8 positions, more when that leaves eight waves or
-    // more per CU.
+    // more per CU (four: 3% slower at 200000 x 64 of 100 rows; two: 38%).
     const int64_t waves_at_1 = ((N << p.lanes_log2) + 63) / 64 * p.slabs;
     int64_t chunk = 8;
     while (chunk < 4096 && waves_at_1 / (2 * chunk) >= 8 * compute_units)

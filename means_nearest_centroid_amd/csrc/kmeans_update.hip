@@ -951,21 +951,6 @@ void upd_bin_kernel(const L *__restrict__ labels, int N, int K, int s_log2, int 
     }
 }
 
-// Workgroups are dispatched to the eight XCDs in turn (workgroup i to XCD
-// i mod 8), and each XCD has its own L2.  Mapping workgroup i to item
-// start(x) + i / 8 (x = i mod 8, XCD x owning the contiguous items
-// [start(x), start(x + 1))) gives each XCD a contiguous range of buckets, so
-// the directory lines and sorted-index lines it reads are its own eighth of
-// them instead of lines shared with every other XCD.  A bijection on
-// [0, n) for any n.
-__device__ __forceinline__ int xcd_contiguous(int i, int n) {
-    constexpr int kXcds = 8;
-    const int x = i % kXcds;
-    const int q = n / kXcds;
-    const int r = n % kXcds;
-    return x * q + min(x, r) + i / kXcds;
-}
-
 // Bucket b's slot words (point index, cluster in bucket) in slot order,
 // i.e. tile order, for a workgroup of kBucketThreads threads; every thread
 // calls it.  A bucket of at most kBucketSlots points gets all its words in

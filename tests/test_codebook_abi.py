@@ -95,8 +95,14 @@ def test_linear_grad_refuses(lib, kw, status):
     assert lib.kmeans_last_error().decode()
 
 
+class Gradient(ctypes.Structure):
+    """kmeans_gradient_t."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def gradient(src=0x10000, dst=0x20000, numel=8, dtype=0, reserved=0):
-    g = (km._Gradient * 1)()
+    g = (Gradient * 1)()
     g[0].src, g[0].dst, g[0].numel, g[0].dtype, g[0].reserved = src, dst, numel, dtype, reserved
     return g
 
