@@ -9,7 +9,10 @@
 // batches of kBatch tensors.  Pass 1: a fixed set of workgroups walks fixed
 // chunks of the batch's tensors, each leaving one fp64 partial sum.  Pass 2:
 // every workgroup adds all partial sums in one fixed order, so all of them
-// derive the same factor without a third launch, and scales its chunks.
+// derive the same factor without a third launch, and scales its chunks.  A
+// list of at most kSmallBytes is one launch of one workgroup, its waves taking
+// the chunks: both passes are a few microseconds there, no more than the second
+// launch costs.
 // Squares are summed in fp64: no fp32 value over- or underflows there, and
 // the conversions and additions stay far below the memory time.
 #include <math.h>
@@ -25,8 +28,11 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kBatch = 96;                 // tensors per launch: 2.8 KiB of arguments
-constexpr int kChunkBytes = 32768;         // of the source, per workgroup step
-constexpr int kLoads = kChunkBytes / 16 / kClipThreads;   // 16-byte loads of a thread in flight
+constexpr int kLoads = 8;                  // 16-byte loads of a thread in flight
+// Bytes of a source that `threads` threads take as one chunk.
+constexpr int chunk_bytes(int threads) { return kLoads * 16 * threads; }
+constexpr int kSmallThreads = 1024;        // waves of the one-workgroup kernel: 16
+constexpr int64_t kSmallBytes = 524288;
 constexpr int64_t kMaxPartials = 2048;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 
@@ -61,8 +67,9 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // The workgroup's total, on every thread.
+template <int THREADS>
 __device__ __forceinline__ double group_sum(double v) {
-    __shared__ double total[kClipThreads / 64];
+    __shared__ double total[THREADS / 64];
     v = wave_sum(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0)
@@ -70,18 +77,20 @@ __device__ __forceinline__ double group_sum(double v) {
     __syncthreads();
     double s = 0.0;
 #pragma unroll
-    for (int w = 0; w < kClipThreads / 64; ++w)
+    for (int w = 0; w < THREADS / 64; ++w)
         s += total[w];
     return s;
 }
 
 // Chunk `c` of a tensor: elements [c E, min(numel, (c + 1) E)), E = elements
-// of kChunkBytes.  Each thread holds kLoads runs of V elements.
-template <typename T>
-__device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c, double (&s)[4]) {
+// of chunk_bytes(THREADS); `tid` of THREADS threads holds kLoads runs of V
+// elements.
+template <typename T, int THREADS>
+__device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c, int tid,
+                                          double (&s)[4]) {
     typedef typename T::bits B;
     constexpr int V = 16 / sizeof(B);
-    constexpr int E = kChunkBytes / sizeof(B);
+    constexpr int E = chunk_bytes(THREADS) / sizeof(B);
     const int64_t beg = static_cast<int64_t>(c) * E;
     const int left = static_cast<int>(min(static_cast<int64_t>(E), numel - beg));
     const B *p = static_cast<const B *>(src) + beg;
@@ -96,13 +105,13 @@ __device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c,
         Packed<B, V> v[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            v[u] = load_packed<B, V>(p + (u * kClipThreads + threadIdx.x) * V);
+            v[u] = load_packed<B, V>(p + (u * THREADS + tid) * V);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
             add(v[u]);
         return;
     }
-    for (int at = threadIdx.x * V; at < left; at += kClipThreads * V) {
+    for (int at = tid * V; at < left; at += THREADS * V) {
         if (at + V <= left) {
             add(load_packed<B, V>(p + at));
         } else {
@@ -114,12 +123,12 @@ __device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c,
     }
 }
 
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t numel, int c,
-                                            float factor) {
+                                            int tid, float factor) {
     typedef typename T::bits B;
     constexpr int V = 16 / sizeof(B);
-    constexpr int E = kChunkBytes / sizeof(B);
+    constexpr int E = chunk_bytes(THREADS) / sizeof(B);
     const int64_t beg = static_cast<int64_t>(c) * E;
     const int left = static_cast<int>(min(static_cast<int64_t>(E), numel - beg));
     const B *p = static_cast<const B *>(src) + beg;
@@ -135,13 +144,13 @@ __device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t 
         Packed<B, V> v[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            v[u] = load_packed<B, V>(p + (u * kClipThreads + threadIdx.x) * V);
+            v[u] = load_packed<B, V>(p + (u * THREADS + tid) * V);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            put((u * kClipThreads + threadIdx.x) * V, v[u]);
+            put((u * THREADS + tid) * V, v[u]);
         return;
     }
-    for (int at = threadIdx.x * V; at < left; at += kClipThreads * V) {
+    for (int at = tid * V; at < left; at += THREADS * V) {
         if (at + V <= left)
             put(at, load_packed<B, V>(p + at));
         else
@@ -150,20 +159,43 @@ __device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t 
     }
 }
 
+// Chunk c of the batch, by its tensor's type.
+template <int THREADS>
+__device__ __forceinline__ void sum_any(const Batch &b, int c, int tid, double (&s)[4]) {
+    const int t = tensor_of(b, c);
+    const int in = c - b.first[t];
+    if (b.dtype[t] == KMEANS_BF16)
+        sum_chunk<Bf16, THREADS>(b.src[t], b.numel[t], in, tid, s);
+    else if (b.dtype[t] == KMEANS_FP16)
+        sum_chunk<Fp16, THREADS>(b.src[t], b.numel[t], in, tid, s);
+    else
+        sum_chunk<Fp32, THREADS>(b.src[t], b.numel[t], in, tid, s);
+}
+template <int THREADS>
+__device__ __forceinline__ void scale_any(const Batch &b, int c, int tid, float factor) {
+    const int t = tensor_of(b, c);
+    const int in = c - b.first[t];
+    if (factor == 1.0f && b.src[t] == b.dst[t])
+        return;                                          // nothing changes
+    if (b.dtype[t] == KMEANS_BF16)
+        scale_chunk<Bf16, THREADS>(b.src[t], b.dst[t], b.numel[t], in, tid, factor);
+    else if (b.dtype[t] == KMEANS_FP16)
+        scale_chunk<Fp16, THREADS>(b.src[t], b.dst[t], b.numel[t], in, tid, factor);
+    else
+        scale_chunk<Fp32, THREADS>(b.src[t], b.dst[t], b.numel[t], in, tid, factor);
+}
+
+__device__ __forceinline__ float clip_factor(float n, float max_norm) {
+    const float ratio = max_norm / (n + 1e-6f);
+    return ratio > 1.0f ? 1.0f : ratio;                  // a NaN stays
+}
+
 __global__ __launch_bounds__(kClipThreads)
 void clip_norm_kernel(const Batch b, double *__restrict__ partial) {
     double s[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
-        const int t = tensor_of(b, c);
-        const int in = c - b.first[t];
-        if (b.dtype[t] == KMEANS_BF16)
-            sum_chunk<Bf16>(b.src[t], b.numel[t], in, s);
-        else if (b.dtype[t] == KMEANS_FP16)
-            sum_chunk<Fp16>(b.src[t], b.numel[t], in, s);
-        else
-            sum_chunk<Fp32>(b.src[t], b.numel[t], in, s);
-    }
-    const double total = group_sum((s[0] + s[1]) + (s[2] + s[3]));
+    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x)
+        sum_any<kClipThreads>(b, c, threadIdx.x, s);
+    const double total = group_sum<kClipThreads>((s[0] + s[1]) + (s[2] + s[3]));
     if (threadIdx.x == 0)
         partial[b.first_partial + blockIdx.x] = total;
 }
@@ -173,7 +205,7 @@ __device__ __forceinline__ float total_norm(const double *partial, int partials)
     double v = 0.0;
     for (int i = threadIdx.x; i < partials; i += kClipThreads)
         v += partial[i];
-    return static_cast<float>(sqrt(group_sum(v)));
+    return static_cast<float>(sqrt(group_sum<kClipThreads>(v)));
 }
 
 __global__ __launch_bounds__(kClipThreads)
@@ -182,20 +214,9 @@ void clip_scale_kernel(const Batch b, const double *__restrict__ partial, int pa
     const float n = total_norm(partial, partials);
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
         *norm = n;
-    const float ratio = max_norm / (n + 1e-6f);
-    const float factor = ratio > 1.0f ? 1.0f : ratio;     // a NaN stays
-    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
-        const int t = tensor_of(b, c);
-        const int in = c - b.first[t];
-        if (factor == 1.0f && b.src[t] == b.dst[t])
-            continue;                                      // nothing changes
-        if (b.dtype[t] == KMEANS_BF16)
-            scale_chunk<Bf16>(b.src[t], b.dst[t], b.numel[t], in, factor);
-        else if (b.dtype[t] == KMEANS_FP16)
-            scale_chunk<Fp16>(b.src[t], b.dst[t], b.numel[t], in, factor);
-        else
-            scale_chunk<Fp32>(b.src[t], b.dst[t], b.numel[t], in, factor);
-    }
+    const float factor = clip_factor(n, max_norm);
+    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x)
+        scale_any<kClipThreads>(b, c, threadIdx.x, factor);
 }
 
 __global__ __launch_bounds__(kClipThreads)
@@ -206,9 +227,49 @@ void clip_finish_kernel(const double *__restrict__ partial, int partials,
         *norm = n;
 }
 
-int64_t chunks_of(const kmeans_gradient_t &t) {
-    const int64_t per = kChunkBytes / static_cast<int64_t>(dtype_size(t.dtype));
+// A small list at once: each wave takes every 16th chunk, in both passes.
+__global__ __launch_bounds__(kSmallThreads)
+void clip_small_kernel(const Batch b, int clip, float max_norm, float *__restrict__ norm) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    constexpr int kWaves = kSmallThreads / 64;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int c = wave; c < b.first[b.count]; c += kWaves)
+        sum_any<64>(b, c, lane, s);
+    const float n = static_cast<float>(
+        sqrt(group_sum<kSmallThreads>((s[0] + s[1]) + (s[2] + s[3]))));
+    if (threadIdx.x == 0)
+        *norm = n;
+    if (clip == 0)
+        return;
+    const float factor = clip_factor(n, max_norm);
+    for (int c = wave; c < b.first[b.count]; c += kWaves)
+        scale_any<64>(b, c, lane, factor);
+}
+
+int64_t chunks_of(const kmeans_gradient_t &t, int threads) {
+    const int64_t per = chunk_bytes(threads) / static_cast<int64_t>(dtype_size(t.dtype));
     return (t.numel + per - 1) / per;
+}
+
+// The next batch of the list from entry i on (empty tensors left out), chunks
+// as `threads` threads take them.
+int64_t fill_batch(Batch &b, const kmeans_gradient_t *list, int64_t count, int64_t &i,
+                   int threads) {
+    int64_t chunks = 0;
+    b.count = 0;
+    for (; i < count && b.count < kBatch; ++i) {
+        const kmeans_gradient_t &t = list[i];
+        if (t.numel == 0)
+            continue;
+        b.src[b.count] = t.src;
+        b.dst[b.count] = t.dst;
+        b.numel[b.count] = t.numel;
+        b.dtype[b.count] = static_cast<uint8_t>(t.dtype);
+        b.first[b.count++] = static_cast<int>(chunks);
+        chunks += chunks_of(t, threads);
+    }
+    b.first[b.count] = static_cast<int>(chunks);
+    return chunks;
 }
 
 kmeans_status_t check_list(const kmeans_gradient_t *list, int64_t count, bool clip,
@@ -254,10 +315,22 @@ kmeans_status_t run_clip(const kmeans_gradient_t *list, int64_t count, bool clip
     kmeans_status_t st = check_list(list, count, clip, norm);
     if (st != KMEANS_OK)
         return st;
-    int64_t total = 0, tensors = 0;
+    int64_t total = 0, tensors = 0, bytes = 0;
     for (int64_t i = 0; i < count; ++i) {
-        total += chunks_of(list[i]);
+        total += chunks_of(list[i], kClipThreads);
         tensors += list[i].numel > 0;
+        bytes += list[i].numel * static_cast<int64_t>(dtype_size(list[i].dtype));
+    }
+    if (bytes <= kSmallBytes && tensors <= kBatch) {
+        Batch b;
+        int64_t i = 0;
+        fill_batch(b, list, count, i, 64);
+        hipLaunchKernelGGL(clip_small_kernel, dim3(1), dim3(kSmallThreads), 0, stream, b,
+                           static_cast<int>(clip), max_norm, norm);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return fail(KMEANS_ERR_HIP, "clip launch failed: %s", hipGetErrorString(e));
+        return ok();
     }
     const int64_t batches = (tensors + kBatch - 1) / kBatch;
     // Each batch gets its share of the workgroups, by chunks, and one at least.
@@ -273,23 +346,10 @@ kmeans_status_t run_clip(const kmeans_gradient_t *list, int64_t count, bool clip
         int used = 0;
         while (i < count) {
             Batch b;
-            b.count = 0;
             b.first_partial = used;
-            int64_t chunks = 0;
-            for (; i < count && b.count < kBatch; ++i) {
-                const kmeans_gradient_t &t = list[i];
-                if (t.numel == 0)
-                    continue;
-                b.src[b.count] = t.src;
-                b.dst[b.count] = t.dst;
-                b.numel[b.count] = t.numel;
-                b.dtype[b.count] = static_cast<uint8_t>(t.dtype);
-                b.first[b.count++] = static_cast<int>(chunks);
-                chunks += chunks_of(t);
-            }
+            const int64_t chunks = fill_batch(b, list, count, i, kClipThreads);
             if (b.count == 0)
                 break;
-            b.first[b.count] = static_cast<int>(chunks);
             const int64_t share =
                 total <= kMaxPartials ? chunks : std::max<int64_t>(1, chunks * kMaxPartials / total);
             if (pass == 0)
@@ -306,7 +366,7 @@ kmeans_status_t run_clip(const kmeans_gradient_t *list, int64_t count, bool clip
         }
         partials = used;
     }
-    if (!clip || partials == 0) {
+    if (!clip) {
         hipLaunchKernelGGL(clip_finish_kernel, dim3(1), dim3(kClipThreads), 0, stream, partial,
                            partials, norm);
         const hipError_t e = hipGetLastError();

@@ -399,14 +399,18 @@ struct Reader {
     }
 };
 
-// Output tile of workgroup b: XCD x = b % 8 takes a contiguous eighth of the
-// tiles (each XCD has its own L2), ordered in bands of 8 tile rows so that
-// the tiles in flight together share rows of both operands.
-__device__ __forceinline__ void tile_of(int b, int ni, int nj, int &ti, int &tj) {
+// Split and output tile of workgroup b: XCD x = b % 8 takes a contiguous eighth
+// of the (split, tile) pairs (each XCD has its own L2), the tiles of a split in
+// bands of 8 tile rows, so that the tiles in flight together share rows of both
+// operands.
+__device__ __forceinline__ void tile_of(int b, int ni, int nj, int splits, int &split, int &ti,
+                                        int &tj) {
     constexpr int kBand = 8;
-    const int n = ni * nj;
+    const int tiles = ni * nj, n = tiles * splits;
     const int x = b & 7, q = n >> 3, rem = n & 7;
-    const int t = x * q + min(x, rem) + (b >> 3);
+    int t = x * q + min(x, rem) + (b >> 3);
+    split = t / tiles;
+    t -= split * tiles;
     const int band = t / (kBand * nj);
     const int i0 = band * kBand;
     const int h = min(kBand, ni - i0);
@@ -465,11 +469,11 @@ void linear_tile_kernel(const Product g) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ni = (g.I + RI - 1) / RI, nj = (g.J + RJ - 1) / RJ;
-    int ti, tj;
-    tile_of(blockIdx.x, ni, nj, ti, tj);
+    int split, ti, tj;
+    tile_of(blockIdx.x, ni, nj, g.splits, split, ti, tj);
     const int i0 = ti * RI, j0 = tj * RJ;
     const int wi = (wave % WI) * TI * 16, wj = (wave / WI) * TJ * 16;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.y) * g.k_chunk;
+    const int64_t k0 = static_cast<int64_t>(split) * g.k_chunk;
     const int k_len = static_cast<int>(min(static_cast<int64_t>(g.k_chunk), g.K - k0));
     const int tiles = (k_len + kTileK - 1) / kTileK;
 
@@ -604,7 +608,7 @@ void linear_tile_kernel(const Product g) {
 
     const int l = lane & 15, g4 = lane >> 4;
     if (g.splits > 1) {
-        float *part = g.partial + static_cast<int64_t>(blockIdx.y) * g.I * g.J;
+        float *part = g.partial + static_cast<int64_t>(split) * g.I * g.J;
 #pragma unroll
         for (int a = 0; a < TI; ++a) {
             const int i = i0 + wi + a * 16 + l;
@@ -837,8 +841,10 @@ void linear_rows_kernel(const Product g) {
 // 16-byte aligned), and the column sums of the unrounded dZ over this
 // workgroup's rows.  A lane owns eight columns; the workgroup's 256 lanes
 // cover `lanes` groups of eight columns (a power of two) and 256 / lanes rows
-// at a time.  The sums of the row groups meet in LDS in a fixed order.
+// at a time, kDzRows of them in flight per lane.  The sums of the row groups
+// meet in LDS in a fixed order.  dZ == null: the sums alone.
 constexpr int kDzThreads = 256;
+constexpr int kDzRows = 4;
 template <typename T>
 __global__ __launch_bounds__(kDzThreads)
 void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp, int N, int F,
@@ -854,26 +860,44 @@ void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp,
     const int r_end = min(N, r_first + rows_per_wg);
     const int n = F - c0;     // columns that exist (may be <= 0)
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (n > 0) {
-        for (int r = r_first + (tid >> lanes_log2); r < r_end; r += groups) {
-            const B *y = static_cast<const B *>(dY) + r * ldy + c0;
-            const B *z = static_cast<const B *>(pre) + r * ldp + c0;
-            const Packed<B, 8> d = load_run<B, 8>(y, n);
-            Packed<B, 8> zz = {};
-            if (act != KMEANS_ACT_NONE)
-                zz = load_run<B, 8>(z, n);
-            float v[8];
+    auto put = [&](int64_t r, const Packed<B, 8> &d, const Packed<B, 8> &z) KM_INLINE {
+        float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = activate_grad(act, T::widen(zz.v[e]), T::widen(d.v[e]));
-                s[e] += v[e];
+        for (int e = 0; e < 8; ++e) {
+            v[e] = activate_grad(act, T::widen(z.v[e]), T::widen(d.v[e]));
+            s[e] += v[e];
+        }
+        if (dZ != nullptr)    // the row's padding may be written
+            *reinterpret_cast<u32x4 *>(static_cast<B *>(dZ) + r * ldz + c0) =
+                __builtin_bit_cast(u32x4, narrow_run<T, 8>(v));
+    };
+    const B *y = static_cast<const B *>(dY) + c0, *z = static_cast<const B *>(pre) + c0;
+    int r = r_first + (tid >> lanes_log2);
+    if (n >= 8) {
+        for (; r + (kDzRows - 1) * groups < r_end; r += kDzRows * groups) {
+            Packed<B, 8> d[kDzRows], p[kDzRows];
+#pragma unroll
+            for (int u = 0; u < kDzRows; ++u) {
+                d[u] = load_packed<B, 8>(y + (r + u * groups) * ldy);
+                p[u] = Packed<B, 8>{};
             }
-            if (dZ != nullptr) {
-                B *w = static_cast<B *>(dZ) + r * ldz + c0;   // the row's padding may be written
-                *reinterpret_cast<u32x4 *>(w) = __builtin_bit_cast(u32x4, narrow_run<T, 8>(v));
+            if (act != KMEANS_ACT_NONE) {
+#pragma unroll
+                for (int u = 0; u < kDzRows; ++u)
+                    p[u] = load_packed<B, 8>(z + (r + u * groups) * ldp);
             }
+#pragma unroll
+            for (int u = 0; u < kDzRows; ++u)
+                put(r + u * groups, d[u], p[u]);
         }
     }
+    if (n > 0)
+        for (; r < r_end; r += groups) {
+            Packed<B, 8> p = {};
+            if (act != KMEANS_ACT_NONE)
+                p = load_run<B, 8>(z + r * ldp, n);
+            put(r, load_run<B, 8>(y + r * ldy, n), p);
+        }
     if (col_partial == nullptr)
         return;
 #pragma unroll
@@ -891,23 +915,34 @@ void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp,
     }
 }
 
-// db[j] = sum of the column partials: one workgroup per 16 columns, 16 threads
-// a column, each a fixed interleaved share of the rows, joined in LDS.
-constexpr int kBiasThreads = 256;
+// db[j] = sum of the column partials: a workgroup takes 32 columns, 32 threads
+// a column, each a fixed interleaved share of the rows (kBiasBatch in flight),
+// joined in LDS.
+constexpr int kBiasThreads = 1024;
+constexpr int kBiasCols = 32;
+constexpr int kBiasBatch = 8;
 template <typename T>
 __global__ __launch_bounds__(kBiasThreads)
 void linear_bias_kernel(const float *col_partial, int rows, int F, void *db) {
-    __shared__ float sums[16][17];
-    const int c = threadIdx.x & 15, w = threadIdx.x >> 4;
-    const int col = blockIdx.x * 16 + c;
+    constexpr int kShares = kBiasThreads / kBiasCols;
+    __shared__ float sums[kShares][kBiasCols + 1];
+    const int c = threadIdx.x % kBiasCols, w = threadIdx.x / kBiasCols;
+    const int col = blockIdx.x * kBiasCols + c;
     float v = 0.0f;
     if (col < F)
-        for (int r = w; r < rows; r += 16)
-            v += col_partial[static_cast<int64_t>(r) * F + col];
+        for (int r0 = w; r0 < rows; r0 += kBiasBatch * kShares) {
+            float x[kBiasBatch];
+#pragma unroll
+            for (int u = 0; u < kBiasBatch; ++u)
+                x[u] = col_partial[static_cast<int64_t>(min(r0 + u * kShares, rows - 1)) * F + col];
+#pragma unroll
+            for (int u = 0; u < kBiasBatch; ++u)
+                v += r0 + u * kShares < rows ? x[u] : 0.0f;
+        }
     sums[w][c] = v;
     __syncthreads();
     if (w == 0 && col < F) {
-        for (int q = 1; q < 16; ++q)
+        for (int q = 1; q < kShares; ++q)
             v += sums[q][c];
         static_cast<typename T::bits *>(db)[col] = T::narrow(v);
     }
@@ -998,7 +1033,7 @@ void plan_product(Product &g, int compute_units) {
 
 template <typename T, bool POWN, bool QOWN>
 hipError_t launch_product_modes(const Product &g, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(tiles_of(g, g.shape == kWide ? 256 : 128)), g.splits);
+    const dim3 grid(static_cast<unsigned>(tiles_of(g, g.shape == kWide ? 256 : 128) * g.splits));
     switch (g.shape) {
     case kWide:
         hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 8, 4, 2, true>), grid,
@@ -1125,8 +1160,8 @@ hipError_t run_grad(const GradPlan &p, const void *dY, int64_t dy_stride, const 
         e = hipGetLastError();
     }
     if (e == hipSuccess && dbias != nullptr) {
-        hipLaunchKernelGGL((linear_bias_kernel<T>), dim3((F + 15) / 16), dim3(kBiasThreads), 0,
-                           stream, reinterpret_cast<const float *>(ws + p.col_at), p.row_wgs, F,
+        hipLaunchKernelGGL((linear_bias_kernel<T>), dim3((F + kBiasCols - 1) / kBiasCols),
+                           dim3(kBiasThreads), 0, stream, reinterpret_cast<const float *>(ws + p.col_at), p.row_wgs, F,
                            dbias);
         e = hipGetLastError();
     }
@@ -1181,7 +1216,7 @@ extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const 
     g.K = static_cast<int>(D);
     g.epi = {bias, residual, residual_stride, Y, y_stride, pre, pre_stride, activation};
     g.dma = rows_aligned(X, x_stride) && rows_aligned(W, w_stride) && D % 8 == 0;
-    if (tiles_of(g, 128) > kMaxRows)
+    if (tiles_of(g, 128) > kMaxRows / kMaxKSplits)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x F=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(F));
     const int cus = device_compute_units();
@@ -1246,13 +1281,14 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
            (activation != KMEANS_ACT_NONE || !rows_aligned(dY, dy_stride) || F % 8 != 0);
     p.ldz = (F + 7) / 8 * 8;
     const int64_t col_groups = p.ldz / 8;
-    while (p.lanes_log2 < 8 && (1 << p.lanes_log2) < col_groups)
+    while (p.lanes_log2 < 6 && (1 << p.lanes_log2) < col_groups)
         ++p.lanes_log2;
     p.col_wgs = static_cast<int>((col_groups + (1 << p.lanes_log2) - 1) >> p.lanes_log2);
-    // About eight workgroups per CU, each at least four rounds of rows.
-    const int64_t rows_round = kDzThreads >> p.lanes_log2;
-    int64_t row_wgs = std::max<int64_t>(1, 8 * cus / p.col_wgs);
-    row_wgs = std::min<int64_t>(row_wgs, (N + 4 * rows_round - 1) / (4 * rows_round));
+    // About eight workgroups per CU, each at least one round of rows; few
+    // enough that the column partials stay small beside dY.
+    const int64_t rows_round = kDzRows * (kDzThreads >> p.lanes_log2);
+    int64_t row_wgs = std::min<int64_t>(512, std::max<int64_t>(1, 8 * cus / p.col_wgs));
+    row_wgs = std::min<int64_t>(row_wgs, (N + rows_round - 1) / rows_round);
     p.rows_per_wg = static_cast<int>((N + row_wgs - 1) / row_wgs);
     p.row_wgs = static_cast<int>((N + p.rows_per_wg - 1) / p.rows_per_wg);
 
@@ -1284,7 +1320,8 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
     // (zeros past F); W and X are read with D contiguous.
     p.dx.dma = rows_aligned(W, w_stride) && D % 8 == 0;
     p.dw.dma = rows_aligned(X, x_stride) && D % 8 == 0;
-    if (tiles_of(p.dx, 128) > kMaxRows || tiles_of(p.dw, 128) > kMaxRows)
+    if (tiles_of(p.dx, 128) > kMaxRows / kMaxKSplits ||
+        tiles_of(p.dw, 128) > kMaxRows / kMaxKSplits)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x D=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(D));
     size_t part = 0;
