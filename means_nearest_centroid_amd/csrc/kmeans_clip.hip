@@ -13,6 +13,9 @@
 // list of at most kSmallBytes is one launch of one workgroup, its waves taking
 // the chunks: both passes are a few microseconds there, no more than the second
 // launch costs.
+// 2^28 bf16 values out of place: 278 us (1.61 GB moved, 5.8 TB/s; the norm
+// alone 93 us); 322 with the second pass in the first one's order and plain
+// stores; 2048 or 4096 workgroups instead of 1024 within 2%.
 // Squares are summed in fp64: no fp32 value over- or underflows there, and
 // the conversions and additions stay far below the memory time.
 #include <math.h>
@@ -33,7 +36,7 @@ constexpr int kLoads = 8;                  // 16-byte loads of a thread in fligh
 constexpr int chunk_bytes(int threads) { return kLoads * 16 * threads; }
 constexpr int kSmallThreads = 1024;        // waves of the one-workgroup kernel: 16
 constexpr int64_t kSmallBytes = 524288;
-constexpr int64_t kMaxPartials = 2048;
+constexpr int64_t kMaxPartials = 1024;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 
 struct Batch {
@@ -83,24 +86,21 @@ __device__ __forceinline__ double group_sum(double v) {
 }
 
 // Chunk `c` of a tensor: elements [c E, min(numel, (c + 1) E)), E = elements
-// of chunk_bytes(THREADS); `tid` of THREADS threads holds kLoads runs of V
-// elements.
-template <typename T, int THREADS>
-__device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c, int tid,
-                                          double (&s)[4]) {
+// of chunk_bytes(THREADS); `tid` of THREADS threads takes kLoads runs of V
+// elements.  A whole chunk has all of them in flight together; one that the
+// tensor's end cuts short has kPartLoads, and its last elements (fewer than V)
+// go one to a thread.
+constexpr int kPartLoads = 4;
+
+template <typename T, int THREADS, typename Run, typename One>
+__device__ __forceinline__ void for_chunk(const void *src, int64_t numel, int c, int tid,
+                                          const Run &run, const One &one) {
     typedef typename T::bits B;
     constexpr int V = 16 / sizeof(B);
     constexpr int E = chunk_bytes(THREADS) / sizeof(B);
     const int64_t beg = static_cast<int64_t>(c) * E;
     const int left = static_cast<int>(min(static_cast<int64_t>(E), numel - beg));
     const B *p = static_cast<const B *>(src) + beg;
-    auto add = [&](const Packed<B, V> &v) __attribute__((always_inline)) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const double x = static_cast<double>(T::widen(v.v[e]));
-            s[e & 3] = fma(x, x, s[e & 3]);
-        }
-    };
     if (left == E) {
         Packed<B, V> v[kLoads];
 #pragma unroll
@@ -108,19 +108,43 @@ __device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c,
             v[u] = load_packed<B, V>(p + (u * THREADS + tid) * V);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            add(v[u]);
+            run(beg + (u * THREADS + tid) * V, v[u]);
         return;
     }
-    for (int at = tid * V; at < left; at += THREADS * V) {
-        if (at + V <= left) {
-            add(load_packed<B, V>(p + at));
-        } else {
-            for (int e = at; e < left; ++e) {
-                const double x = static_cast<double>(T::widen(p[e]));
-                s[0] = fma(x, x, s[0]);
-            }
-        }
+    const int whole = left / V * V;
+#pragma unroll 1
+    for (int at = tid * V; at < whole; at += kPartLoads * THREADS * V) {
+        Packed<B, V> v[kPartLoads];
+#pragma unroll
+        for (int u = 0; u < kPartLoads; ++u)
+            v[u] = load_packed<B, V>(p + min(at + u * THREADS * V, whole - V));
+#pragma unroll
+        for (int u = 0; u < kPartLoads; ++u)
+            if (at + u * THREADS * V < whole)
+                run(beg + at + u * THREADS * V, v[u]);
     }
+    if (whole + tid < left)
+        one(beg + whole + tid, p[whole + tid]);
+}
+
+template <typename T, int THREADS>
+__device__ __forceinline__ void sum_chunk(const void *src, int64_t numel, int c, int tid,
+                                          double (&s)[4]) {
+    typedef typename T::bits B;
+    constexpr int V = 16 / sizeof(B);
+    for_chunk<T, THREADS>(
+        src, numel, c, tid,
+        [&](int64_t, const Packed<B, V> &v) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const double x = static_cast<double>(T::widen(v.v[e]));
+                s[e & 3] = fma(x, x, s[e & 3]);
+            }
+        },
+        [&](int64_t, B b) __attribute__((always_inline)) {
+            const double x = static_cast<double>(T::widen(b));
+            s[0] = fma(x, x, s[0]);
+        });
 }
 
 template <typename T, int THREADS>
@@ -128,35 +152,21 @@ __device__ __forceinline__ void scale_chunk(const void *src, void *dst, int64_t 
                                             int tid, float factor) {
     typedef typename T::bits B;
     constexpr int V = 16 / sizeof(B);
-    constexpr int E = chunk_bytes(THREADS) / sizeof(B);
-    const int64_t beg = static_cast<int64_t>(c) * E;
-    const int left = static_cast<int>(min(static_cast<int64_t>(E), numel - beg));
-    const B *p = static_cast<const B *>(src) + beg;
-    B *o = static_cast<B *>(dst) + beg;
-    auto put = [&](int at, Packed<B, V> v) __attribute__((always_inline)) {
-        float x[V];
+    auto *o = static_cast<B *>(dst);
+    for_chunk<T, THREADS>(
+        src, numel, c, tid,
+        [&](int64_t at, const Packed<B, V> &v) __attribute__((always_inline)) {
+            float x[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            x[e] = T::widen(v.v[e]) * factor;
-        store_packed<B, V>(o + at, narrow_run<T, V>(x));
-    };
-    if (left == E) {
-        Packed<B, V> v[kLoads];
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u)
-            v[u] = load_packed<B, V>(p + (u * THREADS + tid) * V);
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u)
-            put((u * THREADS + tid) * V, v[u]);
-        return;
-    }
-    for (int at = tid * V; at < left; at += THREADS * V) {
-        if (at + V <= left)
-            put(at, load_packed<B, V>(p + at));
-        else
-            for (int e = at; e < left; ++e)
-                o[e] = T::narrow(T::widen(p[e]) * factor);
-    }
+            for (int e = 0; e < V; ++e)
+                x[e] = T::widen(v.v[e]) * factor;
+            // Past the caches, which leaves the rest of the sources there.
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, narrow_run<T, V>(x)),
+                                        reinterpret_cast<u32x4_any *>(o + at));
+        },
+        [&](int64_t at, B b) __attribute__((always_inline)) {
+            o[at] = T::narrow(T::widen(b) * factor);
+        });
 }
 
 // Chunk c of the batch, by its tensor's type.
@@ -215,7 +225,8 @@ void clip_scale_kernel(const Batch b, const double *__restrict__ partial, int pa
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
         *norm = n;
     const float factor = clip_factor(n, max_norm);
-    for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x)
+    // From the end: what the first pass read last is still in the caches.
+    for (int c = b.first[b.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x)
         scale_any<kClipThreads>(b, c, threadIdx.x, factor);
 }
 

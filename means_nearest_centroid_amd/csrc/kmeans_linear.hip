@@ -714,7 +714,17 @@ void linear_tile_kernel(const Product g) {
                             v[c] += T::widen(res[s].v[c]);
                     }
                 }
-                store_packed(static_cast<B *>(e.out) + i * e.ldo + j, narrow_run<T, 8>(v));
+                B *o = static_cast<B *>(e.out) + i * e.ldo + j;
+                const Packed<B, 8> y = narrow_run<T, 8>(v);
+                // Gradients of aligned rows go past the caches, which leaves
+                // the operands there (65536 x 512 x 128: 63 -> 56 us for both
+                // gradients); forward outputs do not (4096 x 4096 x 1000 37 us,
+                // 41 so; unaligned rows 26 and 31).
+                if constexpr (QOWN && DMA)
+                    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, y),
+                                                reinterpret_cast<u32x4_any *>(o));
+                else
+                    store_packed(o, y);
             }
         };
         if (!whole) {
@@ -745,34 +755,48 @@ void linear_tile_kernel(const Product g) {
     static_assert(TI <= 8, "two passes");
 }
 
-// Joins the splits of a product: each run of four outputs adds its partial
-// sums in split order (kJoinBatch loads in flight) and goes through the
-// epilogue.
+// Joins the splits of a product: the partial sums of a run of four outputs are
+// added by four threads, one of each wave (every fourth split each, kJoinBatch
+// loads in flight), whose sums meet in LDS; then the epilogue.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinRuns = 64;          // of one workgroup
 constexpr int kJoinBatch = 8;
 template <typename T>
 __global__ __launch_bounds__(kJoinThreads)
 void linear_join_kernel(const Product g) {
+    constexpr int kShares = kJoinThreads / kJoinRuns;
+    __shared__ f32x4 sums[kShares][kJoinRuns];
+    const int share = threadIdx.x / kJoinRuns, lane = threadIdx.x % kJoinRuns;
     const int runs = (g.J + 3) / 4;
     const int64_t total = static_cast<int64_t>(g.I) * runs;
     const int64_t plane = static_cast<int64_t>(g.I) * g.J;
-    for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; x < total;
-         x += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
+    for (int64_t x0 = static_cast<int64_t>(blockIdx.x) * kJoinRuns; x0 < total;
+         x0 += static_cast<int64_t>(gridDim.x) * kJoinRuns) {
+        const int64_t x = min(x0 + lane, total - 1);
         const int i = static_cast<int>(x / runs), j = static_cast<int>(x % runs) * 4;
         const float *p = g.partial + static_cast<int64_t>(i) * g.J + j;
-        float v[4] = {0, 0, 0, 0};
-        for (int s0 = 0; s0 < g.splits; s0 += kJoinBatch) {
+        f32x4 v = {0, 0, 0, 0};
+        for (int s0 = share; s0 < g.splits; s0 += kShares * kJoinBatch) {
             Packed<float, 4> w[kJoinBatch];
 #pragma unroll
             for (int u = 0; u < kJoinBatch; ++u)
-                w[u] = load_run<float, 4>(p + min(s0 + u, g.splits - 1) * plane, g.J - j);
+                w[u] = load_run<float, 4>(p + min(s0 + u * kShares, g.splits - 1) * plane, g.J - j);
 #pragma unroll
             for (int u = 0; u < kJoinBatch; ++u)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    v[c] += s0 + u < g.splits ? w[u].v[c] : 0.0f;
+                    v[c] += s0 + u * kShares < g.splits ? w[u].v[c] : 0.0f;
         }
-        finish_run<T, 4>(g.epi, i, j, g.J, v);
+        sums[share][lane] = v;
+        __syncthreads();
+        if (share == 0 && x0 + lane < total) {
+#pragma unroll
+            for (int q = 1; q < kShares; ++q)
+                v += sums[q][lane];
+            float y[4] = {v[0], v[1], v[2], v[3]};
+            finish_run<T, 4>(g.epi, i, j, g.J, y);
+        }
+        __syncthreads();
     }
 }
 
@@ -1056,7 +1080,7 @@ hipError_t launch_product_modes(const Product &g, hipStream_t stream) {
     if (e == hipSuccess && g.splits > 1) {
         const int64_t runs = static_cast<int64_t>(g.I) * ((g.J + 3) / 4);
         const unsigned wgs = static_cast<unsigned>(
-            std::min<int64_t>((runs + kJoinThreads - 1) / kJoinThreads, 4096));
+            std::min<int64_t>((runs + kJoinRuns - 1) / kJoinRuns, 4096));
         hipLaunchKernelGGL((linear_join_kernel<T>), dim3(wgs), dim3(kJoinThreads), 0, stream, g);
         e = hipGetLastError();
     }

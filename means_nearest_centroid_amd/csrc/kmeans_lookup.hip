@@ -62,8 +62,11 @@ __device__ __forceinline__ int table_row(L label, int K) {
 // of D >= V elements starts at D - V, so it may write elements of the piece
 // before it a second time (the same values) and no row needs a scalar tail.
 // Rows shorter than V move by elements.  Each thread moves kUnroll pieces
-// whose loads are in flight together.
-constexpr int kUnroll = 4;
+// whose loads are in flight together; the rows are written past the caches
+// (non-temporal), which leaves the table there.  262144 rows of 128 bf16 from
+// a table of 4096: 12.6 us a call (5.5 TB/s); 14.0 with four pieces, 17.8 with
+// eight, 15.4 with plain stores; 16384 rows of 4096 fp32 85 us instead of 98.
+constexpr int kUnroll = 2;
 template <typename T, int V, typename L>
 __global__ __launch_bounds__(kRowThreads)
 void lookup_kernel(const typename T::bits *__restrict__ C, int64_t ldc, const L *__restrict__ labels,
@@ -98,7 +101,9 @@ void lookup_kernel(const typename T::bits *__restrict__ C, int64_t ldc, const L 
             for (int e = 0; e < V; ++e)
                 x[e] = from[u] >= 0 ? scale * T::widen(v[u].v[e]) : 0.0f;
             if (row[u] < N)
-                store_packed<B, V>(Y + row[u] * ldy + col[u], narrow_run<T, V>(x));
+                __builtin_nontemporal_store(
+                    __builtin_bit_cast(u32x4_any, narrow_run<T, V>(x)),
+                    reinterpret_cast<u32x4_any *>(Y + row[u] * ldy + col[u]));
         }
     } else {
 #pragma unroll
