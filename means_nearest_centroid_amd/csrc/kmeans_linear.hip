@@ -650,9 +650,11 @@ void linear_tile_kernel(const Product g) {
     const int j = j0 + wj + c8 * 8;
     const int n = g.J - j;                              // columns that exist
     const int i_first = i0 + wi + lane / kRuns;
-    // Tiles whose columns all exist (nearly all) take whole-run accesses without
-    // a branch each; a tile at the right edge goes run by run.
-    const bool whole = j0 + RJ <= g.J;
+    // A run that the right edge cuts short is left to one last step, in which
+    // each lane finishes it for one row.
+    const bool whole = n >= 8;
+    const int cut = g.J % 8 == 0 ? -1 : (g.J / 8 * 8 - j0 - wj) / 8;     // run, uniform
+    const bool has_cut = g.J % 8 != 0 && g.J / 8 * 8 >= j0 + wj && cut < kRuns;
     float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (!QOWN && e.bias != nullptr && whole) {
         const Packed<B, 8> q = load_packed<B, 8>(static_cast<const B *>(e.bias) + j);
@@ -660,10 +662,10 @@ void linear_tile_kernel(const Product g) {
         for (int c = 0; c < 8; ++c)
             bias[c] = T::widen(q.v[c]);
     }
-    auto take = [&](int r, float (&v)[8]) KM_INLINE {
+    auto take = [&](int r, int run, float (&v)[8]) KM_INLINE {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(mine + spot(r, 2 * c8 + h));
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(mine + spot(r, 2 * run + h));
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 v[4 * h + c] = x[c];
@@ -698,8 +700,8 @@ void linear_tile_kernel(const Product g) {
             for (int s = 0; s < kSteps; ++s) {
                 const int i = i_pass + s * (64 / kRuns);
                 float v[8];
-                take(lane / kRuns + s * (64 / kRuns), v);
-                if (i >= g.I)
+                take(lane / kRuns + s * (64 / kRuns), c8, v);
+                if (i >= g.I || !whole)
                     continue;
                 if constexpr (!QOWN) {
 #pragma unroll
@@ -727,16 +729,7 @@ void linear_tile_kernel(const Product g) {
                     store_packed(o, y);
             }
         };
-        if (!whole) {
-#pragma unroll 1
-            for (int s = 0; s < kSteps; ++s) {
-                const int i = i_pass + s * (64 / kRuns);
-                float v[8];
-                take(lane / kRuns + s * (64 / kRuns), v);
-                if (i < g.I && n > 0)
-                    finish_run<T, 8>(e, i, j, g.J, v);
-            }
-        } else if constexpr (QOWN) {
+        if constexpr (QOWN) {
             finish(Index<KMEANS_ACT_NONE>{});
         } else {
             switch (e.act) {
@@ -746,6 +739,13 @@ void linear_tile_kernel(const Product g) {
             case KMEANS_ACT_SILU: finish(Index<KMEANS_ACT_SILU>{}); break;
             default: finish(Index<KMEANS_ACT_NONE>{}); break;
             }
+        }
+        if (has_cut) {
+            const int i = i0 + wi + half * 64 + lane;
+            float v[8];
+            take(lane, cut, v);
+            if (i < g.I)
+                finish_run<T, 8>(e, i, g.J / 8 * 8, g.J, v);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
@@ -869,10 +869,10 @@ void linear_rows_kernel(const Product g) {
 // meet in LDS in a fixed order.  dZ == null: the sums alone.
 constexpr int kDzThreads = 256;
 constexpr int kDzRows = 4;
-template <typename T>
+template <typename T, int ACT>
 __global__ __launch_bounds__(kDzThreads)
 void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp, int N, int F,
-                      int act, int lanes_log2, int rows_per_wg, void *dZ, int64_t ldz,
+                      int lanes_log2, int rows_per_wg, void *dZ, int64_t ldz,
                       float *col_partial) {
     typedef typename T::bits B;
     __shared__ float sums[kDzThreads][9];
@@ -888,7 +888,7 @@ void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp,
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            v[e] = activate_grad(act, T::widen(z.v[e]), T::widen(d.v[e]));
+            v[e] = activate_grad(ACT, T::widen(z.v[e]), T::widen(d.v[e]));
             s[e] += v[e];
         }
         if (dZ != nullptr)    // the row's padding may be written
@@ -905,7 +905,7 @@ void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp,
                 d[u] = load_packed<B, 8>(y + (r + u * groups) * ldy);
                 p[u] = Packed<B, 8>{};
             }
-            if (act != KMEANS_ACT_NONE) {
+            if (ACT != KMEANS_ACT_NONE) {
 #pragma unroll
                 for (int u = 0; u < kDzRows; ++u)
                     p[u] = load_packed<B, 8>(z + (r + u * groups) * ldp);
@@ -918,7 +918,7 @@ void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp,
     if (n > 0)
         for (; r < r_end; r += groups) {
             Packed<B, 8> p = {};
-            if (act != KMEANS_ACT_NONE)
+            if (ACT != KMEANS_ACT_NONE)
                 p = load_run<B, 8>(z + r * ldp, n);
             put(r, load_run<B, 8>(y + r * ldy, n), p);
         }
@@ -1177,11 +1177,22 @@ hipError_t run_grad(const GradPlan &p, const void *dY, int64_t dy_stride, const 
                     void *dbias, char *ws, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (p.dz || dbias != nullptr) {
-        hipLaunchKernelGGL((linear_dz_kernel<T>), dim3(p.row_wgs, p.col_wgs), dim3(kDzThreads), 0,
-                           stream, dY, dy_stride, pre, pre_stride, N, F, act, p.lanes_log2,
-                           p.rows_per_wg, p.dz ? ws + p.dz_at : nullptr, p.ldz,
-                           dbias != nullptr ? reinterpret_cast<float *>(ws + p.col_at) : nullptr);
-        e = hipGetLastError();
+        auto launch = [&](auto kind) {
+            hipLaunchKernelGGL((linear_dz_kernel<T, decltype(kind)::value>),
+                               dim3(p.row_wgs, p.col_wgs), dim3(kDzThreads), 0, stream, dY,
+                               dy_stride, pre, pre_stride, N, F, p.lanes_log2, p.rows_per_wg,
+                               p.dz ? ws + p.dz_at : nullptr, p.ldz,
+                               dbias != nullptr ? reinterpret_cast<float *>(ws + p.col_at)
+                                                : nullptr);
+            return hipGetLastError();
+        };
+        switch (act) {
+        case KMEANS_ACT_RELU: e = launch(Index<KMEANS_ACT_RELU>{}); break;
+        case KMEANS_ACT_GELU: e = launch(Index<KMEANS_ACT_GELU>{}); break;
+        case KMEANS_ACT_GELU_TANH: e = launch(Index<KMEANS_ACT_GELU_TANH>{}); break;
+        case KMEANS_ACT_SILU: e = launch(Index<KMEANS_ACT_SILU>{}); break;
+        default: e = launch(Index<KMEANS_ACT_NONE>{}); break;
+        }
     }
     if (e == hipSuccess && dbias != nullptr) {
         hipLaunchKernelGGL((linear_bias_kernel<T>), dim3((F + kBiasCols - 1) / kBiasCols),
