@@ -912,7 +912,8 @@ void linear_rows_kernel(const Product g) {
 // workgroup's rows.  A lane owns eight columns; the workgroup's 256 lanes
 // cover `lanes` groups of eight columns (a power of two) and 256 / lanes rows
 // at a time, kDzRows of them in flight per lane.  The sums of the row groups
-// meet in LDS in a fixed order.  dZ == null: the sums alone.
+// meet in LDS in a fixed order.  dZ == null: the sums alone.  Without an
+// activation and sums it lays rows out anew (Operand).
 constexpr int kDzThreads = 256;
 constexpr int kDzRows = 4;
 template <typename T, int ACT>
@@ -1029,6 +1030,8 @@ void linear_zero_kernel(uint16_t *p, int64_t rows, int cols, int64_t ld) {
 
 // ---- launch ----------------------------------------------------------------
 
+size_t align_up(size_t n) { return (n + 255) & ~size_t(255); }
+
 // Rows that DMA may read: 16-byte aligned base and stride.
 bool rows_aligned(const void *p, int64_t ld) {
     return aligned(p, 16) && ld % 8 == 0;
@@ -1063,8 +1066,9 @@ int64_t tiles_of(const Product &g, int side) {
            ((static_cast<int64_t>(g.J) + side - 1) / side);
 }
 
-// Chooses the shape and the splits of k with the least estimated time.
-void plan_product(Product &g, int compute_units) {
+// Chooses the shape and the splits of k with the least estimated time (us),
+// which it returns.
+double plan_product(Product &g, int compute_units) {
     const int64_t k_tiles = (g.K + kTileK - 1) / kTileK;
     struct Cost {
         Shape shape;
@@ -1076,7 +1080,7 @@ void plan_product(Product &g, int compute_units) {
     static constexpr Cost kAligned[] = {{kWide, 256, 1, 1.50, 1.50, 4.0},
                                         {kDeep, 128, 1, 0.50, 0.50, 2.0},
                                         {kPaired, 128, 2, 0.92, 0.65, 1.5}};
-    static constexpr Cost kOther[] = {{kUnaligned, 128, 2, 1.2, 0.8, 2.0}};
+    static constexpr Cost kOther[] = {{kUnaligned, 128, 2, 1.6, 1.1, 2.0}};
     const Cost *costs = g.dma ? kAligned : kOther;
     const int kinds = g.dma ? 3 : 1;
     double best = 1e30;
@@ -1087,8 +1091,10 @@ void plan_product(Product &g, int compute_units) {
             const int64_t per = (k_tiles + s - 1) / s;
             const int64_t wgs = tiles * ((k_tiles + per - 1) / per);
             const int64_t slots = static_cast<int64_t>(compute_units) * k.per_cu;
-            const double step = wgs <= compute_units ? k.single : k.round;
-            double t = static_cast<double>((wgs + slots - 1) / slots) * (per * step + k.fixed);
+            const int64_t rest = wgs % slots;       // workgroups of the last round
+            double t = static_cast<double>(wgs / slots) * (per * k.round + k.fixed);
+            if (rest > 0)
+                t += per * (rest <= compute_units ? k.single : k.round) + k.fixed;
             if (s > 1)    // the join's launch, and the partial sums written and read
                 t += 4.5 + static_cast<double>(s) * g.I * g.J * 8e-6 / 4.0;
             if (t < best) {
@@ -1099,6 +1105,87 @@ void plan_product(Product &g, int compute_units) {
             }
         }
     }
+    return best;
+}
+
+// How linear_dz_kernel divides N rows of F values.
+struct RowPlan {
+    int64_t ld;                 // values from one written row to the next
+    int lanes_log2, rows_per_wg, row_wgs, col_wgs;
+    RowPlan(int64_t N, int64_t F, int compute_units) : ld((F + 7) / 8 * 8), lanes_log2(0) {
+        const int64_t col_groups = ld / 8;
+        while (lanes_log2 < 6 && (1 << lanes_log2) < col_groups)
+            ++lanes_log2;
+        col_wgs = static_cast<int>((col_groups + (1 << lanes_log2) - 1) >> lanes_log2);
+        // About eight workgroups per CU, each at least one round of rows; few
+        // enough that the column partials stay small beside dY.
+        const int64_t rows_round = kDzRows * (kDzThreads >> lanes_log2);
+        int64_t wgs = std::min<int64_t>(512, std::max<int64_t>(1, 8 * compute_units / col_wgs));
+        wgs = std::min<int64_t>(wgs, (N + rows_round - 1) / rows_round);
+        rows_per_wg = static_cast<int>((N + wgs - 1) / wgs);
+        row_wgs = static_cast<int>((N + rows_per_wg - 1) / rows_per_wg);
+    }
+    size_t bytes(int64_t N) const { return align_up(static_cast<size_t>(N) * ld * 2); }
+};
+
+template <typename T, int ACT>
+hipError_t launch_dz(const RowPlan &r, const void *dY, int64_t ldy, const void *pre, int64_t ldp,
+                     int N, int F, void *dZ, float *col_partial, hipStream_t stream) {
+    hipLaunchKernelGGL((linear_dz_kernel<T, ACT>), dim3(r.row_wgs, r.col_wgs), dim3(kDzThreads), 0,
+                       stream, dY, ldy, pre, ldp, N, F, r.lanes_log2, r.rows_per_wg, dZ, r.ld,
+                       col_partial);
+    return hipGetLastError();
+}
+
+// An operand as its caller has it, and whether and where in the workspace it
+// is laid out anew, with rows that the global-to-LDS copies take.
+struct Operand {
+    const void *p;
+    int64_t ld, rows, cols;
+    bool moved;
+    size_t at;
+    bool fits() const { return rows_aligned(p, ld) && cols % 8 == 0; }
+};
+
+// Plans a product of operands, some of which may not fit the copies: as they
+// lie through registers (kUnaligned), or laid out anew first where that costs
+// less, at workspace offset `bytes` on (as it lies, moved: forward 4133 x 515 x
+// 1001 24 us, 33; 8192 x 2001 x 2000 140 us, 114; gradients 263 us, 198).
+void plan_operands(Product &g, Operand *const *ops, int n, int compute_units, size_t &bytes) {
+    double moves = 0;
+    g.dma = true;
+    for (int i = 0; i < n; ++i)
+        if (!ops[i]->fits()) {
+            g.dma = false;
+            moves += 5.0 + static_cast<double>(ops[i]->rows) * ops[i]->cols * 4e-6 / 2.5;
+        }
+    const double as_is = plan_product(g, compute_units);
+    if (g.dma)
+        return;
+    Product moved = g;
+    moved.dma = true;
+    if (plan_product(moved, compute_units) + moves >= as_is)
+        return;
+    g = moved;
+    for (int i = 0; i < n; ++i)
+        if (!ops[i]->fits()) {
+            ops[i]->moved = true;
+            ops[i]->at = bytes;
+            bytes += RowPlan(ops[i]->rows, ops[i]->cols, compute_units).bytes(ops[i]->rows);
+        }
+}
+
+// Lays the operand out anew if it was planned so, and points (p, ld) to it.
+template <typename T>
+hipError_t move_operand(const Operand &o, int compute_units, char *ws, const void *&p, int64_t &ld,
+                        hipStream_t stream) {
+    if (!o.moved)
+        return hipSuccess;
+    const RowPlan r(o.rows, o.cols, compute_units);
+    p = ws + o.at;
+    ld = r.ld;
+    return launch_dz<T, KMEANS_ACT_NONE>(r, o.p, o.ld, nullptr, 0, static_cast<int>(o.rows),
+                                         static_cast<int>(o.cols), ws + o.at, nullptr, stream);
 }
 
 template <typename T, bool POWN, bool QOWN>
@@ -1147,8 +1234,6 @@ hipError_t launch_product(const Product &g, Modes m, hipStream_t stream) {
     }
 }
 
-size_t align_up(size_t n) { return (n + 255) & ~size_t(255); }
-
 kmeans_status_t check_linear(int64_t N, int64_t D, int64_t F, int32_t dtype, int32_t activation) {
     if (N < 0 || D < 1 || F < 1)
         return fail(KMEANS_ERR_INVALID_ARG, "N=%lld must be >= 0, D=%lld and F=%lld >= 1",
@@ -1191,9 +1276,14 @@ kmeans_status_t check_vector(const char *name, const void *p) {
 }
 
 template <typename T>
-hipError_t run_forward(const Product &g, int compute_units, hipStream_t stream) {
-    if (g.shape != kRows)
-        return launch_product<T>(g, kForward, stream);
+hipError_t run_forward(Product g, const Operand &x, const Operand &w, int compute_units, char *ws,
+                       hipStream_t stream) {
+    if (g.shape != kRows) {
+        hipError_t e = move_operand<T>(x, compute_units, ws, g.P, g.ldp, stream);
+        if (e == hipSuccess)
+            e = move_operand<T>(w, compute_units, ws, g.Q, g.ldq, stream);
+        return e == hipSuccess ? launch_product<T>(g, kForward, stream) : e;
+    }
     // As many waves as D gives work to, while the CUs hold them (32 each).
     const dim3 grid((g.J + 15) / 16);
     int64_t waves = 4;
@@ -1211,26 +1301,22 @@ hipError_t run_forward(const Product &g, int compute_units, hipStream_t stream) 
 // The launches of kmeans_linear_grad on workspace `ws`.
 struct GradPlan {
     bool dz;                    // whether dZ is written (else dY stands for it)
-    int64_t ldz;
-    int lanes_log2, rows_per_wg, row_wgs, col_wgs;
+    RowPlan rows;
     size_t dz_at, col_at, part_at, bytes;
+    Operand x, w;
     Product dx, dw;
 };
 
 template <typename T>
-hipError_t run_grad(const GradPlan &p, const void *dY, int64_t dy_stride, const void *pre,
+hipError_t run_grad(GradPlan &p, int compute_units, const void *dY, int64_t dy_stride, const void *pre,
                     int64_t pre_stride, int N, int F, int act, bool want_dx, bool want_dw,
                     void *dbias, char *ws, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (p.dz || dbias != nullptr) {
         auto launch = [&](auto kind) {
-            hipLaunchKernelGGL((linear_dz_kernel<T, decltype(kind)::value>),
-                               dim3(p.row_wgs, p.col_wgs), dim3(kDzThreads), 0, stream, dY,
-                               dy_stride, pre, pre_stride, N, F, p.lanes_log2, p.rows_per_wg,
-                               p.dz ? ws + p.dz_at : nullptr, p.ldz,
-                               dbias != nullptr ? reinterpret_cast<float *>(ws + p.col_at)
-                                                : nullptr);
-            return hipGetLastError();
+            return launch_dz<T, decltype(kind)::value>(
+                p.rows, dY, dy_stride, pre, pre_stride, N, F, p.dz ? ws + p.dz_at : nullptr,
+                dbias != nullptr ? reinterpret_cast<float *>(ws + p.col_at) : nullptr, stream);
         };
         switch (act) {
         case KMEANS_ACT_RELU: e = launch(Index<KMEANS_ACT_RELU>{}); break;
@@ -1242,10 +1328,15 @@ hipError_t run_grad(const GradPlan &p, const void *dY, int64_t dy_stride, const 
     }
     if (e == hipSuccess && dbias != nullptr) {
         hipLaunchKernelGGL((linear_bias_kernel<T>), dim3((F + kBiasCols - 1) / kBiasCols),
-                           dim3(kBiasThreads), 0, stream, reinterpret_cast<const float *>(ws + p.col_at), p.row_wgs, F,
+                           dim3(kBiasThreads), 0, stream,
+                           reinterpret_cast<const float *>(ws + p.col_at), p.rows.row_wgs, F,
                            dbias);
         e = hipGetLastError();
     }
+    if (e == hipSuccess)
+        e = move_operand<T>(p.w, compute_units, ws, p.dx.Q, p.dx.ldq, stream);
+    if (e == hipSuccess)
+        e = move_operand<T>(p.x, compute_units, ws, p.dw.Q, p.dw.ldq, stream);
     if (e == hipSuccess && want_dx)
         e = launch_product<T>(p.dx, kInputGrad, stream);
     if (e == hipSuccess && want_dw)
@@ -1296,28 +1387,33 @@ extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const 
     g.J = static_cast<int>(F);
     g.K = static_cast<int>(D);
     g.epi = {bias, residual, residual_stride, Y, y_stride, pre, pre_stride, activation};
-    g.dma = rows_aligned(X, x_stride) && rows_aligned(W, w_stride) && D % 8 == 0;
     if (tiles_of(g, 128) > kMaxRows / kMaxKSplits)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x F=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(F));
     const int cus = device_compute_units();
+    Operand x{X, x_stride, N, D, false, 0}, w{W, w_stride, F, D, false, 0};
+    size_t bytes = 0;
     if (N <= kMaxFewRows) {
         g.shape = kRows;
         g.splits = 1;
     } else {
-        plan_product(g, cus);
+        Operand *const ops[] = {&x, &w};
+        plan_operands(g, ops, 2, cus, bytes);
     }
+    const size_t part_at = bytes;
+    bytes += partial_bytes(g);
     std::unique_ptr<WorkspaceLease> lease;
-    const size_t bytes = partial_bytes(g);
+    char *ws = nullptr;
     if (bytes > 0) {
         lease = std::make_unique<WorkspaceLease>(stream, bytes);
         if (lease->error() != hipSuccess)
             return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", bytes,
                         hipGetErrorString(lease->error()));
-        g.partial = static_cast<float *>(lease->ptr());
+        ws = static_cast<char *>(lease->ptr());
+        g.partial = reinterpret_cast<float *>(ws + part_at);
     }
-    const hipError_t e = dtype == KMEANS_BF16 ? run_forward<Bf16>(g, cus, stream)
-                                              : run_forward<Fp16>(g, cus, stream);
+    const hipError_t e = dtype == KMEANS_BF16 ? run_forward<Bf16>(g, x, w, cus, ws, stream)
+                                              : run_forward<Fp16>(g, x, w, cus, ws, stream);
     if (e != hipSuccess)
         return fail(KMEANS_ERR_HIP, "linear launch failed: %s", hipGetErrorString(e));
     return ok();
@@ -1355,36 +1451,24 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
         return ok();
 
     const int cus = device_compute_units();
-    GradPlan p{};
+    GradPlan p{false, RowPlan(N, F, cus), 0, 0, 0, 0, {X, x_stride, N, D, false, 0},
+               {W, w_stride, F, D, false, 0}, {}, {}};
     // dZ is dY itself without an activation, where its rows can be staged as
     // they lie; otherwise it is written once with rows of whole chunks.
     p.dz = (dX || dW) &&
            (activation != KMEANS_ACT_NONE || !rows_aligned(dY, dy_stride) || F % 8 != 0);
-    p.ldz = (F + 7) / 8 * 8;
-    const int64_t col_groups = p.ldz / 8;
-    while (p.lanes_log2 < 6 && (1 << p.lanes_log2) < col_groups)
-        ++p.lanes_log2;
-    p.col_wgs = static_cast<int>((col_groups + (1 << p.lanes_log2) - 1) >> p.lanes_log2);
-    // About eight workgroups per CU, each at least one round of rows; few
-    // enough that the column partials stay small beside dY.
-    const int64_t rows_round = kDzRows * (kDzThreads >> p.lanes_log2);
-    int64_t row_wgs = std::min<int64_t>(512, std::max<int64_t>(1, 8 * cus / p.col_wgs));
-    row_wgs = std::min<int64_t>(row_wgs, (N + rows_round - 1) / rows_round);
-    p.rows_per_wg = static_cast<int>((N + row_wgs - 1) / row_wgs);
-    p.row_wgs = static_cast<int>((N + p.rows_per_wg - 1) / p.rows_per_wg);
 
     const void *z = dY;
     int64_t ldz = dy_stride;
     size_t at = 0;
     if (p.dz) {
         p.dz_at = at;
-        at += align_up(static_cast<size_t>(N) * p.ldz * 2);
+        at += p.rows.bytes(N);
     }
     if (dbias) {
         p.col_at = at;
-        at += align_up(static_cast<size_t>(p.row_wgs) * F * sizeof(float));
+        at += align_up(static_cast<size_t>(p.rows.row_wgs) * F * sizeof(float));
     }
-    p.part_at = at;
     p.dx.ldq = w_stride;
     p.dx.I = static_cast<int>(N);
     p.dx.J = static_cast<int>(D);
@@ -1397,23 +1481,22 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
     p.dw.K = static_cast<int>(N);
     p.dw.Q = X;
     p.dw.epi = {nullptr, nullptr, 0, dW, dw_stride, nullptr, 0, KMEANS_ACT_NONE};
-    // dZ's rows may be read up to a whole chunk where they are the workspace's
-    // (zeros past F); W and X are read with D contiguous.
-    p.dx.dma = rows_aligned(W, w_stride) && D % 8 == 0;
-    p.dw.dma = rows_aligned(X, x_stride) && D % 8 == 0;
     if (tiles_of(p.dx, 128) > kMaxRows / kMaxKSplits ||
         tiles_of(p.dw, 128) > kMaxRows / kMaxKSplits)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x D=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(D));
+    // dZ fits the copies (zeros past F in its last chunk); X and W may not.
+    Operand *const w = &p.w, *const x = &p.x;
     size_t part = 0;
     if (dX) {
-        plan_product(p.dx, cus);
+        plan_operands(p.dx, &w, 1, cus, at);
         part = std::max(part, partial_bytes(p.dx));
     }
     if (dW) {
-        plan_product(p.dw, cus);
+        plan_operands(p.dw, &x, 1, cus, at);
         part = std::max(part, partial_bytes(p.dw));
     }
+    p.part_at = at;
     p.bytes = at + part;
     std::unique_ptr<WorkspaceLease> lease;
     char *ws = nullptr;
@@ -1426,17 +1509,17 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
     }
     if (p.dz) {
         z = ws + p.dz_at;
-        ldz = p.ldz;
+        ldz = p.rows.ld;
     }
     p.dx.P = p.dw.P = z;
     p.dx.ldp = p.dw.ldp = ldz;
     p.dx.partial = p.dw.partial = reinterpret_cast<float *>(ws + p.part_at);
     const hipError_t e =
         dtype == KMEANS_BF16
-            ? run_grad<Bf16>(p, dY, dy_stride, pre, pre_stride, static_cast<int>(N),
+            ? run_grad<Bf16>(p, cus, dY, dy_stride, pre, pre_stride, static_cast<int>(N),
                              static_cast<int>(F), activation, dX != nullptr, dW != nullptr, dbias,
                              ws, stream)
-            : run_grad<Fp16>(p, dY, dy_stride, pre, pre_stride, static_cast<int>(N),
+            : run_grad<Fp16>(p, cus, dY, dy_stride, pre, pre_stride, static_cast<int>(N),
                              static_cast<int>(F), activation, dX != nullptr, dW != nullptr, dbias,
                              ws, stream);
     if (e != hipSuccess)
