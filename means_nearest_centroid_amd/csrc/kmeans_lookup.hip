@@ -6,12 +6,12 @@
 // Both move rows and compute next to nothing: the bound is the bytes of the
 // rows, read once and written once.
 //
-// Gradient.  Two paths, by a rule on N and K alone.  In neither are there
+// Gradient.  Two paths, by a rule on N, K and the row's bytes.  In neither are there
 // floating-point atomics: the order of every sum follows from the labels.
 //
-// Buckets (K from 256 to 65536 and at most 1024 positions per bucket on
-// average): each tile of positions is sorted by bucket of up to 64 rows, as in
-// the centroid update.
+// Buckets (K up to 65536 and N up to 2^20, rows of 256 bytes or more, or 256
+// buckets of at most 1024 positions on average): each tile of positions is
+// sorted by bucket of up to 64 rows, as in the centroid update.
 //  1. lookup_bucket_kernel: one workgroup per bucket gathers its positions,
 //     sorts them by row in LDS (stably) and sums them; groups of lanes that
 //     together hold one row's columns each take an equal share of the sorted
@@ -779,9 +779,16 @@ struct GradPlan {
 
 size_t align_up(size_t n) { return (n + 255) & ~size_t(255); }
 
-constexpr int64_t kMinBucketRows = 256;                 // fewer buckets leave CUs idle
-constexpr int64_t kMaxBucketTable = int64_t(1024) * kMaxBucketRows;
+// Buckets pay where a row is wide enough to hide the gathering of its position
+// (256 bytes: 262144 x 1024 of 16 rows 129 us, sorted 210; 65536 x 128 of 255
+// 20 and 30; 4096 x 128 of 128 16 and 19), or where most of them are summed by
+// one workgroup and there are enough to fill the GPU (262144 x 32 of 250 rows
+// 69 us, sorted 37; 1000000 x 16 of 300 135 and 108).
+constexpr int64_t kWideRow = 256;                       // bytes
+constexpr int64_t kMinBucketRows = 256;
 constexpr int64_t kMaxMeanBucket = 1024;                // positions
+constexpr int64_t kMaxBucketTable = int64_t(1024) * kMaxBucketRows;
+constexpr int64_t kMaxBucketPositions = int64_t(1) << 20;
 constexpr int64_t kMinCap = 128;
 
 GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_units) {
@@ -792,9 +799,10 @@ GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_unit
     p.slabs = static_cast<int>((D + slab - 1) / slab);
     if (N == 0)
         return p;
-    if (K >= kMinBucketRows && K <= kMaxBucketTable && N <= kMaxMeanBucket * 1024) {
+    if (K <= kMaxBucketTable && N <= kMaxBucketPositions) {
         p.bins = make_label_bins(N, K);
-        p.by_buckets = N <= kMaxMeanBucket * p.bins.buckets;
+        p.by_buckets = D * (V == 8 ? 2 : 4) >= kWideRow ||
+                       (K >= kMinBucketRows && N <= kMaxMeanBucket * p.bins.buckets);
     }
     if (p.by_buckets) {
         // Few positions per bucket and wide rows: the groups of a workgroup
@@ -806,12 +814,13 @@ GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_unit
                 ++p.col_groups_log2;
         p.column_groups = (p.slabs + (1 << p.col_groups_log2) - 1) >> p.col_groups_log2;
         // A part is 512 positions of 256 bytes, fewer for wider slabs, and
-        // at least twice the mean bucket; larger where the partial sums would
-        // take more than 256 MiB.  A heavy bucket has more than `cap`
+        // at least twice the mean bucket if there is one for every CU; larger
+        // where the partial sums would take more than 256 MiB.  A heavy bucket has more than `cap`
         // positions, so its parts hold half of that each on average at least.
         const int64_t bytes = std::min(D, slab) * (V == 8 ? 2 : 4);
-                int64_t cap = std::max<int64_t>((int64_t(1) << 25) / (bytes * bytes),
-                                        2 * N / p.bins.buckets);
+        int64_t cap = (int64_t(1) << 25) / (bytes * bytes);
+        if (p.bins.buckets >= compute_units)
+            cap = std::max<int64_t>(cap, 2 * N / p.bins.buckets);
         cap = std::min<int64_t>(std::max(cap, kMinCap), kBucketCap);
         auto rows = [&] { return static_cast<size_t>(2 * N / cap + 1) << p.bins.bucket_log2; };
         while (cap < kBucketCap && rows() * D * sizeof(float) > (size_t(256) << 20))

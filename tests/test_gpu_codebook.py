@@ -167,6 +167,20 @@ def test_lookup_grad_of_frequent_labels(N, K, D, kind, accumulate):
     assert torch.equal(again, into)
 
 
+@pytest.mark.parametrize("N,K,D,kind", [
+    (5000, 1, 128, "one"), (129, 1, 2000, "one"), (6000, 3, 257, "uniform"),
+    (40000, 16, 128, "zipf"), (20000, 255, 136, "uniform"), (7, 2, 4096, "uniform"),
+    ((1 << 20) + 1, 5, 128, "uniform"), (3000, 100, 127, "zipf")])
+def test_lookup_grad_of_few_wide_rows(N, K, D, kind):
+    """Tables of fewer rows than the GPU has CUs, at the row width and the
+    number of positions where the path changes."""
+    dY = rand((N, D), BF, 41)
+    lab = some_labels(N, K, 42, torch.int32, kind)
+    want, bound = ref.lookup_grad(dY, lab, K, 1.5, F32)
+    got = km.kmeans_lookup_grad(dY, lab, K, scale=1.5, out=torch.empty(K, D, device="cuda"))
+    ref.check(got, want, bound, f"{N} {K} {D} {kind}")
+
+
 @pytest.mark.parametrize("dtype,out_dtype", [(BF, BF), (BF, F32), (FP, F32), (F32, F32)])
 @pytest.mark.parametrize("N,K,D", [(1000, 37, 16), (777, 300, 129), (3000, 2, 64), (50, 9, 515),
                                    (900, 270, 515), (40, 300, 5)])
