@@ -11,8 +11,9 @@
 // every workgroup adds all partial sums in one fixed order, so all of them
 // derive the same factor without a third launch, and scales its chunks.  A
 // list of at most kSmallBytes is one launch of one workgroup, its waves taking
-// the chunks: both passes are a few microseconds there, no more than the second
-// launch costs.
+// the chunks, which costs less there than a second launch (one launch, two: 60
+// KB 7.8 us, 10.5; 200 KB 9.5, 10.2; 400 KB 15.0, 10.1; 12 tensors of 200 KB,
+// bound by the host, 13.0, 16.0).
 // 2^28 bf16 values out of place: 278 us (1.61 GB moved, 5.8 TB/s; the norm
 // alone 93 us); 322 with the second pass in the first one's order and plain
 // stores; 2048 or 4096 workgroups instead of 1024 within 2%.
@@ -35,7 +36,7 @@ constexpr int kLoads = 8;                  // 16-byte loads of a thread in fligh
 // Bytes of a source that `threads` threads take as one chunk.
 constexpr int chunk_bytes(int threads) { return kLoads * 16 * threads; }
 constexpr int kSmallThreads = 1024;        // waves of the one-workgroup kernel: 16
-constexpr int64_t kSmallBytes = 524288;
+constexpr int64_t kSmallBytes = 320 << 10;
 constexpr int64_t kMaxPartials = 1024;
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 
