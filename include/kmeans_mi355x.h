@@ -328,8 +328,9 @@ kmeans_status_t kmeans_lookup(const void *C, int64_t c_stride, const void *label
  *   dC        [K][D] of `out_dtype` (`dtype` or KMEANS_FP32), rows dc_stride
  *             apart, written (accumulate: read and written).
  *
- * Scratch (about 16 bytes per label and 8 D bytes per 64 labels) is the
- * stream's workspace; KMEANS_ERR_NO_MEMORY if it cannot grow.
+ * Scratch is the stream's workspace: about 16 bytes per label, and fp32
+ * partial sums of rows (at most D bytes per label, or 256 MiB where that is
+ * more); KMEANS_ERR_NO_MEMORY if it cannot grow.
  */
 kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride, const void *labels,
                                    int32_t label_type, int64_t N, int64_t D, int64_t K,
@@ -351,8 +352,9 @@ kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride, const void
  *             KMEANS_ACT_NONE.
  *   N, D, F   0 <= N < 2^31, 1 <= D, F <= 2^20.
  *
- * Small N or few output tiles split the sum over D between workgroups; the
- * partial sums (fp32) are the stream's workspace.
+ * Small N or few output tiles split the sum over D between workgroups; their
+ * partial sums (fp32), and copies of large operands whose rows are not 16-byte
+ * aligned, are the stream's workspace.
  */
 kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const void *W, int64_t w_stride,
                               const void *bias, const void *residual, int64_t residual_stride,
@@ -375,8 +377,9 @@ kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const void *W, in
  *
  * dZ is rounded once to `dtype` (the matrix instructions take 16-bit
  * operands; an fp16 dZ past 65504 becomes infinite), dbias sums it
- * unrounded.  dZ and partial sums are the stream's workspace (2 bytes per
- * element of dY, and partial sums where few tiles fill the GPU).
+ * unrounded.  dZ (2 bytes per element of dY), partial sums where few tiles
+ * fill the GPU, and copies of large X and W whose rows are not 16-byte aligned
+ * are the stream's workspace.
  */
 kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride, const void *X,
                                    int64_t x_stride, const void *W, int64_t w_stride,

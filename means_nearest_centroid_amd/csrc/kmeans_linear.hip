@@ -479,6 +479,13 @@ __device__ __forceinline__ void tile_of(int b, int ni, int nj, int splits, int &
 // freed, both under the last phase's matrix instructions.  The stages are
 // distinct arrays and the loop is unrolled by S so that the compiler can tell
 // an LDS read of one stage from a copy into another.
+//
+// Bound by the matrix pipe where k is long (8192 x 4096 x 4096 forward 192 us,
+// 1430 TFLOP/s), and by the epilogue's bytes where it is short or the epilogue
+// has more to move: nothing overlaps it with one workgroup per CU.  16384 x
+// 4096 x 4096 with gelu, residual and pre-activations kept is 484 us, of which
+// about 37 are the residual, 24 the pre-activations and 10 to 20 the activation
+// (all residual loads ahead of both passes spill: 505).
 template <int I>
 using Index = std::integral_constant<int, I>;
 
@@ -765,8 +772,8 @@ void linear_tile_kernel(const Product g) {
                 B *o = static_cast<B *>(e.out) + i * e.ldo + j;
                 const Packed<B, 8> y = narrow_run<T, 8>(v);
                 // Gradients of aligned rows go past the caches, which leaves
-                // the operands there (65536 x 512 x 128: 63 -> 56 us for both
-                // gradients); forward outputs do not (4096 x 4096 x 1000 37 us,
+                // the operands there (65536 x 512 x 128: 56 us for both gradients,
+                // 63 with plain stores); forward outputs do not (4096 x 4096 x 1000 37 us,
                 // 41 so; unaligned rows 26 and 31).
                 if constexpr (QOWN && DMA)
                     __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, y),
@@ -853,9 +860,10 @@ void linear_join_kernel(const Product g) {
 // their sums in LDS in wave order.  kRowsUnroll matrix instructions' operands
 // are in flight per wave.  Loads are 16 bytes per lane at the rows' own
 // alignment; the last values of a row that is no multiple of 8 are loaded one
-// by one.  Against the tile kernels: 1 x 4096 x 4096 8.5 us per call (the
-// host's time) instead of 11.5, 16 rows 9.3 instead of 11.6, but 32 rows (two
-// row blocks) 12.9 instead of 12.7, so it stops at 16.
+// by one.  1 x 4096 x 4096: 7.9 us (33.6 MB, 4.2 TB/s: 256 workgroups of 16
+// waves start and end together, which a stream this short feels).  Against the
+// tile kernels, per call: 8.5 us instead of 11.5, 16 rows 9.3 instead of 11.6,
+// but 32 rows (two row blocks) 12.9 instead of 12.7, so it stops at 16.
 constexpr int kRowsUnroll = 4;
 constexpr int kRowsStep = 32 * kRowsUnroll;
 template <typename T, int WAVES>
@@ -913,7 +921,10 @@ void linear_rows_kernel(const Product g) {
 // cover `lanes` groups of eight columns (a power of two) and 256 / lanes rows
 // at a time, kDzRows of them in flight per lane.  The sums of the row groups
 // meet in LDS in a fixed order.  dZ == null: the sums alone.  Without an
-// activation and sums it lays rows out anew (Operand).
+// activation and sums it lays rows out anew (Operand).  Bound by memory: 8192 x
+// 4096 with silu 35 us (201 MB, 5.8 TB/s); the activation is chosen at compile
+// time (20000 x 1111 with gelu: 12 us less for the call than by a branch per
+// value).
 constexpr int kDzThreads = 256;
 constexpr int kDzRows = 4;
 template <typename T, int ACT>

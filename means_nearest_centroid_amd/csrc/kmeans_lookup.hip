@@ -26,6 +26,12 @@
 //     themselves once done with their buckets, without further launches, was
 //     700 us instead of 160 at 16384 x 4096 of 32768 tokens: the fences that
 //     hand partial sums from one XCD to another inside a launch empty its L2.
+// 262144 x 128 of 4096 rows: 25.5 us a call (16 of them lookup_bucket_kernel,
+// 5 the binning; 68 MB); by the sort 61.  16384 x 4096 of 32768 tokens: 124 us
+// (81 lookup_bucket_kernel, 26 + 9 the parts; 403 MB, 3.2 TB/s), by the sort
+// 213.  What is above the bytes is the chain from directory to slots to rows,
+// which a workgroup walks before its first row arrives; deeper batches of rows,
+// smaller parts or stores past the caches change nothing.
 //
 // Sort (every other shape): the positions are sorted by label (the stable
 // radix sort of the centroid update), so that a label's rows are one run of
@@ -64,7 +70,7 @@ __device__ __forceinline__ int table_row(L label, int K) {
 // Rows shorter than V move by elements.  Each thread moves kUnroll pieces
 // whose loads are in flight together; the rows are written past the caches
 // (non-temporal), which leaves the table there.  262144 rows of 128 bf16 from
-// a table of 4096: 12.6 us a call (5.5 TB/s); 14.0 with four pieces, 17.8 with
+// a table of 4096: 11.8 us a call (5.9 TB/s); 14.0 with four pieces, 17.8 with
 // eight, 15.4 with plain stores; 16384 rows of 4096 fp32 85 us instead of 98.
 constexpr int kUnroll = 2;
 template <typename T, int V, typename L>
@@ -815,8 +821,9 @@ GradPlan make_grad_plan(int64_t N, int64_t D, int64_t K, int V, int compute_unit
         p.column_groups = (p.slabs + (1 << p.col_groups_log2) - 1) >> p.col_groups_log2;
         // A part is 512 positions of 256 bytes, fewer for wider slabs, and
         // at least twice the mean bucket if there is one for every CU; larger
-        // where the partial sums would take more than 256 MiB.  A heavy bucket has more than `cap`
-        // positions, so its parts hold half of that each on average at least.
+        // where the partial sums would take more than 256 MiB.  A heavy bucket
+        // has more than `cap` positions, so its parts hold half of that each
+        // on average at least.
         const int64_t bytes = std::min(D, slab) * (V == 8 ? 2 : 4);
         int64_t cap = (int64_t(1) << 25) / (bytes * bytes);
         if (p.bins.buckets >= compute_units)
