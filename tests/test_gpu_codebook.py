@@ -88,6 +88,30 @@ def test_lookup_strides_and_shapes(extra, shift):
     assert km.kmeans_lookup(C, lab[:0].contiguous()).shape == (0, 7, 5, 72)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+@pytest.mark.parametrize("N,D", [(1, 8), (1, 9), (3, 11), (70, 8), (600, 16), (257, 129), (40, 1003),
+                                 (2, 4100)])
+@pytest.mark.parametrize("shift", [0, 1, 3, 7])
+def test_lookup_into_rows_that_follow_one_another(N, D, dtype, shift):
+    """Rows without gaps that start anywhere: each 16 bytes of the output may
+    hold the end of one row and the beginning of the next; nothing before the
+    first row or after the last is touched, and a stray row beside one of
+    infinities stays zero."""
+    C = rand((30, D), dtype, 51)
+    C[7] = float("inf")
+    lab = some_labels(N, 30, 52, torch.int32)
+    lab[::3] = 7
+    lab[1::5] = -1
+    flat = torch.full((N * D + shift + 9,), 7.0, dtype=dtype, device="cuda")
+    out = flat[shift:shift + N * D].view(N, D)
+    km.kmeans_lookup(C, lab, scale=0.5, out=out)
+    seen = ((lab >= 0) & (lab < 30)).unsqueeze(1)
+    want = (C.float()[lab.long().clamp(0, 29)] * 0.5).to(dtype)
+    want = torch.where(seen, want, torch.zeros_like(want))
+    assert torch.equal(out, want)
+    assert (flat[:shift] == 7).all() and (flat[shift + N * D:] == 7).all()
+
+
 def test_lookup_of_special_values():
     C = torch.tensor([[float("inf"), -float("inf"), float("nan"), -0.0, 3e38]] * 3,
                      dtype=F32).cuda()
