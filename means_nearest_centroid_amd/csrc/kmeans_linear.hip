@@ -749,7 +749,7 @@ void linear_tile_kernel(const Product g) {
         // One wave writes and reads the region, in program order; the fence
         // keeps the compiler to it.
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        auto finish = [&](auto act) KM_INLINE {
+        auto finish = [&](auto act, auto stream) KM_INLINE {
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const int i = i_pass + s * (64 / kRuns);
@@ -774,9 +774,10 @@ void linear_tile_kernel(const Product g) {
                 const Packed<B, 8> y = narrow_run<T, 8>(v);
                 // Gradients of aligned rows go past the caches, which leaves
                 // the operands there (65536 x 512 x 128: 56 us for both gradients,
-                // 63 with plain stores); forward outputs do not (4096 x 4096 x 1000 37 us,
-                // 41 so; unaligned rows 26 and 31).
-                if constexpr (QOWN && DMA)
+                // 63 with plain stores); unaligned rows do not (100 x 8001 x
+                // 8001 113 us, 137 past the caches), nor forward outputs (4096
+                // x 4096 x 1000 37 us, 41 so).
+                if constexpr (decltype(stream)::value)
                     __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, y),
                                                 reinterpret_cast<u32x4_any *>(o));
                 else
@@ -784,14 +785,17 @@ void linear_tile_kernel(const Product g) {
             }
         };
         if constexpr (QOWN) {
-            finish(Index<KMEANS_ACT_NONE>{});
+            if (DMA && e.ldo % 8 == 0)
+                finish(Index<KMEANS_ACT_NONE>{}, std::bool_constant<DMA>{});
+            else
+                finish(Index<KMEANS_ACT_NONE>{}, std::false_type{});
         } else {
             switch (e.act) {
-            case KMEANS_ACT_RELU: finish(Index<KMEANS_ACT_RELU>{}); break;
-            case KMEANS_ACT_GELU: finish(Index<KMEANS_ACT_GELU>{}); break;
-            case KMEANS_ACT_GELU_TANH: finish(Index<KMEANS_ACT_GELU_TANH>{}); break;
-            case KMEANS_ACT_SILU: finish(Index<KMEANS_ACT_SILU>{}); break;
-            default: finish(Index<KMEANS_ACT_NONE>{}); break;
+            case KMEANS_ACT_RELU: finish(Index<KMEANS_ACT_RELU>{}, std::false_type{}); break;
+            case KMEANS_ACT_GELU: finish(Index<KMEANS_ACT_GELU>{}, std::false_type{}); break;
+            case KMEANS_ACT_GELU_TANH: finish(Index<KMEANS_ACT_GELU_TANH>{}, std::false_type{}); break;
+            case KMEANS_ACT_SILU: finish(Index<KMEANS_ACT_SILU>{}, std::false_type{}); break;
+            default: finish(Index<KMEANS_ACT_NONE>{}, std::false_type{}); break;
             }
         }
         if (has_cut) {
