@@ -339,6 +339,38 @@ def test_linear_strides(extra, shift):
         ref.check(got, *want[name], name)
 
 
+def gaps(t, extra):
+    """The same values in rows of an odd stride, NaN between them."""
+    v = rows_in(t, extra)
+    keep = v.clone()
+    v._base.fill_(float("nan"))
+    v.copy_(keep)
+    return v
+
+
+@pytest.mark.parametrize("N,D,F,odd", [(1200, 1600, 1200, "X"), (1200, 1600, 1200, "W"),
+                                       (2900, 2907, 2901, "both")])
+def test_linear_of_large_unaligned_operands(N, D, F, odd):
+    """Products long enough that operands whose rows are not 16-byte aligned
+    are laid out anew first, one of them or both."""
+    X, W = rand((N, D), BF, 1), rand((F, D), BF, 2, D ** -0.5)
+    b, R = rand((F,), BF, 3), rand((N, F), BF, 4)
+    y, z, yb, zb = ref.linear(X, W, b, R, "silu")
+    Y, Z = km.kmeans_linear(gaps(X, 5) if odd != "W" else X, gaps(W, 3) if odd != "X" else W,
+                            bias=b, residual=R, activation="silu", save_pre=True)
+    ref.check(Y, y, yb, "Y")
+    ref.check(Z, z, zb, "Z")
+
+
+@pytest.mark.parametrize("N,D,F", [(1024, 1001, 1024), (900, 1201, 1100), (1300, 1003, 1101)])
+def test_linear_grad_of_large_unaligned_operands(N, D, F):
+    X, W = gaps(rand((N, D), BF, 1), 7), gaps(rand((F, D), BF, 2, D ** -0.5), 2)
+    dY, Z = gaps(rand((N, F), BF, 3, 0.25), 1), gaps(rand((N, F), BF, 4, 2.0), 3)
+    want = ref.linear_grad(dY, X, W, Z, "gelu")
+    for name, got in zip(("dX", "dW", "db"), km.kmeans_linear_grad(dY, X, W, Z, "gelu")):
+        ref.check(got, *want[name], name)
+
+
 def test_linear_in_place_residual_and_leading_shape():
     X, W, R = rand((3, 5, 64), BF, 1), rand((48, 64), BF, 2, 0.1), rand((3, 5, 48), BF, 3)
     want = km.kmeans_linear(X, W, residual=R, activation="gelu")
