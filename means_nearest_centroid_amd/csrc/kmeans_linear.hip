@@ -23,6 +23,7 @@
 #include <utility>
 
 #include "kmeans_internal.h"
+#include "kmeans_linear_plan.h"
 #include "kmeans_types.h"
 
 namespace kmeans {
@@ -35,7 +36,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define KM_LDS __attribute__((address_space(3)))
 #define KM_INLINE __attribute__((always_inline))
 
-constexpr int kTileK = 64;            // k extent of a staged tile: two MFMA k-steps of 32
 constexpr uint32_t kOutOfRange = 0x80000000u;
 constexpr int64_t kMaxWidth = 1 << 20;   // D, F and row strides: 64 rows stay below 2^31 bytes
 constexpr int kMaxKSplits = 64;
@@ -213,36 +213,6 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// One operand's tile of kTileK values of k by R values of its own index, as
-// it is staged in LDS.
-//
-//   own index contiguous == false: R rows of 64 k (128 bytes, 8 chunks of 16).
-//     Chunk c of row r lies at chunk c ^ ((r >> 1) & 7): the 16 rows that a
-//     ds_read_b128 group reads at one k cover all 64 banks once.
-//   own index contiguous == true: 64 rows (k) of R values (R / 16 granules of
-//     32 bytes).  Granule g of row k lies at g ^ f(k), f(k) = (k & 3) |
-//     ((k >> 3) & 3) << 2 (as many bits as there are granules): the 16 rows
-//     that one ds_read_b64_tr_b16 reads of one granule then lie in different
-//     granules, so in different banks.
-template <bool OWN, int R>
-struct TileMap {
-    static constexpr int kRows = OWN ? kTileK : R;
-    static constexpr int kRowBytes = (OWN ? R : kTileK) * 2;
-    static constexpr int kChunks = kRowBytes / 16;
-    static constexpr int kBytes = kRows * kRowBytes;
-    static constexpr int kGranules = R / 16;
-
-    static __device__ __forceinline__ int spread(int k) {
-        return ((k & 3) | (((k >> 3) & 3) << 2)) & (kGranules - 1);
-    }
-    // The chunk of row r that lies at chunk slot c (its own inverse).
-    static __device__ __forceinline__ int chunk(int r, int c) {
-        if (OWN)
-            return (((c >> 1) ^ spread(r)) << 1) | (c & 1);
-        return c ^ ((r >> 1) & 7);
-    }
-};
-
 // Copies tiles of one operand from global memory into LDS, THREADS threads
 // together; tile t covers k in [t * 64, t * 64 + 64) of the workgroup's range.
 // Values past the range of k are zero (so they add nothing); values past the
@@ -252,17 +222,19 @@ struct TileMap {
 // DMA (16-byte aligned rows of whole chunks): buffer loads straight into LDS,
 // nothing held in registers.  Else: 16-byte buffer loads at the rows' own
 // alignment into registers at issue(), written to LDS at commit().  Such a load
-// may run past the end of its row, into the next one.  The last tile, where
-// there may be no next one, loads a run that is cut short so that it ends with
-// its row, and commit() shifts it down (4133 x 515 x 1001 24.6 us, 26.5 with
-// those values loaded one by one, which rows of less than eight values still
-// are).
+// may run past the end of its row, into the rows after it, where those hold it
+// (runs_stay_inside).  The last tile, where there may be no next row, loads a
+// run that is cut short so that it ends with its row, and commit() shifts it
+// down (4133 x 515 x 1001 24.6 us, 26.5 with those values loaded one by one).
+// Rows of less than eight values have no such run: their last tile, and the
+// one before it where its runs would leave the operand, is loaded value by
+// value.
 template <typename T, bool OWN, int R, int THREADS, bool DMA>
 struct Stager {
     typedef TileMap<OWN, R> Map;
+    typedef TilePieces<OWN, R, THREADS, DMA> Pieces;
     typedef typename T::bits B;
-    static constexpr int kPieces = Map::kBytes / 16 / THREADS;
-    static_assert(kPieces >= 1 && Map::kBytes % (16 * THREADS) == 0, "whole pieces per thread");
+    static constexpr int kPieces = Pieces::kCount;
 
     const B *base;        // element (0, 0) of the current range, own offset included
     int64_t ld;
@@ -277,9 +249,17 @@ struct Stager {
 
     // Piece u of this thread: row r and chunk c (elements 8 c ..) it fetches.
     __device__ __forceinline__ void piece(int u, int &r, int &c) const {
-        const int o = DMA ? (((tid >> 6) * kPieces + u) * 64 + (tid & 63)) : u * THREADS + tid;
-        r = o / Map::kChunks;
-        c = Map::chunk(r, o % Map::kChunks);
+        Pieces::at(tid, u, r, c);
+    }
+    // Whether a tile with k_left values of k to the end of the range (its own
+    // among them) may load whole runs.
+    __device__ __forceinline__ bool whole_runs(int k_left) const {
+        return runs_stay_inside(OWN, k_left, ld, own_lim);
+    }
+    // Tiles at the end of the range that may not.
+    __device__ __forceinline__ int cut_tiles() const {
+        const int last = (k_len - 1) % kTileK + 1;
+        return k_len > kTileK && !whole_runs(last + kTileK) ? 2 : 1;
     }
     __device__ __forceinline__ void init(const void *p, int64_t stride, int own0, int own,
                                          int64_t k0, int k_n, int thread) {
@@ -301,7 +281,8 @@ struct Stager {
                 off[u] = static_cast<uint32_t>(min(r, own_lim - 1) * ld + c * 8) * 2u;
         }
     }
-    // FULL: the tile is known to hold kTileK values of k, and k goes on after it.
+    // FULL: the tile is known to hold kTileK values of k, and to be none of the
+    // last cut_tiles() ones where those count (without DMA).
     template <bool FULL>
     __device__ __forceinline__ void issue(int t, uint8_t *stage) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -326,7 +307,7 @@ struct Stager {
                         rs, (KM_LDS void *)(dst + u * 1024), 16, o, 0, 0, 0);
                 }
             }
-        } else if (FULL || k_left > kTileK) {
+        } else if (FULL || whole_runs(k_left)) {
 #pragma unroll
             for (int u = 0; u < kPieces; ++u)
                 held[u] = __builtin_bit_cast(
@@ -371,7 +352,7 @@ struct Stager {
     }
     // Values by which the last tile's run c starts early to end with its row.
     __device__ __forceinline__ int cut(int c, int k_left) const {
-        return max(0, c * 8 + 8 - (OWN ? own_lim : k_left));
+        return values_cut(c, OWN ? own_lim : k_left);
     }
     // Tile t, issued last, is in LDS once this returned on every wave and
     // they met at a barrier.  FULL: it is not the last one.
@@ -570,9 +551,9 @@ void linear_tile_kernel(const Product g) {
     constexpr int kReads = (POWN ? 2 : 1) * HB + (QOWN ? 2 : 1) * TJ;
     constexpr int kCopies = decltype(ps)::kPieces + decltype(qs)::kPieces;
     // Tile t, in stage at % S.  FULL: tiles t + 1 .. t + S exist and t + S is a
-    // whole one (and not the last, without DMA), so the step has no branches (a branch around the copies would
-    // cost the compiler its knowledge of which stage they write, and a wait
-    // before the next reads).
+    // whole one (without DMA: and none of the last cut_tiles()), so the step has
+    // no branches (a branch around the copies would cost the compiler its
+    // knowledge of which stage they write, and a wait before the next reads).
     auto step = [&](auto full, auto at, int t) KM_INLINE {
         constexpr bool FULL = decltype(full)::value;
         uint8_t *pc = p_stage(at), *qc = q_stage(at);
@@ -640,7 +621,8 @@ void linear_tile_kernel(const Product g) {
     lds_barrier();
     read_phase(p0, q0, 0);
     int t = 0;
-    for (const int whole = DMA ? k_len / kTileK : tiles - 1; t + 2 * S - 1 < whole; t += S) {
+    const int full = DMA ? k_len / kTileK : tiles - max(ps.cut_tiles(), qs.cut_tiles());
+    for (; t + 2 * S - 1 < full; t += S) {
         step(std::true_type{}, Index<0>{}, t);
         step(std::true_type{}, Index<1>{}, t + 1);
         if constexpr (S > 2) {
