@@ -418,9 +418,11 @@ kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t cou
 
 /*
  * The workspace of `stream` on the current device.  kmeans_assign's K-split
- * path and kmeans_update take their scratch from one device buffer per
- * (device, stream), kept between calls: a stream-ordered allocation and free
- * on every call costs more host time than a small call's kernels.  It grows
+ * path, kmeans_update, kmeans_lookup_grad, kmeans_linear, kmeans_linear_grad,
+ * kmeans_gradient_norm and kmeans_clip_gradients take their scratch from one
+ * device buffer per (device, stream), kept between calls: a stream-ordered
+ * allocation and free on every call costs more host time than a small call's
+ * kernels.  It grows
  * in stream order (the old buffer freed by hipFreeAsync and a larger one
  * taken from hipMallocAsync, both on `stream`), so calls on one stream share
  * it safely and calls on different streams never do.  The library never
@@ -432,6 +434,14 @@ kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t cou
  * buffer per calling thread (release it from that thread).  The same call
  * gives back the stream's tile queue of the persistent path.  No-op when the
  * stream holds none; KMEANS_ERR_HIP if the free fails.
+ *
+ * Graphs.  A call that is captured into a graph uses the workspace of the
+ * stream it was captured on at every replay: replays must not overlap one
+ * another, another graph captured on that stream, or calls on it (all on one
+ * stream is enough).  A buffer that a captured call was given stays allocated
+ * when later calls outgrow it, until this call; after it, such graphs must not
+ * be replayed.  What a capture itself takes is ordinary device memory
+ * (hipMalloc), and this call waits for the device to free it.
  */
 kmeans_status_t kmeans_release_workspace(hipStream_t stream);
 

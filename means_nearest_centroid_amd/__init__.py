@@ -617,10 +617,11 @@ def kmeans_clip_gradients(grads, max_norm: float, out=None, norm=None, stream=No
 
 
 def kmeans_release_workspace(stream=None):
-    """Return the stream's workspace (the K-split path's and the update's
-    scratch, kept between calls) and its tile queue (the persistent path's)
-    to the device's memory pool, in stream order; a later call on the stream
-    allocates them again."""
+    """Return the stream's workspace (scratch of the K-split path, the update,
+    the lookup's gradient, the linear layer and the clipping, kept between
+    calls) and its tile queue (the persistent path's) to the device's memory
+    pool, in stream order; a later call on the stream allocates them again.
+    Graphs that captured calls on the stream must not be replayed afterwards."""
     lib = load_library()
     _check(lib, lib.kmeans_release_workspace(_stream_handle(stream)))
 

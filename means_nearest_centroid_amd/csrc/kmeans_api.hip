@@ -4,13 +4,8 @@
 #include <stdio.h>
 
 #include <atomic>
-#include <map>
 #include <mutex>
-#include <functional>
 #include <string>
-#include <thread>
-#include <tuple>
-#include <utility>
 
 #include "kmeans_internal.h"
 #include "kmeans_mi355x.h"
@@ -63,106 +58,6 @@ int device_compute_units() {
         cache[dev].store(cus, std::memory_order_relaxed);
     }
     return cus;
-}
-
-namespace {
-// (device, stream, thread) -> (buffer, bytes).  The thread is part of the key
-// only for hipStreamPerThread, one handle that names a different stream in
-// every thread.  Never destroyed: at process exit the runtime may be gone
-// before static destructors run, and it reclaims device memory itself.
-using WsKey = std::tuple<int, uintptr_t, size_t>;
-std::mutex g_ws_mutex;
-auto *g_ws = new std::map<WsKey, std::pair<void *, size_t>>();
-// The persistent path's tile queue per (device, stream, thread): two int32
-// counters in a small allocation of their own (the workspace above is
-// overwritten by other calls, the queue must stay zero between launches).
-auto *g_queues = new std::map<WsKey, int *>();
-constexpr size_t kQueueBytes = 256;
-constexpr size_t kWorkspaceGranule = size_t(1) << 20;
-
-WsKey ws_key(int dev, hipStream_t stream) {
-    const size_t thread = stream == hipStreamPerThread
-                              ? std::hash<std::thread::id>()(std::this_thread::get_id())
-                              : 0;
-    return WsKey{dev, reinterpret_cast<uintptr_t>(stream), thread};
-}
-}  // namespace
-
-WorkspaceLease::WorkspaceLease(hipStream_t stream, size_t bytes) {
-    g_ws_mutex.lock();
-    int dev = 0;
-    error_ = hipGetDevice(&dev);
-    if (error_ != hipSuccess)
-        return;
-    auto &slot = (*g_ws)[ws_key(dev, stream)];
-    if (slot.second < bytes) {
-        if (slot.first != nullptr) {
-            void *old = slot.first;
-            slot = {nullptr, 0};
-            error_ = hipFreeAsync(old, stream);
-            if (error_ != hipSuccess)
-                return;
-        }
-        const size_t want = (bytes + kWorkspaceGranule - 1) / kWorkspaceGranule * kWorkspaceGranule;
-        void *p = nullptr;
-        error_ = hipMallocAsync(&p, want, stream);
-        if (error_ == hipSuccess && p == nullptr)
-            error_ = hipErrorOutOfMemory;
-        if (error_ != hipSuccess)
-            return;
-        slot = {p, want};
-    }
-    ptr_ = slot.first;
-}
-
-WorkspaceLease::~WorkspaceLease() { g_ws_mutex.unlock(); }
-
-QueueLease::QueueLease(hipStream_t stream) {
-    g_ws_mutex.lock();
-    int dev = 0;
-    error_ = hipGetDevice(&dev);
-    if (error_ != hipSuccess)
-        return;
-    int *&q = (*g_queues)[ws_key(dev, stream)];
-    if (q == nullptr) {
-        void *p = nullptr;
-        error_ = hipMallocAsync(&p, kQueueBytes, stream);
-        if (error_ == hipSuccess && p == nullptr)
-            error_ = hipErrorOutOfMemory;
-        if (error_ != hipSuccess)
-            return;
-        error_ = launch_zero_queue(static_cast<int *>(p), stream);
-        if (error_ != hipSuccess) {
-            (void)hipFreeAsync(p, stream);
-            return;
-        }
-        q = static_cast<int *>(p);
-    }
-    ptr_ = q;
-}
-
-QueueLease::~QueueLease() { g_ws_mutex.unlock(); }
-
-hipError_t release_workspace(hipStream_t stream) {
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess)
-        return e;
-    const WsKey key = ws_key(dev, stream);
-    auto qit = g_queues->find(key);
-    if (qit != g_queues->end()) {
-        int *q = qit->second;
-        g_queues->erase(qit);
-        if (q != nullptr && (e = hipFreeAsync(q, stream)) != hipSuccess)
-            return e;
-    }
-    auto it = g_ws->find(key);
-    if (it == g_ws->end())
-        return hipSuccess;
-    void *p = it->second.first;
-    g_ws->erase(it);
-    return p != nullptr ? hipFreeAsync(p, stream) : hipSuccess;
 }
 
 kmeans_status_t check_d(int64_t D) {

@@ -173,8 +173,9 @@ int device_compute_units();
 // per call costs ~15 us of host time (more than a small call's kernels).  It
 // grows stream-ordered: the old buffer is freed by hipFreeAsync and the new
 // one taken from hipMallocAsync, both on `stream`, behind the work already
-// queued there.  Calls on one stream run in order, so they can share it;
-// another stream gets its own.  The lease holds a process-wide lock until it
+// queued there (a buffer that a captured call was given is kept for the graph's
+// replays instead, until release_workspace).  Calls on one stream run in order,
+// so they can share it; another stream gets its own.  The lease holds a process-wide lock until it
 // is destroyed, so no other thread can grow the buffer between this call's
 // acquisition and its launches.
 class WorkspaceLease {
@@ -208,8 +209,8 @@ private:
     hipError_t error_ = hipSuccess;
 };
 
-// Frees (stream-ordered) the current device's buffer and tile queue kept for
-// `stream`.
+// Frees (stream-ordered where they were taken so) the current device's buffers
+// and tile queue kept for `stream`.
 hipError_t release_workspace(hipStream_t stream);
 
 }  // namespace kmeans
