@@ -5,13 +5,12 @@
 
 #include <atomic>
 #include <mutex>
-#include <string>
 
 #include "kmeans_internal.h"
 #include "kmeans_mi355x.h"
 
 namespace {
-thread_local std::string g_last_error;
+thread_local char g_last_error[512];   // fixed: reporting an error allocates nothing
 }  // namespace
 
 // ---- The fixed device scratch of kmeans_assign_static ----
@@ -28,17 +27,15 @@ static __device__ __align__(256) uint8_t scratch[KMEANS_STATIC_SCRATCH_BYTES];
 namespace kmeans {
 
 kmeans_status_t fail(kmeans_status_t st, const char *fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
+    vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return st;
 }
 
 kmeans_status_t ok() {
-    g_last_error.clear();
+    g_last_error[0] = 0;
     return KMEANS_OK;
 }
 
@@ -311,7 +308,7 @@ kmeans_status_t kmeans_release_workspace(hipStream_t stream) {
     return ok();
 }
 
-const char *kmeans_last_error(void) { return g_last_error.c_str(); }
+const char *kmeans_last_error(void) { return g_last_error; }
 
 int kmeans_abi_version(void) { return KMEANS_ABI_VERSION; }
 

@@ -18,7 +18,7 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <memory>
+#include <optional>
 #include <type_traits>
 #include <utility>
 
@@ -1443,10 +1443,10 @@ extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const 
     }
     const size_t part_at = bytes;
     bytes += partial_bytes(g);
-    std::unique_ptr<WorkspaceLease> lease;
+    std::optional<WorkspaceLease> lease;
     char *ws = nullptr;
     if (bytes > 0) {
-        lease = std::make_unique<WorkspaceLease>(stream, bytes);
+        lease.emplace(stream, bytes);
         if (lease->error() != hipSuccess)
             return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", bytes,
                         hipGetErrorString(lease->error()));
@@ -1539,10 +1539,10 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
     }
     p.part_at = at;
     p.bytes = at + part;
-    std::unique_ptr<WorkspaceLease> lease;
+    std::optional<WorkspaceLease> lease;
     char *ws = nullptr;
     if (p.bytes > 0) {
-        lease = std::make_unique<WorkspaceLease>(stream, p.bytes);
+        lease.emplace(stream, p.bytes);
         if (lease->error() != hipSuccess)
             return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", p.bytes,
                         hipGetErrorString(lease->error()));

@@ -46,7 +46,7 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <memory>
+#include <optional>
 
 #include "kmeans_types.h"
 #include "kmeans_update_internal.h"
@@ -1025,10 +1025,10 @@ extern "C" kmeans_status_t kmeans_lookup_grad(const void *dY, int64_t dy_stride,
     g.lanes_log2 = p.lanes_log2;
     g.slabs = p.slabs;
     BucketArgs bk{};
-    std::unique_ptr<WorkspaceLease> lease;
+    std::optional<WorkspaceLease> lease;
     hipError_t e = hipSuccess;
     if (N > 0) {
-        lease = std::make_unique<WorkspaceLease>(stream, p.bytes);
+        lease.emplace(stream, p.bytes);
         if (lease->error() != hipSuccess)
             return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", p.bytes,
                         hipGetErrorString(lease->error()));

@@ -39,7 +39,7 @@
 //     pre-pass computes it (row_sq_norm16 over a copy of the row in LDS).
 #include <stdint.h>
 
-#include <memory>
+#include <optional>
 
 #include "kmeans_update_internal.h"
 
@@ -1815,10 +1815,10 @@ extern "C" kmeans_status_t kmeans_update_path(const void *X, const int32_t *labe
                     static_cast<long long>(K));
     const UpdatePlan pl = make_update_plan(N, D, K, device_compute_units(), path);
     // The stream's scratch (none when N == 0), held until the launches are queued.
-    std::unique_ptr<WorkspaceLease> lease;
+    std::optional<WorkspaceLease> lease;
     void *ws = nullptr;
     if (pl.bytes > 0) {
-        lease = std::make_unique<WorkspaceLease>(stream, pl.bytes);
+        lease.emplace(stream, pl.bytes);
         if (lease->error() != hipSuccess)
             return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", pl.bytes,
                         hipGetErrorString(lease->error()));

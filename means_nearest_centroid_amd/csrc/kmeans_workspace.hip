@@ -9,6 +9,7 @@
 #include <functional>
 #include <map>
 #include <mutex>
+#include <new>
 #include <thread>
 #include <tuple>
 #include <utility>
@@ -104,22 +105,27 @@ WorkspaceLease::WorkspaceLease(hipStream_t stream, size_t bytes) {
     error_ = hipGetDevice(&dev);
     if (error_ != hipSuccess)
         return;
-    Workspace &ws = (*g_ws)[ws_key(dev, stream)];
-    const bool capturing = is_capturing(stream);
-    if (ws.now.bytes < bytes) {
-        if (ws.now.captured || (capturing && ws.now.ptr != nullptr)) {
-            ws.kept.push_back(ws.now);
-            ws.now = {};
-        } else if ((error_ = give(ws.now, stream)) != hipSuccess) {
-            return;
+    try {
+        Workspace &ws = (*g_ws)[ws_key(dev, stream)];
+        const bool capturing = is_capturing(stream);
+        if (ws.now.bytes < bytes) {
+            if (ws.now.captured || (capturing && ws.now.ptr != nullptr)) {
+                ws.kept.push_back(ws.now);
+                ws.now = {};
+            } else if ((error_ = give(ws.now, stream)) != hipSuccess) {
+                return;
+            }
+            const size_t want =
+                (bytes + kWorkspaceGranule - 1) / kWorkspaceGranule * kWorkspaceGranule;
+            error_ = take(ws.now, want, capturing, stream);
+            if (error_ != hipSuccess)
+                return;
         }
-        const size_t want = (bytes + kWorkspaceGranule - 1) / kWorkspaceGranule * kWorkspaceGranule;
-        error_ = take(ws.now, want, capturing, stream);
-        if (error_ != hipSuccess)
-            return;
+        ws.now.captured |= capturing;
+        ptr_ = ws.now.ptr;
+    } catch (const std::bad_alloc &) {   // must not leave a C entry point, nor the lock held
+        error_ = hipErrorOutOfMemory;
     }
-    ws.now.captured |= capturing;
-    ptr_ = ws.now.ptr;
 }
 
 WorkspaceLease::~WorkspaceLease() { g_ws_mutex.unlock(); }
@@ -130,22 +136,26 @@ QueueLease::QueueLease(hipStream_t stream) {
     error_ = hipGetDevice(&dev);
     if (error_ != hipSuccess)
         return;
-    Queue &q = (*g_queues)[ws_key(dev, stream)];
-    const bool capturing = is_capturing(stream);
-    if (q.buf.ptr == nullptr) {
-        error_ = take(q.buf, kQueueBytes, capturing, stream);
-        if (error_ != hipSuccess)
-            return;
+    try {
+        Queue &q = (*g_queues)[ws_key(dev, stream)];
+        const bool capturing = is_capturing(stream);
+        if (q.buf.ptr == nullptr) {
+            error_ = take(q.buf, kQueueBytes, capturing, stream);
+            if (error_ != hipSuccess)
+                return;
+        }
+        if (!q.zero) {
+            // Within a capture this zeroes before every replay, where the
+            // counters are zero anyway, but not before a call that comes first.
+            error_ = launch_zero_queue(static_cast<int *>(q.buf.ptr), stream);
+            if (error_ != hipSuccess)
+                return;
+            q.zero = !capturing;
+        }
+        ptr_ = static_cast<int *>(q.buf.ptr);
+    } catch (const std::bad_alloc &) {
+        error_ = hipErrorOutOfMemory;
     }
-    if (!q.zero) {
-        // Within a capture this zeroes before every replay, where the counters
-        // are zero anyway, but not before a call that comes first.
-        error_ = launch_zero_queue(static_cast<int *>(q.buf.ptr), stream);
-        if (error_ != hipSuccess)
-            return;
-        q.zero = !capturing;
-    }
-    ptr_ = static_cast<int *>(q.buf.ptr);
 }
 
 QueueLease::~QueueLease() { g_ws_mutex.unlock(); }

@@ -5,9 +5,20 @@
 #include <cstdio>
 #include <cstdlib>
 #include <map>
+#include <new>
 #include <set>
 
 #include "kmeans_internal.h"
+
+bool fail_new = false;
+void *operator new(size_t n) {
+    void *p = fail_new ? nullptr : std::malloc(n);
+    if (p == nullptr)
+        throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, size_t) noexcept { std::free(p); }
 
 namespace {
 
@@ -165,6 +176,23 @@ int main() {
         expect(usable(a) && eager_zeros == 0, "a queue of its own");
         expect(kmeans::QueueLease(s).ptr() == a && eager_zeros == 1, "zeroed for eager calls");
         expect(kmeans::QueueLease(s).ptr() == a && eager_zeros == 1, "once");
+        expect(kmeans::release_workspace(s) == hipSuccess && live() == 0, "released");
+    }
+    {   // Host memory that runs out is a status too, and leaves no lock held.
+        const hipStream_t s = stream(5);
+        hipError_t w = hipSuccess, q = hipSuccess;
+        try {
+            fail_new = true;
+            w = kmeans::WorkspaceLease(s, kMiB).error();
+            q = kmeans::QueueLease(s).error();
+            fail_new = false;
+        } catch (const std::bad_alloc &) {
+            fail_new = false;
+            std::printf("failed: an exception left a lease\n");
+            return 1;
+        }
+        expect(w == hipErrorOutOfMemory && q == hipErrorOutOfMemory, "reported");
+        expect(usable(lease(s, kMiB)), "a later call gets a workspace");
         expect(kmeans::release_workspace(s) == hipSuccess && live() == 0, "released");
     }
     if (!broken)
