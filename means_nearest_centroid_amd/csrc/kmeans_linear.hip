@@ -88,8 +88,13 @@ __device__ __forceinline__ float activate(int act, float z) {
     }
 }
 
-// d * act'(z)
+// d * act'(z).  Past 128 every slope but relu's is 1 or 0 to the last bit in
+// fp32; z is held there, since its square or cube would overflow, or an
+// infinite z (a pre-activation kept in fp16) meet a zero, and make NaN of it.
+// A NaN stays.
 __device__ __forceinline__ float activate_grad(int act, float z, float d) {
+    if (act != KMEANS_ACT_NONE && act != KMEANS_ACT_RELU)
+        z = z > 128.0f ? 128.0f : z < -128.0f ? -128.0f : z;
     switch (act) {
     case KMEANS_ACT_RELU:
         return z <= 0.0f ? 0.0f : d;
