@@ -55,6 +55,9 @@ namespace kmeans {
 namespace {
 
 constexpr int kRowThreads = 256;
+// Workgroups across a grid: a launch takes less than 2^32 threads that way.
+// More go to a second dimension (lookup) or are walked (zeroed rows).
+constexpr int64_t kMaxGridX = int64_t(1) << 20;
 
 // The label as a row of the table, -1 for a stray one.
 template <typename L>
@@ -79,7 +82,8 @@ void lookup_kernel(const typename T::bits *__restrict__ C, int64_t ldc, const L 
                    int64_t N, int D, int K, float scale, int pieces, uint32_t inv,
                    typename T::bits *__restrict__ Y, int64_t ldy) {
     typedef typename T::bits B;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kUnroll * kRowThreads);
+    const int64_t wg = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t first = wg * (kUnroll * kRowThreads);
     const int64_t row0 = first / pieces;
     const uint32_t rem0 = static_cast<uint32_t>(first - row0 * pieces);
     int64_t row[kUnroll];
@@ -87,7 +91,7 @@ void lookup_kernel(const typename T::bits *__restrict__ C, int64_t ldc, const L 
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const uint32_t x = rem0 + u * kRowThreads + threadIdx.x;
-        // x / pieces for x < pieces + 1024: inv = ceil(2^32 / pieces), one
+        // x / pieces for x < pieces + 512: inv = ceil(2^32 / pieces), one
         // too high at most.
         uint32_t q = inv != 0 ? __umulhi(x, inv) : x;
         q -= q * pieces > x ? 1 : 0;
@@ -229,21 +233,24 @@ void lookup_sum_kernel(const GradArgs g, int sum_wgs) {
     const int lanes = 1 << g.lanes_log2;
     const int l = tid & (lanes - 1);
     if (static_cast<int>(blockIdx.x) >= sum_wgs) {
-        // Zero the rows that no label names: kFillRows of them, this slab.
+        // Zero the rows that no label names: kFillRows at a time, this slab.
         __shared__ uint8_t named[kFillRows];
-        const int r0 = (blockIdx.x - sum_wgs) * kFillRows;
-        if (tid < kFillRows) {
-            const int k = r0 + tid;
-            const int p = bound_of(g.keys, 0, g.N, k, false);
-            named[tid] = p < g.N && g.keys[p] == k;
-        }
-        __syncthreads();
         const Columns<V> cols(blockIdx.y, lanes, l, g.D);
-        if (!cols.any)
-            return;
-        for (int r = tid >> g.lanes_log2; r < kFillRows; r += kRowThreads >> g.lanes_log2)
-            if (r0 + r < g.K && !named[r])
-                zero_row<O, V>(g, r0 + r, cols);
+        const int64_t step = static_cast<int64_t>(gridDim.x - sum_wgs) * kFillRows;
+        for (int64_t first = static_cast<int64_t>(blockIdx.x - sum_wgs) * kFillRows; first < g.K;
+             first += step) {
+            const int r0 = static_cast<int>(first), rows = min(kFillRows, g.K - r0);
+            __syncthreads();
+            if (tid < rows) {
+                const int p = bound_of(g.keys, 0, g.N, r0 + tid, false);
+                named[tid] = p < g.N && g.keys[p] == r0 + tid;
+            }
+            __syncthreads();
+            if (cols.any)
+                for (int r = tid >> g.lanes_log2; r < rows; r += kRowThreads >> g.lanes_log2)
+                    if (!named[r])
+                        zero_row<O, V>(g, r0 + r, cols);
+        }
         return;
     }
     const int c = blockIdx.x * (kRowThreads >> g.lanes_log2) + (tid >> g.lanes_log2);
@@ -878,7 +885,9 @@ hipError_t launch_grad(const GradPlan &p, const GradArgs &g, const BucketArgs &b
     }
     const int per_wg = kRowThreads >> p.lanes_log2;
     const int sum_wgs = (p.chunks + per_wg - 1) / per_wg;
-    const int fill_wgs = g.accumulate ? 0 : (g.K + kFillRows - 1) / kFillRows;
+    const int fill_wgs =
+        g.accumulate ? 0 : static_cast<int>(std::min<int64_t>((int64_t(g.K) + kFillRows - 1) / kFillRows,
+                                                              kMaxGridX));
     if (sum_wgs + fill_wgs > 0) {
         hipLaunchKernelGGL((lookup_sum_kernel<T, O, V>), dim3(sum_wgs + fill_wgs, p.slabs),
                            dim3(kRowThreads), 0, stream, g, sum_wgs);
@@ -902,10 +911,13 @@ hipError_t launch_lookup(const void *C, int64_t ldc, const void *labels, int64_t
     const uint32_t inv = pieces == 1 ? 0
                                      : static_cast<uint32_t>(((uint64_t(1) << 32) + pieces - 1) / pieces);
     const int64_t wgs = (N * pieces + kUnroll * kRowThreads - 1) / (kUnroll * kRowThreads);
-    hipLaunchKernelGGL((lookup_kernel<T, V, L>), dim3(static_cast<unsigned>(wgs)), dim3(kRowThreads),
-                       0, stream, static_cast<const B *>(C), ldc, static_cast<const L *>(labels),
-                       N, static_cast<int>(D), static_cast<int>(K), scale,
-                       static_cast<int>(pieces), inv, static_cast<B *>(Y), ldy);
+    const int64_t across = std::min(wgs, kMaxGridX);
+    const dim3 grid(static_cast<unsigned>(across),
+                    static_cast<unsigned>((wgs + across - 1) / across));
+    hipLaunchKernelGGL((lookup_kernel<T, V, L>), grid, dim3(kRowThreads), 0, stream,
+                       static_cast<const B *>(C), ldc, static_cast<const L *>(labels), N,
+                       static_cast<int>(D), static_cast<int>(K), scale, static_cast<int>(pieces),
+                       inv, static_cast<B *>(Y), ldy);
     return hipGetLastError();
 }
 
