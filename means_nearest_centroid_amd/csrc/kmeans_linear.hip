@@ -146,6 +146,7 @@ struct Product {
     int shape;              // Shape
     int k_chunk;            // k per split, a multiple of kTileK
     int splits;
+    int first_wg;           // of this launch
     float *partial;         // [splits][I][J] fp32 when splits > 1
     Epilogue epi;
 };
@@ -517,7 +518,7 @@ void linear_tile_kernel(const Product g) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ni = (g.I + RI - 1) / RI, nj = (g.J + RJ - 1) / RJ;
     int split, ti, tj;
-    tile_of(blockIdx.x, ni, nj, g.splits, split, ti, tj);
+    tile_of(g.first_wg + static_cast<int>(blockIdx.x), ni, nj, g.splits, split, ti, tj);
     const int i0 = ti * RI, j0 = tj * RJ;
     const int wi = (wave % WI) * TI * 16, wj = (wave / WI) * TJ * 16;
     const int64_t k0 = static_cast<int64_t>(split) * g.k_chunk;
@@ -1231,27 +1232,35 @@ hipError_t move_operand(const Operand &o, int compute_units, char *ws, const voi
 }
 
 template <typename T, bool POWN, bool QOWN>
-hipError_t launch_product_modes(const Product &g, const BiasSums &bias, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(tiles_of(g, g.shape == kWide ? 256 : 128) * g.splits));
-    switch (g.shape) {
-    case kWide:
-        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 8, 4, 2, true>), grid,
-                           dim3(512), 0, stream, g);
-        break;
-    case kDeep:
-        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 4, 2, 4, true>), grid,
-                           dim3(512), 0, stream, g);
-        break;
-    case kPaired:
-        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, 2, true>), grid,
-                           dim3(256), 0, stream, g);
-        break;
-    default:
-        hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 4, 2, 2, false>), grid,
-                           dim3(512), 0, stream, g);
-        break;
+hipError_t launch_product_modes(const Product &product, const BiasSums &bias, hipStream_t stream) {
+    // A launch has less than 2^32 threads: products of more tiles take several.
+    constexpr int64_t kMaxGrid = int64_t(1) << 22;
+    Product g = product;
+    const int64_t tiles = tiles_of(g, g.shape == kWide ? 256 : 128) * g.splits;
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < tiles && e == hipSuccess; first += kMaxGrid) {
+        g.first_wg = static_cast<int>(first);
+        const dim3 grid(static_cast<unsigned>(std::min(tiles - first, kMaxGrid)));
+        switch (g.shape) {
+        case kWide:
+            hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 8, 4, 2, true>), grid,
+                               dim3(512), 0, stream, g);
+            break;
+        case kDeep:
+            hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 4, 2, 4, true>), grid,
+                               dim3(512), 0, stream, g);
+            break;
+        case kPaired:
+            hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 2, 4, 4, 2, true>), grid,
+                               dim3(256), 0, stream, g);
+            break;
+        default:
+            hipLaunchKernelGGL((linear_tile_kernel<T, POWN, QOWN, 2, 4, 4, 2, 2, false>), grid,
+                               dim3(512), 0, stream, g);
+            break;
+        }
+        e = hipGetLastError();
     }
-    hipError_t e = hipGetLastError();
     if (e == hipSuccess && g.splits > 1) {
         const int64_t runs = static_cast<int64_t>(g.I) * ((g.J + 3) / 4);
         const int wgs = static_cast<int>(

@@ -49,3 +49,16 @@ def test_lookup_of_2_to_the_33_pieces():
     rows = torch.cat([C, torch.zeros(1, D, dtype=BF, device="cuda")])
     for i in range(0, N, 1 << 18):
         assert torch.equal(out[i:i + (1 << 18)], rows[lab[i:i + (1 << 18)].long()]), i
+
+
+def test_linear_of_2_to_the_30_unaligned_rows():
+    """2^23 tiles of 512 threads each: rows that are taken as they lie."""
+    need(80)
+    N, D = (1 << 30) + 77, 15
+    X = torch.zeros((N, D), dtype=BF, device="cuda")
+    X[:, 7] = (torch.arange(N, dtype=torch.int32, device="cuda") % 251).to(BF)
+    W = torch.ones((1, D), dtype=BF, device="cuda")
+    W[0, 7] = 2.0
+    Y = torch.full((N, 1), float("nan"), dtype=BF, device="cuda")
+    km.kmeans_linear(X, W, out=Y)
+    assert torch.equal(Y[:, 0], X[:, 7] * 2)
