@@ -1125,9 +1125,9 @@ void merge_kernel(const float *__restrict__ ws_score, const int32_t *__restrict_
 // bits.
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads)))
 void norms_kernel(const uint16_t *__restrict__ C, int K, int D, float *__restrict__ norms) {
-    const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int row = (blockIdx.y * gridDim.x + blockIdx.x) * 16 + (threadIdx.x >> 4);
     const int l = threadIdx.x & 15;
-    const bool live = row < K;
+    const bool live = row >= 0 && row < K;   // a grid of several rows may pass 2^31
     const float n = row_sq_norm16(C + static_cast<size_t>(live ? row : 0) * D, live ? D : 0, l);
     if (live && l == 0)
         norms[row] = n;
@@ -1191,8 +1191,11 @@ hipError_t launch_assign_ks(const Plan &pl, const uint16_t *X, const uint16_t *C
 }  // namespace
 
 hipError_t launch_norms(const uint16_t *C, int K, int D, float *norms, hipStream_t stream) {
-    const int blocks = (K + 15) / 16;
-    hipLaunchKernelGGL(norms_kernel, dim3(blocks), dim3(kThreads), 0, stream, C, K, D, norms);
+    // Less than 2^32 threads across; more workgroups go to a second dimension.
+    constexpr int kMaxGridX = 1 << 20;
+    const int blocks = (K + 15) / 16, across = min(blocks, kMaxGridX);
+    hipLaunchKernelGGL(norms_kernel, dim3(across, (blocks + across - 1) / across), dim3(kThreads), 0,
+                       stream, C, K, D, norms);
     return hipGetLastError();
 }
 

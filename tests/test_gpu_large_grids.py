@@ -62,3 +62,13 @@ def test_linear_of_2_to_the_30_unaligned_rows():
     Y = torch.full((N, 1), float("nan"), dtype=BF, device="cuda")
     km.kmeans_linear(X, W, out=Y)
     assert torch.equal(Y[:, 0], X[:, 7] * 2)
+
+
+def test_norms_of_2_to_the_28_rows():
+    need(20)
+    K = (1 << 28) + 21
+    C = torch.ones((K, 16), dtype=BF, device="cuda")
+    C[-5:] = 2.0
+    norms = torch.full((K,), float("nan"), device="cuda")
+    km.kmeans_centroid_norms(C, norms)
+    assert bool((norms[:-5] == 16.0).all()) and bool((norms[-5:] == 64.0).all())
