@@ -37,8 +37,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define KM_INLINE __attribute__((always_inline))
 
 constexpr uint32_t kOutOfRange = 0x80000000u;
-constexpr int64_t kMaxWidth = 1 << 20;   // D, F and row strides: 64 rows stay below 2^31 bytes
-constexpr int kMaxKSplits = 64;
 
 // ---- activations -----------------------------------------------------------
 
@@ -126,30 +124,6 @@ __device__ __forceinline__ float activate_grad(int act, float z, float d) {
 }
 
 // ---- the product -----------------------------------------------------------
-
-struct Epilogue {
-    const void *bias;       // [J] or null
-    const void *residual;   // [I][J] or null
-    int64_t ldr;
-    void *out;              // [I][J]
-    int64_t ldo;
-    void *pre;              // [I][J] or null
-    int64_t ldp;
-    int act;
-};
-
-struct Product {
-    const void *P, *Q;
-    int64_t ldp, ldq;       // elements between rows as they lie in memory
-    int I, J, K;
-    bool dma;               // both operands' rows are 16-byte aligned and of whole chunks of 8
-    int shape;              // Shape
-    int k_chunk;            // k per split, a multiple of kTileK
-    int splits;
-    int first_wg;           // of this launch
-    float *partial;         // [splits][I][J] fp32 when splits > 1
-    Epilogue epi;
-};
 
 template <int ACT, int V>
 __device__ __forceinline__ void activate_run(float (&v)[V]) {
@@ -976,8 +950,6 @@ void linear_rows_kernel(const Product g) {
 // 4096 with silu 35 us (201 MB, 5.8 TB/s); the activation is chosen at compile
 // time (20000 x 1111 with gelu: 12 us less for the call than by a branch per
 // value).
-constexpr int kDzThreads = 256;
-constexpr int kDzRows = 4;
 template <typename T, int ACT>
 __global__ __launch_bounds__(kDzThreads)
 void linear_dz_kernel(const void *dY, int64_t ldy, const void *pre, int64_t ldp, int N, int F,
@@ -1073,104 +1045,6 @@ void linear_zero_kernel(uint16_t *p, int64_t rows, int cols, int64_t ld) {
 
 // ---- launch ----------------------------------------------------------------
 
-size_t align_up(size_t n) { return (n + 255) & ~size_t(255); }
-
-// Rows that DMA may read: 16-byte aligned base and stride.
-bool rows_aligned(const void *p, int64_t ld) {
-    return aligned(p, 16) && ld % 8 == 0;
-}
-
-// A product's workspace: its partial sums.
-size_t partial_bytes(const Product &g) {
-    return g.splits > 1 ? static_cast<size_t>(g.splits) * g.I * g.J * sizeof(float) : 0;
-}
-
-// How one product is tiled and split.  Rates of the shapes on an MI355X, bf16,
-// as the whole call (the library's product beside it):
-//   8192 x 4096 x 4096   kWide 1310-1440 TFLOP/s by operand order, kPaired
-//                        1110-1200, kDeep 1020-1100 (library 1440, 1260, 1140)
-//   2048 x 2048 x 2048   kDeep 21.5 us, kPaired 24.6-27.4, kWide 45 (21.4-25.3)
-//   65536 x 512 x 128    kPaired 18.1 us, kWide 22.6, kDeep 22.0 (18.6)
-// kWide halves the LDS reads per flop; kDeep keeps three tiles on their way
-// where one workgroup per CU is all there is; kPaired overlaps one workgroup's
-// epilogue with the other's products where k is short.
-enum Shape {
-    kWide,      // 256 x 256 tiles, two stages, one workgroup of eight waves per CU
-    kDeep,      // 128 x 128, four stages, one workgroup of eight waves per CU
-    kPaired,    // 128 x 128, two stages, two workgroups of four waves per CU
-    kRows,      // at most kMaxFewRows rows: weights straight into fragments (forward only)
-    kUnaligned  // 128 x 128, two stages through registers, two of eight waves per CU
-};
-
-constexpr int kMaxFewRows = 16;
-
-int64_t tiles_of(const Product &g, int side) {
-    return ((static_cast<int64_t>(g.I) + side - 1) / side) *
-           ((static_cast<int64_t>(g.J) + side - 1) / side);
-}
-
-// Chooses the shape and the splits of k with the least estimated time (us),
-// which it returns.
-double plan_product(Product &g, int compute_units) {
-    const int64_t k_tiles = (g.K + kTileK - 1) / kTileK;
-    struct Cost {
-        Shape shape;
-        int side, per_cu;
-        double round;     // us per staged tile of a full round of workgroups
-        double single;    // the same with one workgroup per CU
-        double fixed;     // us per round: first copies, epilogue
-    };
-    static constexpr Cost kAligned[] = {{kWide, 256, 1, 1.50, 1.50, 4.0},
-                                        {kDeep, 128, 1, 0.50, 0.50, 2.0},
-                                        {kPaired, 128, 2, 0.92, 0.65, 1.5}};
-    static constexpr Cost kOther[] = {{kUnaligned, 128, 2, 1.6, 1.1, 2.0}};
-    const Cost *costs = g.dma ? kAligned : kOther;
-    const int kinds = g.dma ? 3 : 1;
-    double best = 1e30;
-    for (int c = 0; c < kinds; ++c) {
-        const Cost &k = costs[c];
-        const int64_t tiles = tiles_of(g, k.side);
-        for (int64_t s = 1; s <= std::min<int64_t>(kMaxKSplits, k_tiles); s *= 2) {
-            const int64_t per = (k_tiles + s - 1) / s;
-            const int64_t wgs = tiles * ((k_tiles + per - 1) / per);
-            const int64_t slots = static_cast<int64_t>(compute_units) * k.per_cu;
-            const int64_t rest = wgs % slots;       // workgroups of the last round
-            double t = static_cast<double>(wgs / slots) * (per * k.round + k.fixed);
-            if (rest > 0)
-                t += per * (rest <= compute_units ? k.single : k.round) + k.fixed;
-            if (s > 1)    // the join's launch, and the partial sums written and read
-                t += 4.5 + static_cast<double>(s) * g.I * g.J * 8e-6 / 4.0;
-            if (t < best) {
-                best = t;
-                g.shape = k.shape;
-                g.k_chunk = static_cast<int>(per * kTileK);
-                g.splits = static_cast<int>((k_tiles + per - 1) / per);
-            }
-        }
-    }
-    return best;
-}
-
-// How linear_dz_kernel divides N rows of F values.
-struct RowPlan {
-    int64_t ld;                 // values from one written row to the next
-    int lanes_log2, rows_per_wg, row_wgs, col_wgs;
-    RowPlan(int64_t N, int64_t F, int compute_units) : ld((F + 7) / 8 * 8), lanes_log2(0) {
-        const int64_t col_groups = ld / 8;
-        while (lanes_log2 < 6 && (1 << lanes_log2) < col_groups)
-            ++lanes_log2;
-        col_wgs = static_cast<int>((col_groups + (1 << lanes_log2) - 1) >> lanes_log2);
-        // About eight workgroups per CU, each at least one round of rows; few
-        // enough that the column partials stay small beside dY.
-        const int64_t rows_round = kDzRows * (kDzThreads >> lanes_log2);
-        int64_t wgs = std::min<int64_t>(512, std::max<int64_t>(1, 8 * compute_units / col_wgs));
-        wgs = std::min<int64_t>(wgs, (N + rows_round - 1) / rows_round);
-        rows_per_wg = static_cast<int>((N + wgs - 1) / wgs);
-        row_wgs = static_cast<int>((N + rows_per_wg - 1) / rows_per_wg);
-    }
-    size_t bytes(int64_t N) const { return align_up(static_cast<size_t>(N) * ld * 2); }
-};
-
 template <typename T, int ACT>
 hipError_t launch_dz(const RowPlan &r, const void *dY, int64_t ldy, const void *pre, int64_t ldp,
                      int N, int F, void *dZ, float *col_partial, hipStream_t stream) {
@@ -1178,44 +1052,6 @@ hipError_t launch_dz(const RowPlan &r, const void *dY, int64_t ldy, const void *
                        stream, dY, ldy, pre, ldp, N, F, r.lanes_log2, r.rows_per_wg, dZ, r.ld,
                        col_partial);
     return hipGetLastError();
-}
-
-// An operand as its caller has it, and whether and where in the workspace it
-// is laid out anew, with rows that the global-to-LDS copies take.
-struct Operand {
-    const void *p;
-    int64_t ld, rows, cols;
-    bool moved;
-    size_t at;
-    bool fits() const { return rows_aligned(p, ld) && cols % 8 == 0; }
-};
-
-// Plans a product of operands, some of which may not fit the copies: as they
-// lie through registers (kUnaligned), or laid out anew first where that costs
-// less, at workspace offset `bytes` on (as it lies, moved: forward 4133 x 515 x
-// 1001 24 us, 33; 8192 x 2001 x 2000 140 us, 114; gradients 263 us, 198).
-void plan_operands(Product &g, Operand *const *ops, int n, int compute_units, size_t &bytes) {
-    double moves = 0;
-    g.dma = true;
-    for (int i = 0; i < n; ++i)
-        if (!ops[i]->fits()) {
-            g.dma = false;
-            moves += 5.0 + static_cast<double>(ops[i]->rows) * ops[i]->cols * 4e-6 / 2.5;
-        }
-    const double as_is = plan_product(g, compute_units);
-    if (g.dma)
-        return;
-    Product moved = g;
-    moved.dma = true;
-    if (plan_product(moved, compute_units) + moves >= as_is)
-        return;
-    g = moved;
-    for (int i = 0; i < n; ++i)
-        if (!ops[i]->fits()) {
-            ops[i]->moved = true;
-            ops[i]->at = bytes;
-            bytes += RowPlan(ops[i]->rows, ops[i]->cols, compute_units).bytes(ops[i]->rows);
-        }
 }
 
 // Lays the operand out anew if it was planned so, and points (p, ld) to it.
@@ -1440,28 +1276,14 @@ extern "C" kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const 
         (pre && (st = check_rows("pre", pre, F, pre_stride)) != KMEANS_OK))
         return st;
 
-    Product g{};
-    g.P = X;
-    g.ldp = x_stride;
-    g.Q = W;
-    g.ldq = w_stride;
-    g.I = static_cast<int>(N);
-    g.J = static_cast<int>(F);
-    g.K = static_cast<int>(D);
+    const int cus = device_compute_units();
+    Operand x{X, x_stride, N, D, false, 0}, w{W, w_stride, F, D, false, 0};
+    size_t bytes = 0;
+    Product g = forward_product(x, w, cus, bytes);
     g.epi = {bias, residual, residual_stride, Y, y_stride, pre, pre_stride, activation};
     if (tiles_of(g, 128) > kMaxRows / kMaxKSplits)
         return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x F=%lld: too many outputs",
                     static_cast<long long>(N), static_cast<long long>(F));
-    const int cus = device_compute_units();
-    Operand x{X, x_stride, N, D, false, 0}, w{W, w_stride, F, D, false, 0};
-    size_t bytes = 0;
-    if (N <= kMaxFewRows) {
-        g.shape = kRows;
-        g.splits = 1;
-    } else {
-        Operand *const ops[] = {&x, &w};
-        plan_operands(g, ops, 2, cus, bytes);
-    }
     const size_t part_at = bytes;
     bytes += partial_bytes(g);
     std::optional<WorkspaceLease> lease;
@@ -1531,33 +1353,22 @@ extern "C" kmeans_status_t kmeans_linear_grad(const void *dY, int64_t dy_stride,
         p.col_at = at;
         at += align_up(static_cast<size_t>(p.rows.row_wgs) * F * sizeof(float));
     }
-    p.dx.ldq = w_stride;
-    p.dx.I = static_cast<int>(N);
-    p.dx.J = static_cast<int>(D);
-    p.dx.K = static_cast<int>(F);
-    p.dx.Q = W;
-    p.dx.epi = {nullptr, nullptr, 0, dX, dx_stride, nullptr, 0, KMEANS_ACT_NONE};
-    p.dw.ldq = x_stride;
-    p.dw.I = static_cast<int>(F);
-    p.dw.J = static_cast<int>(D);
-    p.dw.K = static_cast<int>(N);
-    p.dw.Q = X;
-    p.dw.epi = {nullptr, nullptr, 0, dW, dw_stride, nullptr, 0, KMEANS_ACT_NONE};
-    if (tiles_of(p.dx, 128) > kMaxRows / kMaxKSplits ||
-        tiles_of(p.dw, 128) > kMaxRows / kMaxKSplits)
-        return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x D=%lld: too many outputs",
-                    static_cast<long long>(N), static_cast<long long>(D));
     // dZ fits the copies (zeros past F in its last chunk); X and W may not.
-    Operand *const w = &p.w, *const x = &p.x;
     size_t part = 0;
     if (dX) {
-        plan_operands(p.dx, &w, 1, cus, at);
+        p.dx = input_grad_product(N, p.w, cus, at);
+        p.dx.epi = {nullptr, nullptr, 0, dX, dx_stride, nullptr, 0, KMEANS_ACT_NONE};
         part = std::max(part, partial_bytes(p.dx));
     }
     if (dW) {
-        plan_operands(p.dw, &x, 1, cus, at);
+        p.dw = weight_grad_product(F, p.x, cus, at);
+        p.dw.epi = {nullptr, nullptr, 0, dW, dw_stride, nullptr, 0, KMEANS_ACT_NONE};
         part = std::max(part, partial_bytes(p.dw));
     }
+    if ((dX && tiles_of(p.dx, 128) > kMaxRows / kMaxKSplits) ||
+        (dW && tiles_of(p.dw, 128) > kMaxRows / kMaxKSplits))
+        return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x D=%lld: too many outputs",
+                    static_cast<long long>(N), static_cast<long long>(D));
     p.part_at = at;
     p.bytes = at + part;
     std::optional<WorkspaceLease> lease;

@@ -1,6 +1,7 @@
 """The linear operators (HIP, through the public binding) at shapes chosen for
-the code path they take: rows of few values, against the definitions in fp64.
-Bounds and their derivation: ``codebook_reference``."""
+the code path they take, against the definitions in fp64: rows of few values,
+and every kernel that the plan chooses between.  Bounds and their derivation:
+``codebook_reference``."""
 
 import pytest
 
@@ -9,6 +10,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 km = pytest.importorskip("means_nearest_centroid_amd")
 import codebook_reference as ref  # noqa: E402
+from linear_paths import PATHS  # noqa: E402
 
 BF, FP = torch.bfloat16, torch.float16
 
@@ -48,3 +50,37 @@ def test_forward_of_narrow_rows(N, D, F, dtype):
     Y, Z = km.kmeans_linear(X, W, bias=b, activation="relu", save_pre=True)
     ref.check(Y, y, yb, "Y")
     ref.check(Z, z, zb, "Z")
+
+
+# ---- every kernel of the plan ----------------------------------------------
+
+def rows(t, extra):
+    """The same values, `extra` more (NaN) between rows."""
+    wide = torch.full((t.shape[0], t.shape[1] + extra), float("nan"), dtype=t.dtype,
+                      device="cuda")
+    v = wide[:, :t.shape[1]]
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("N,D,F,extra", [p[:4] for p in PATHS])
+def test_forward_of_every_kernel(N, D, F, extra, dtype):
+    X, W = rand((N, D), dtype, 1), rand((F, D), dtype, 2, D ** -0.5)
+    b, R = rand((F,), dtype, 3), rand((N, F), dtype, 4)
+    y, z, yb, zb = ref.linear(X, W, b, R, "gelu_tanh")
+    Y, Z = km.kmeans_linear(rows(X, extra), rows(W, extra), bias=b, residual=R,
+                            activation="gelu_tanh", save_pre=True)
+    ref.check(Y, y, yb, "Y")
+    ref.check(Z, z, zb, "Z")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("N,D,F,extra", [p[:4] for p in PATHS])
+def test_gradients_of_every_kernel(N, D, F, extra, dtype):
+    X, W = rand((N, D), dtype, 1), rand((F, D), dtype, 2, D ** -0.5)
+    dY, Z = rand((N, F), dtype, 3, 0.25), rand((N, F), dtype, 4, 2.0)
+    want = ref.linear_grad(dY, X, W, Z, "silu")
+    got = km.kmeans_linear_grad(dY, rows(X, extra), rows(W, extra), Z, "silu")
+    for name, g in zip(("dX", "dW", "db"), got):
+        ref.check(g, *want[name], name)
