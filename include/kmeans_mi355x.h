@@ -377,7 +377,9 @@ kmeans_status_t kmeans_linear(const void *X, int64_t x_stride, const void *W, in
  *
  * dZ is rounded once to `dtype` (the matrix instructions take 16-bit
  * operands; an fp16 dZ past 65504 becomes infinite), dbias sums it
- * unrounded.  dZ (2 bytes per element of dY), partial sums where few tiles
+ * unrounded.  A pre-activation that is infinite has the slope 0 or 1 (an fp16
+ * Z past 65504 was kept so), a NaN the slope NaN
+ * (KMEANS_ACT_RELU: 1).  dZ (2 bytes per element of dY), partial sums where few tiles
  * fill the GPU, and copies of large X and W whose rows are not 16-byte aligned
  * are the stream's workspace.
  */
@@ -403,13 +405,15 @@ typedef struct {
  *     n = sqrt(sum over the list of sum_j src_j^2)     (fp64 sums)
  *     dst = src * min(1, max_norm / (n + 1e-6))        (fp32, rounded once)
  *
- * norm (fp32 [1], device) receives n.  `list` is a host array, read before
+ * norm (fp32 [1], device) receives n (infinite past the largest fp32, and the
+ * factor, taken from this fp32 n, then 0).  `list` is a host array, read before
  * the call returns; its buffers must not overlap one another, except that a
  * dst may be its own src.  A NaN anywhere makes n and every output NaN, an
  * infinity makes n infinite and the outputs 0 or NaN, as the formula says.
  * When nothing is to be clipped, dst == src tensors are not written.
  * kmeans_gradient_norm computes n alone and ignores dst.  count and numel
- * may be 0 (n = 0).  max_norm must be >= 0.
+ * may be 0 (n = 0).  max_norm must be >= 0.  Lists of more than 96 tensors or
+ * 320 KiB keep partial sums in the stream's workspace.
  */
 kmeans_status_t kmeans_gradient_norm(const kmeans_gradient_t *list, int64_t count, float *norm,
                                      hipStream_t stream);

@@ -22,6 +22,10 @@ its gradient and the clipping also fp32):
     dC = kmeans_lookup_grad(dY, labels, K, scale=1.0)
     dX, dW, db = kmeans_linear_grad(dY, X, W, Z, activation="gelu")
     norm, _ = kmeans_clip_gradients([dW, db, dC], max_norm=1.0)
+
+Autograd does not see these calls: their results carry no gradient function,
+whatever their inputs require, and the gradients are the calls above (inside a
+``torch.autograd.Function``, say, whose ``backward`` makes them).
 """
 
 from __future__ import annotations
@@ -533,7 +537,9 @@ def kmeans_linear_grad(dY, X, W, Z=None, activation: str = "none", bias: bool = 
     """Gradients of ``kmeans_linear`` for the output gradient ``dY``:
     ``(dX, dW, dbias)``, ``None`` for one not asked for.  ``Z``: the
     pre-activations that ``kmeans_linear`` kept (not needed for ``"none"``).
-    The residual's gradient is ``dY`` itself."""
+    The residual's gradient is ``dY`` itself.  With an activation, ``dY *
+    act'(Z)`` is rounded to the inputs' 16-bit type before the products (the
+    bias's sum takes it unrounded)."""
     import torch
     x_shape = X.shape
     X = _flat(X, "X")

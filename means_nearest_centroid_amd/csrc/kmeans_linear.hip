@@ -449,12 +449,15 @@ __device__ __forceinline__ void tile_of(int b, int ni, int nj, int splits, int &
 // distinct arrays and the loop is unrolled by S so that the compiler can tell
 // an LDS read of one stage from a copy into another.
 //
-// Bound by the matrix pipe where k is long (8192 x 4096 x 4096 forward 192 us,
-// 1430 TFLOP/s), and by the epilogue's bytes where it is short or the epilogue
-// has more to move: nothing overlaps it with one workgroup per CU.  16384 x
-// 4096 x 4096 with gelu, residual and pre-activations kept is 484 us, of which
-// about 37 are the residual, 24 the pre-activations and 10 to 20 the activation
-// (all residual loads ahead of both passes spill: 505).
+// Where k is long the matrix pipe is busy 0.66 to 0.69 of the time (8192 x 4096
+// x 4096 forward 192 us, 1430 TFLOP/s; a kernel of matrix instructions alone
+// reaches 0.87 by the same counters); waves wait at the barriers between tiles
+// for the rest, and while the first copies and the epilogue run alone: nothing
+// overlaps them with one workgroup per CU.  Where k is short or the epilogue has
+// more to move, its bytes bound it: 16384 x 4096 x 4096 with tanh-gelu, residual
+// and pre-activations kept is 484 us (busy 0.54), of which about 37 are the
+// residual, 24 the pre-activations and 10 to 20 the activation (all residual
+// loads ahead of both passes spill: 505).
 template <int I>
 using Index = std::integral_constant<int, I>;
 
@@ -887,8 +890,9 @@ void linear_join_kernel(const Product g, int join_wgs, const BiasSums bias) {
 // alignment; the last values of a row that is no multiple of 8 are loaded one
 // by one.  1 x 4096 x 4096: 7.9 us (33.6 MB, 4.2 TB/s: 256 workgroups of 16
 // waves start and end together, which a stream this short feels).  Against the
-// tile kernels, per call: 8.5 us instead of 11.5, 16 rows 9.3 instead of 11.6,
-// but 32 rows (two row blocks) 12.9 instead of 12.7, so it stops at 16.
+// tile kernels, per call without an epilogue: 8.5 us instead of 11.5, 16 rows
+// 9.3 instead of 11.6, but 32 rows (two row blocks) 12.9 instead of 12.7, so it
+// stops at 16.
 constexpr int kRowsUnroll = 4;
 constexpr int kRowsStep = 32 * kRowsUnroll;
 template <typename T, int WAVES>
