@@ -241,9 +241,9 @@ def _draw(logits, u, settings):
     before = torch.cat([torch.zeros_like(sums[:, :1]), sums[:, :-1]], 1)
     kept = ((p >= 1) | (before < p * sums[:, -1:]) | (rank == 0)) & (w >= least)
     kept &= (t > 0) | (rank == 0)
-    w = torch.zeros_like(w).scatter_(1, order, torch.where(kept, w, 0.0))
-    sums = torch.cumsum(w, 1)
-    label = (sums <= u.double()[:, None] * sums[:, -1:]).sum(1)
+    sums = torch.cumsum(torch.where(kept, w, 0.0), 1)
+    at = (sums <= u.double()[:, None] * sums[:, -1:]).sum(1, keepdim=True)
+    label = order.gather(1, at.clamp(max=K - 1))[:, 0]
     return torch.where(sums[:, -1] > 0, label, -1).to(torch.int32)
 
 
@@ -369,10 +369,10 @@ def _exact_draw(logits, u, settings):
         if p < 1:
             run_sum = np.cumsum(w[ranked])
             ranked = ranked[:int(np.searchsorted(run_sum, p * run_sum[-1])) + 1]
-        kept = np.sort(ranked[w[ranked] >= least])
-        run_sum = np.cumsum(w[kept])
-        labels[i] = kept[min(int(np.searchsorted(run_sum, u[i] * run_sum[-1], side="right")),
-                             len(kept) - 1)]
+        ranked = ranked[w[ranked] >= least]
+        run_sum = np.cumsum(w[ranked])
+        labels[i] = ranked[min(int(np.searchsorted(run_sum, u[i] * run_sum[-1], side="right")),
+                               len(ranked) - 1)]
     return torch.from_numpy(labels)
 
 
