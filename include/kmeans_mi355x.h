@@ -1,7 +1,8 @@
 /*
  * kmeans_mi355x.h -- C ABI of the MI355X (gfx950) k-means assignment library
- * (with the centroid update that follows assignment in a Lloyd iteration, and
- * the operators that train a centroid table by gradients inside a model).
+ * (with the centroid update that follows assignment in a Lloyd iteration, the
+ * operators that train a centroid table by gradients inside a model, and those
+ * by which a model that predicts labels serves).
  *
  * The operation.  flashlib PR #22, "Optimize Blackwell k-means assignment
  * reduction", Summary: the assignment step scores every (point, centroid)
@@ -47,7 +48,7 @@
 extern "C" {
 #endif
 
-#define KMEANS_ABI_VERSION 8
+#define KMEANS_ABI_VERSION 9
 
 /* Supported feature dimension: 16 <= D <= 512 and D % 16 == 0. */
 #define KMEANS_MIN_D 16
@@ -420,10 +421,169 @@ kmeans_status_t kmeans_gradient_norm(const kmeans_gradient_t *list, int64_t coun
 kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t count,
                                       float max_norm, float *norm, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Predicting labels.  A model that generates labels of a table (codes, tokens)
+ * normalises its hidden rows, multiplies them with the table's rows or a head
+ * of its own, and draws a label for each row from the scores; kmeans_lookup
+ * takes the labels on.  In serving the products run on 8-bit operands:
+ * kmeans_rms_norm writes them, with the residual's addition in the same pass,
+ * kmeans_quantize makes the weights, kmeans_linear_fp8 multiplies them,
+ * kmeans_sample draws.  In training the norm has its gradient, and the products
+ * are kmeans_linear and kmeans_linear_grad (8-bit weights have no gradient here).
+ *
+ * Layouts as in the section before: rows of unit column stride, strides in
+ * elements, the alignment of one element, fast loads at 16 bytes.
+ *
+ * 8-bit values are OCP e4m3 (4 exponent and 3 mantissa bits, largest value 448,
+ * no infinities), each block of 128 columns with one fp32 scale: value = scale
+ * times the e4m3 number.  The last block of a row may be narrower.
+ *
+ *     scale = max|v| / 448 over the block (fp32; 1 where all are zero, and no
+ *             less than 2^-126),   q = v / scale rounded once
+ *
+ * A block with a NaN or an infinity has that magnitude as its scale, and at
+ * least one NaN.
+ */
+
+/*
+ * Root-mean-square norm, with the residual's addition before it:
+ *
+ *     H = X + residual                          (fp32; written rounded once)
+ *     r_i = 1 / sqrt(mean_j H_ij^2 + eps)       (fp32, of the unrounded H)
+ *     y = H r w                                 (fp32)
+ *     Y = y rounded once, or Q and scales: y by blocks of 1 x 128
+ *
+ *   X         [N][D] of `dtype`.   residual  [N][D] of `dtype`, or NULL.
+ *   weight    [D] of `dtype`, or NULL (w = 1).
+ *   N, D      0 <= N < 2^31, 1 <= D <= 2^20.
+ *   eps       >= 0 (with 0 a row of zeros gives NaN, as the formula says).
+ *   sum       [N][D] of `dtype`, or NULL: H, which the next layer's residual and
+ *             kmeans_rms_norm_grad take.  May be X or residual itself.
+ *   Y         [N][D] of `dtype`, or NULL; may be X itself.
+ *   Q         [N][D] e4m3 and scales fp32 [N][ceil(D / 128)], or NULL.  One of
+ *             Y and Q is given.
+ *
+ * Squares are summed in fp32: a row with a value of magnitude 2^63 or more gives
+ * zeros (or NaN).
+ */
+kmeans_status_t kmeans_rms_norm(const void *X, int64_t x_stride, const void *residual,
+                                int64_t residual_stride, const void *weight, int64_t N, int64_t D,
+                                int32_t dtype, float eps, void *sum, int64_t sum_stride, void *Y,
+                                int64_t y_stride, void *Q, int64_t q_stride, float *scales,
+                                int64_t scales_stride, hipStream_t stream);
+
+/*
+ * Gradient of kmeans_rms_norm for the gradient dY of its output Y, at H (the sum
+ * it wrote, or X where there was no residual).  With g = dY w:
+ *
+ *     dX = r g - H r^3 mean_j(g H) + dH         (fp32, rounded once)
+ *     dweight = sum_i dY_i H_i r_i              (fp32, rounded once)
+ *
+ *   dY, H     [N][D] of `dtype`.   weight  [D] of `dtype`, or NULL (w = 1).
+ *   dH        [N][D] of `dtype`, or NULL: the gradient that reaches the sum
+ *             itself, along the residual path.
+ *   dX        [N][D] of `dtype`, written: the gradient of X and of the residual.
+ *   dweight   [D] of `dtype`, written, or NULL (N == 0: zeros).
+ *
+ * dweight's partial sums are the stream's workspace: at most D floats for each of
+ * four workgroups per compute unit (D > 16384: and one float per row).
+ */
+kmeans_status_t kmeans_rms_norm_grad(const void *dY, int64_t dy_stride, const void *H,
+                                     int64_t h_stride, const void *weight, const void *dH,
+                                     int64_t dh_stride, int64_t N, int64_t D, int32_t dtype,
+                                     float eps, void *dX, int64_t dx_stride, void *dweight,
+                                     hipStream_t stream);
+
+/*
+ * Values in 8 bits with scales, by blocks of block_rows x 128 (block_rows: 1 for
+ * the rows of X, 128 for weights; the last block of either may be smaller).
+ *
+ *   X         [N][D] of `dtype`.   N, D  0 <= N < 2^31, 1 <= D <= 2^20.
+ *   Q         [N][D] e4m3, written.
+ *   scales    fp32 [ceil(N / block_rows)][ceil(D / 128)], written.
+ */
+kmeans_status_t kmeans_quantize(const void *X, int64_t x_stride, int64_t N, int64_t D,
+                                int32_t dtype, int32_t block_rows, void *Q, int64_t q_stride,
+                                float *scales, int64_t scales_stride, hipStream_t stream);
+
+/*
+ * Linear layer on 8-bit operands:
+ *
+ *     Z_ij = sum_b x_scales[i][b] w_scales[j / 128][b] (sum_{k in block b} X_ik W_jk)
+ *     Y = act(Z + bias) + residual              (fp32, rounded once)
+ *
+ *   X         [N][D] e4m3, x_scales fp32 [N][ceil(D / 128)].
+ *   W         [F][D] e4m3, w_scales fp32 [ceil(F / 128)][ceil(D / 128)].
+ *   bias      [F] of `dtype`, or NULL.   residual  [N][F] of `dtype`, or NULL.
+ *   Y         [N][F] of `dtype` (any kmeans_dtype_t), written (may be `residual`
+ *             itself).
+ *   N, D, F   0 <= N < 2^31, 1 <= D, F <= 2^20; strides at most 2^20.
+ *
+ * Blocks are summed in fp32, each scaled in fp32.  Operands whose rows are not
+ * 16-byte aligned runs of 16 (address, stride and D) are laid out anew in the
+ * stream's workspace for more than 16 rows; the partial sums of products of few
+ * tiles lie there too.
+ */
+kmeans_status_t kmeans_linear_fp8(const void *X, int64_t x_stride, const float *x_scales,
+                                  int64_t xs_stride, const void *W, int64_t w_stride,
+                                  const float *w_scales, int64_t ws_stride, const void *bias,
+                                  const void *residual, int64_t residual_stride, int64_t N,
+                                  int64_t D, int64_t F, int32_t dtype, int32_t activation, void *Y,
+                                  int64_t y_stride, hipStream_t stream);
+
+/* Settings of kmeans_sample: a value for all rows, or an array (device, fp32 or
+ * int32 [N]) of one for each, which goes before it where it is not NULL. */
+typedef struct {
+    float temperature;          /* >= 0; 0: the largest logit */
+    float top_p;                /* in [0, 1]; 1: no limit */
+    float min_p;                /* in [0, 1]; 0: no limit */
+    int32_t top_k;              /* >= 0; 0: no limit */
+    const float *temperatures;
+    const float *top_ps;
+    const float *min_ps;
+    const int32_t *top_ks;
+} kmeans_sampling_t;
+
+/*
+ * A label for each row of logits, from given random numbers.  A row's labels are
+ * ordered by logit, largest first, equal ones by index; with z the largest logit
+ * label i weighs w_i = exp((logits_i - z) / temperature).  Kept are the labels
+ * that belong to all of
+ *
+ *     the first top_k;
+ *     the shortest run from the first on with at least top_p of the weight of
+ *     the first top_k (one label at least);
+ *     those with w_i >= min_p
+ *
+ * and the result is the first label in that order at which the running weight of
+ * the kept exceeds `uniform` times their whole weight.  So a uniform of 0 gives
+ * the largest logit, and the result does not decrease in rank as it grows.
+ *
+ * Weights are multiples of 2^-43 (a label below 2^-44 is never drawn) in 64-bit
+ * integers, whose sums are exact.  A logit of -infinity or NaN is never drawn, nor
+ * counted; a row that has no other gets the label -1 (for which kmeans_lookup
+ * gives zeros).  Logits of +infinity share the row between them.  A temperature
+ * that is 0 (in the array also one below 0 or NaN) gives the lowest index of the
+ * largest logit.  Array values beyond their ranges count as the nearest in range,
+ * a NaN as no limit; a uniform below 0 or NaN counts as 0, one of 1 or more gives
+ * the last label kept.
+ *
+ *   logits    [N][K] of `dtype` (any kmeans_dtype_t), rows logits_stride apart.
+ *   N, K      0 <= N < 2^31, 1 <= K <= 2^20.
+ *   uniforms  fp32 [N].
+ *   labels    [N] of `label_type`, written.
+ *   settings  a host struct, read before the call returns.
+ */
+kmeans_status_t kmeans_sample(const void *logits, int64_t logits_stride, int64_t N, int64_t K,
+                              int32_t dtype, const float *uniforms,
+                              const kmeans_sampling_t *settings, void *labels, int32_t label_type,
+                              hipStream_t stream);
+
 /*
  * The workspace of `stream` on the current device.  kmeans_assign's K-split
  * path, kmeans_update, kmeans_lookup_grad, kmeans_linear, kmeans_linear_grad,
- * kmeans_gradient_norm and kmeans_clip_gradients take their scratch from one
+ * kmeans_gradient_norm, kmeans_clip_gradients, kmeans_rms_norm_grad and
+ * kmeans_linear_fp8 take their scratch from one
  * device buffer per (device, stream), kept between calls: a stream-ordered
  * allocation and free on every call costs more host time than a small call's
  * kernels.  It grows

@@ -23,6 +23,15 @@ its gradient and the clipping also fp32):
     dX, dW, db = kmeans_linear_grad(dY, X, W, Z, activation="gelu")
     norm, _ = kmeans_clip_gradients([dW, db, dC], max_norm=1.0)
 
+A model that predicts labels has the norm with its gradient, the linear layer on
+8-bit operands, and the draw of a label from each row of scores:
+
+    Q, scales, H = kmeans_rms_norm(X, weight, residual, quantize=True)
+    W8, w_scales = kmeans_quantize(W, rows=128)                 # once
+    logits = kmeans_linear_fp8(Q, scales, W8, w_scales, dtype=torch.float32)
+    labels = kmeans_sample(logits, uniforms, temperature=0.8, top_k=50, top_p=0.95)
+    dX, dw = kmeans_rms_norm_grad(dY, H, weight, dH=dH)
+
 Autograd does not see these calls: their results carry no gradient function,
 whatever their inputs require, and the gradients are the calls above (inside a
 ``torch.autograd.Function``, say, whose ``backward`` makes them).
@@ -124,6 +133,19 @@ def load_library(path: str = LIBRARY):
     lib.kmeans_gradient_norm.restype = ctypes.c_int
     lib.kmeans_clip_gradients.argtypes = [vp, i64, f32, vp, vp]
     lib.kmeans_clip_gradients.restype = ctypes.c_int
+    lib.kmeans_rms_norm.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, f32, vp, i64, vp, i64, vp,
+                                    i64, vp, i64, vp]
+    lib.kmeans_rms_norm.restype = ctypes.c_int
+    lib.kmeans_rms_norm_grad.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i32, f32, vp,
+                                         i64, vp, vp]
+    lib.kmeans_rms_norm_grad.restype = ctypes.c_int
+    lib.kmeans_quantize.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp]
+    lib.kmeans_quantize.restype = ctypes.c_int
+    lib.kmeans_linear_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, i64, i64,
+                                      i64, i32, i32, vp, i64, vp]
+    lib.kmeans_linear_fp8.restype = ctypes.c_int
+    lib.kmeans_sample.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, i32, vp]
+    lib.kmeans_sample.restype = ctypes.c_int
     lib.kmeans_release_workspace.argtypes = [vp]
     lib.kmeans_release_workspace.restype = ctypes.c_int
     lib.kmeans_last_error.argtypes = []
@@ -622,10 +644,252 @@ def kmeans_clip_gradients(grads, max_norm: float, out=None, norm=None, stream=No
     return norm, list(grads if out is None else out)
 
 
+# ---- predicting labels ----
+
+FP8_BLOCK = 128
+_FP8 = None
+
+
+def _fp8_rows(t, name, device=None, shape=None):
+    """Check rows of 8-bit values; their stride."""
+    global _FP8
+    import torch
+    if _FP8 is None:
+        _FP8 = torch.float8_e4m3fn
+    stride = _rows(t, name, shape=shape)
+    if t.dtype is not _FP8 or (device is not None and t.get_device() != device.index):
+        raise ValueError(f"{name} must be {_FP8} on {device or 'one GPU'} "
+                         f"(got {t.dtype} on {t.device})")
+    return stride
+
+
+def _scale_rows(t, name, device, shape):
+    import torch
+    stride = _rows(t, name, shape=shape)
+    if t.dtype is not torch.float32 or t.get_device() != device.index:
+        raise ValueError(f"{name} must be float32 on {device} (got {t.dtype} on {t.device})")
+    return stride
+
+
+def _blocks(D: int) -> int:
+    return (D + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _gain(t, D, like):
+    import torch
+    if (not isinstance(t, torch.Tensor) or t.dtype is not like.dtype
+            or t.get_device() != like.get_device() or t.numel() != D or not t.is_contiguous()):
+        raise ValueError(f"weight must be a contiguous {like.dtype} tensor of {D} elements on "
+                         f"{like.device}")
+    return t.data_ptr()
+
+
+def kmeans_rms_norm(X, weight=None, residual=None, eps: float = 1e-6, quantize: bool = False,
+                    out=None, scales=None, sum=None, stream=None):
+    """``H = X + residual``, ``Y = H / sqrt(mean(H^2) + eps) * weight`` along the
+    last dimension, one pass.  ``X``: ``[..., D]`` bf16, fp16 or fp32.  With
+    ``quantize`` the output is ``float8_e4m3fn`` with one fp32 scale for each
+    128 columns (``scales``: ``[..., ceil(D / 128)]``).  Returns ``Y`` or ``(Y,
+    scales)``, and ``H`` after it where there is a residual (``sum``: its
+    tensor, which may be ``residual`` itself)."""
+    import torch
+    lead, D = X.shape[:-1], X.shape[-1]
+    x = _flat(X, "X")
+    x_stride = _rows(x, "X")
+    code = _dtype(x, "X")
+    N = x.shape[0]
+    if weight is not None:
+        weight = _gain(weight, D, x)
+    r, r_stride, h, h_stride = None, 0, None, 0
+    if residual is not None:
+        r = _flat(residual, "residual")
+        r_stride = _rows(r, "residual", like=x, shape=(N, D))
+        r = r.data_ptr()
+        if sum is None:
+            sum = x.new_empty((*lead, D))
+        h = _flat(sum, "sum")
+        h_stride = _rows(h, "sum", like=x, shape=(N, D))
+        h = h.data_ptr()
+    elif sum is not None:
+        raise ValueError("sum needs residual")
+    y, y_stride, q, q_stride, s, s_stride = None, 0, None, 0, None, 0
+    if quantize:
+        if out is None:
+            out = torch.empty((*lead, D), dtype=torch.float8_e4m3fn, device=x.device)
+        q = _flat(out, "out")
+        q_stride = _fp8_rows(q, "out", x.device, (N, D))
+        q = q.data_ptr()
+        if scales is None:
+            scales = torch.empty((*lead, _blocks(D)), dtype=torch.float32, device=x.device)
+        s = _flat(scales, "scales")
+        s_stride = _scale_rows(s, "scales", x.device, (N, _blocks(D)))
+        s = s.data_ptr()
+    else:
+        if scales is not None:
+            raise ValueError("scales need quantize=True")
+        if out is None:
+            out = x.new_empty((*lead, D))
+        y = _flat(out, "out")
+        y_stride = _rows(y, "out", like=x, shape=(N, D))
+        y = y.data_ptr()
+    lib = load_library()
+    _launch(lib.kmeans_rms_norm, x.device, stream, x.data_ptr(), x_stride, r, r_stride, weight, N,
+            D, code, eps, h, h_stride, y, y_stride, q, q_stride, s, s_stride)
+    got = (out, scales) if quantize else (out,)
+    got = got if residual is None else (*got, sum)
+    return got if len(got) > 1 else out
+
+
+def kmeans_rms_norm_grad(dY, H, weight=None, eps: float = 1e-6, dH=None, need_dw: bool = True,
+                         stream=None):
+    """Gradients of ``kmeans_rms_norm`` for the gradient ``dY`` of its output in
+    ``X``'s type: ``(dX, dweight)``.  ``H``: the sum that it wrote (``X`` where
+    there was no residual); ``dH``: the gradient that reaches the sum along the
+    residual path, added to ``dX``, which is the residual's gradient too.
+    ``dweight`` is ``None`` without a weight or with ``need_dw`` false."""
+    shape = H.shape
+    H = _flat(H, "H")
+    h_stride = _rows(H, "H")
+    code = _dtype(H, "H")
+    N, D = H.shape
+    dY = _flat(dY, "dY")
+    y_stride = _rows(dY, "dY", like=H, shape=(N, D))
+    d, d_stride = None, 0
+    if dH is not None:
+        d = _flat(dH, "dH")
+        d_stride = _rows(d, "dH", like=H, shape=(N, D))
+        d = d.data_ptr()
+    dw = H.new_empty(D) if weight is not None and need_dw else None
+    if weight is not None:
+        weight = _gain(weight, D, H)
+    dX = H.new_empty(shape)
+    lib = load_library()
+    _launch(lib.kmeans_rms_norm_grad, H.device, stream, dY.data_ptr(), y_stride, H.data_ptr(),
+            h_stride, weight, d, d_stride, N, D, code, eps, dX.data_ptr(), D, _ptr(dw))
+    return dX, dw
+
+
+def kmeans_quantize(X, rows: int = 1, out=None, scales=None, stream=None):
+    """``X`` (``[N, D]`` bf16, fp16 or fp32) as ``float8_e4m3fn`` values with an
+    fp32 scale for each block of ``rows`` (1 or 128) x 128: ``(Q, scales)``."""
+    import torch
+    x_stride = _rows(X, "X")
+    code = _dtype(X, "X")
+    N, D = X.shape
+    if rows not in (1, FP8_BLOCK):
+        raise ValueError(f"rows must be 1 or {FP8_BLOCK} (got {rows})")
+    n = -(-N // rows)
+    if out is None:
+        out = torch.empty((N, D), dtype=torch.float8_e4m3fn, device=X.device)
+    q_stride = _fp8_rows(out, "out", X.device, (N, D))
+    if scales is None:
+        scales = torch.empty((n, _blocks(D)), dtype=torch.float32, device=X.device)
+    s_stride = _scale_rows(scales, "scales", X.device, (n, _blocks(D)))
+    lib = load_library()
+    _launch(lib.kmeans_quantize, X.device, stream, X.data_ptr(), x_stride, N, D, code, rows,
+            out.data_ptr(), q_stride, scales.data_ptr(), s_stride)
+    return out, scales
+
+
+def kmeans_linear_fp8(X, x_scales, W, w_scales, bias=None, residual=None,
+                      activation: str = "none", dtype=None, out=None, stream=None):
+    """``Y = act(X W^T + bias) + residual`` of ``float8_e4m3fn`` operands with
+    scales: ``X`` ``[..., D]`` with ``x_scales`` ``[..., ceil(D / 128)]`` (as
+    ``kmeans_rms_norm`` or ``kmeans_quantize`` with ``rows=1`` give them), ``W``
+    ``[F, D]`` with ``w_scales`` ``[ceil(F / 128), ceil(D / 128)]`` (``rows=128``).
+    ``dtype``: of ``Y``, bias and residual (bfloat16 when not given, or
+    ``out``'s)."""
+    import torch
+    lead = X.shape[:-1]
+    X = _flat(X, "X")
+    x_stride = _fp8_rows(X, "X")
+    device = X.device
+    N, D = X.shape
+    w_stride = _fp8_rows(W, "W", device)
+    F, d = W.shape
+    if d != D:
+        raise ValueError(f"X has D={D} but W has D={d}")
+    sx = _flat(x_scales, "x_scales")
+    xs_stride = _scale_rows(sx, "x_scales", device, (N, _blocks(D)))
+    ws_stride = _scale_rows(w_scales, "w_scales", device, (_blocks(F), _blocks(D)))
+    act = _activation(activation)
+    if out is None:
+        out = torch.empty((*lead, F), dtype=dtype or torch.bfloat16, device=device)
+    elif dtype is not None and out.dtype is not dtype:
+        raise ValueError(f"out must be {dtype} (got {out.dtype})")
+    y = _flat(out, "out")
+    y_stride = _rows(y, "out", shape=(N, F))
+    if y.get_device() != device.index:
+        raise ValueError(f"out must be on {device} (got {y.device})")
+    code = _dtype(y, "out")
+    if bias is not None:
+        bias = _bias(bias, F, y).data_ptr()
+    r, r_stride = None, 0
+    if residual is not None:
+        r = _flat(residual, "residual")
+        r_stride = _rows(r, "residual", like=y, shape=(N, F))
+        r = r.data_ptr()
+    lib = load_library()
+    _launch(lib.kmeans_linear_fp8, device, stream, X.data_ptr(), x_stride, sx.data_ptr(), xs_stride,
+            W.data_ptr(), w_stride, w_scales.data_ptr(), ws_stride, bias, r, r_stride, N, D, F,
+            code, act, y.data_ptr(), y_stride)
+    return out
+
+
+class _Sampling(ctypes.Structure):
+    """kmeans_sampling_t."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("temperatures", ctypes.c_void_p), ("top_ps", ctypes.c_void_p),
+                ("min_ps", ctypes.c_void_p), ("top_ks", ctypes.c_void_p)]
+
+
+def _setting(value, name, dtype, N, device, other):
+    """(value for all rows, address of one for each) of a setting."""
+    import torch
+    if isinstance(value, torch.Tensor):
+        return other, _vector(value, name, dtype, N, device).data_ptr()
+    return value, None
+
+
+def kmeans_sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None,
+                  stream=None):
+    """A label for each row of ``logits`` (``[..., K]`` bf16, fp16 or fp32) from
+    the random numbers ``uniforms`` (fp32 in ``[0, 1)``, one for each row): labels
+    in descending order of their logits, limited to the first ``top_k`` (0: all),
+    to the first with ``top_p`` of their weight and to those with ``min_p`` of the
+    largest weight, and the one at which their running weight exceeds ``uniform``
+    of the whole.  Each setting is a number or a tensor of one for each row (fp32,
+    ``top_k`` int32); a temperature of 0 takes the largest logit.  ``out``: int32
+    (made when not given) or int64.  A row without a finite logit gets -1."""
+    import torch
+    lead = logits.shape[:-1]
+    z = _flat(logits, "logits") if logits.dim() != 1 else logits.view(1, -1)
+    stride = _rows(z, "logits")
+    code = _dtype(z, "logits")
+    N, K = z.shape
+    device = z.device
+    _vector(uniforms, "uniforms", torch.float32, N, device)
+    if out is None:
+        out = torch.empty(lead, dtype=torch.int32, device=device)
+    elif out.numel() != N:
+        raise ValueError(f"out must have {N} elements (got {tuple(out.shape)})")
+    kind = _labels(out, device.index)
+    t, ts = _setting(temperature, "temperature", torch.float32, N, device, 1.0)
+    k, ks = _setting(top_k, "top_k", torch.int32, N, device, 0)
+    p, ps = _setting(top_p, "top_p", torch.float32, N, device, 1.0)
+    m, ms = _setting(min_p, "min_p", torch.float32, N, device, 0.0)
+    settings = _Sampling(t, p, m, k, ts, ps, ms, ks)
+    lib = load_library()
+    _launch(lib.kmeans_sample, device, stream, z.data_ptr(), stride, N, K, code,
+            uniforms.data_ptr(), ctypes.addressof(settings), out.data_ptr(), kind)
+    return out
+
+
 def kmeans_release_workspace(stream=None):
     """Return the stream's workspace (scratch of the K-split path, the update,
-    the lookup's gradient, the linear layer and the clipping, kept between
-    calls) and its tile queue (the persistent path's) to the device's memory
+    the lookup's gradient, the linear layers, the norm's gradient and the
+    clipping, kept between calls) and its tile queue (the persistent path's) to the device's memory
     pool, in stream order; a later call on the stream allocates them again.
     Graphs that captured calls on the stream must not be replayed afterwards."""
     lib = load_library()

@@ -20,8 +20,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libkmeans_mi355x.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("kmeans_kernels.hip", "kmeans_update.hip",
                                            "kmeans_lookup.hip", "kmeans_linear.hip",
-                                           "kmeans_clip.hip", "kmeans_workspace.hip",
-                                           "kmeans_api.hip")]
+                                           "kmeans_clip.hip", "kmeans_norm.hip",
+                                           "kmeans_linear_fp8.hip", "kmeans_sample.hip",
+                                           "kmeans_workspace.hip", "kmeans_api.hip")]
 PROBE_LIBRARY = os.path.join(PKG, "libkmeans_mfma_stream.so")
 PROBE_SOURCES = [os.path.join(CSRC, "mfma_stream.hip")]
 ARCH = "gfx950"

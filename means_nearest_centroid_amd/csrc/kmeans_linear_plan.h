@@ -150,9 +150,9 @@ inline int64_t tiles_of(const Product &g, int side) {
            ((static_cast<int64_t>(g.J) + side - 1) / side);
 }
 
-// Chooses the shape and the splits of k with the least estimated time (us),
-// which it returns.
-inline double plan_product(Product &g, int compute_units) {
+// Chooses the shape (kWide only where `wide`) and the splits of k with the least
+// estimated time (us), which it returns.
+inline double plan_product(Product &g, int compute_units, bool wide = true) {
     const int64_t k_tiles = (g.K + kTileK - 1) / kTileK;
     struct Cost {
         Shape shape;
@@ -170,6 +170,8 @@ inline double plan_product(Product &g, int compute_units) {
     double best = 1e30;
     for (int c = 0; c < kinds; ++c) {
         const Cost &k = costs[c];
+        if (k.shape == kWide && !wide)
+            continue;
         const int64_t tiles = tiles_of(g, k.side);
         for (int64_t s = 1; s <= std::min<int64_t>(kMaxKSplits, k_tiles); s *= 2) {
             const int64_t per = (k_tiles + s - 1) / s;

@@ -1,0 +1,825 @@
+// kmeans_norm.hip -- gfx950 kernels of the root-mean-square norm with the
+// residual's addition (its output in the inputs' type, or in 8 bits with a
+// scale for each 128 columns), of its gradient, and of quantisation by blocks.
+//
+//     h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w
+//     gradient, with g = dy w:  dx = r g - h r^3 mean(g h) + dh,
+//                               dw = sum over rows of dy h r
+//     block of values y:  s = max|y| / 448,  q = e4m3(y / s)
+//
+// All are bound by memory: each row is read once into registers, its sums are
+// joined across the lanes that hold it, and what follows is computed from the
+// registers.
+#include <stdint.h>
+
+#include <algorithm>
+#include <optional>
+
+#include "kmeans_fp8.h"
+#include "kmeans_internal.h"
+#include "kmeans_types.h"
+
+namespace kmeans {
+namespace {
+
+constexpr int64_t kMaxNormWidth = 1 << 20;
+constexpr int kNormThreads = 256;
+constexpr int kRun = 8;                  // values a lane takes at once
+constexpr int kLanesPerBlock = kFp8Block / kRun;
+// Widest row that a group of 256 lanes holds in registers; wider ones are read
+// twice.
+constexpr int64_t kMaxHeld = 256 * 8 * kRun;
+
+// ---- sums over the G lanes that share a row --------------------------------
+
+// The group's totals of M values, on each of its lanes.  Groups wider than a
+// wave meet in `part` ([2][M][4], two halves in turn: a call may begin while
+// other waves still read the one before it, and a third cannot, since the
+// second's barrier lies between).
+template <int G, int M>
+__device__ __forceinline__ void group_sums(float (&v)[M], float (*part)[M][4], int &turn) {
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int x = (G < 64 ? G : 64) / 2; x >= 1; x >>= 1)
+            v[m] += __shfl_xor(v[m], x, 64);
+    if constexpr (G > 64) {
+        static_assert(G == 256, "four waves to a row");
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                part[turn][m][wave] = v[m];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            v[m] = (part[turn][m][0] + part[turn][m][1]) + (part[turn][m][2] + part[turn][m][3]);
+        turn ^= 1;
+    }
+}
+
+// ---- forward ---------------------------------------------------------------
+
+struct Norm {
+    const void *x;
+    const void *residual;    // or null
+    const void *weight;      // or null
+    void *sum;               // or null
+    void *y;                 // or null: quantised
+    uint8_t *q;
+    float *scales;
+    int64_t ldx, ldr, ldh, ldy, ldq, lds;
+    int64_t first;           // row of this launch
+    int N, D;
+    float eps;
+};
+
+template <typename T>
+__device__ __forceinline__ void widen_run(const Packed<typename T::bits, kRun> &p,
+                                          float (&v)[kRun]) {
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+        v[e] = T::widen(p.v[e]);
+}
+
+// Output of one run from column c on: y = h r w, rounded once to the type or by
+// its block of 16 lanes to 8 bits.  Every lane of a block calls it (h = 0 past
+// the row's end, where n <= 0).
+template <typename T, bool QUANT>
+__device__ __forceinline__ void norm_out(const Norm &a, int64_t row, int c, float r,
+                                         const float (&h)[kRun],
+                                         const Packed<typename T::bits, kRun> &w) {
+    typedef typename T::bits B;
+    const int n = a.D - c;
+    float y[kRun], scale[kRun];
+    widen_run<T>(w, scale);
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+        y[e] = h[e] * r;
+        if (a.weight != nullptr)
+            y[e] *= scale[e];
+    }
+    if constexpr (QUANT) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            most = max(most, e < n ? magnitude(y[e]) : 0u);
+        most = block_most<kLanesPerBlock>(most);
+        const float s = fp8_scale(most);
+        if (n > 0) {
+            store_fp8_run(a.q + row * a.ldq + c, n, y, 1.0f / s);
+            if (c % kFp8Block == 0)
+                a.scales[row * a.lds + c / kFp8Block] = s;
+        }
+    } else if (n > 0) {
+        store_run<B, kRun>(static_cast<B *>(a.y) + row * a.ldy + c, n, narrow_run<T, kRun>(y));
+    }
+}
+
+// G lanes to a row, R runs to a lane: run i of the row is lane i % G's.
+template <typename T, bool QUANT, int G, int R>
+__global__ __launch_bounds__(kNormThreads)
+void norm_kernel(const Norm a) {
+    typedef typename T::bits B;
+    __shared__ float part[2][1][4];
+    constexpr int kRows = kNormThreads / G;
+    const int lane = threadIdx.x % G;
+    const int64_t row = a.first + static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
+    const bool real = row < a.N;
+    Packed<B, kRun> px[R], pr[R], pw[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * G + lane) * kRun;
+        px[i] = load_run<B, kRun>(static_cast<const B *>(a.x) + row * a.ldx + c,
+                                  real ? a.D - c : 0);
+    }
+    if (a.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * G + lane) * kRun;
+            pr[i] = load_run<B, kRun>(static_cast<const B *>(a.residual) + row * a.ldr + c,
+                                      real ? a.D - c : 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * G + lane) * kRun;
+        pw[i] = Packed<B, kRun>{};
+        if (a.weight != nullptr)
+            pw[i] = load_run<B, kRun>(static_cast<const B *>(a.weight) + c, a.D - c);
+    }
+    float h[R][kRun], ss[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        widen_run<T>(px[i], h[i]);
+        if (a.residual != nullptr) {
+            float r[kRun];
+            widen_run<T>(pr[i], r);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                h[i][e] += r[e];
+        }
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            ss[0] = fmaf(h[i][e], h[i][e], ss[0]);
+        const int c = (i * G + lane) * kRun;
+        if (a.sum != nullptr && real && c < a.D)
+            store_run<B, kRun>(static_cast<B *>(a.sum) + row * a.ldh + c, a.D - c,
+                               narrow_run<T, kRun>(h[i]));
+    }
+    int turn = 0;
+    group_sums<G>(ss, part, turn);
+    const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
+    if (!real)                   // whole groups of lanes
+        return;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        norm_out<T, QUANT>(a, row, (i * G + lane) * kRun, r, h[i], pw[i]);
+}
+
+// Rows wider than the registers of a workgroup: read twice, the second time
+// from the caches.  Nothing is written before the row's sum is known, so that
+// the outputs may lie on the inputs.
+template <typename T, bool QUANT>
+__global__ __launch_bounds__(kNormThreads)
+void norm_long_kernel(const Norm a) {
+    typedef typename T::bits B;
+    __shared__ float part[2][1][4];
+    const int64_t row = a.first + blockIdx.x;
+    const int step = kNormThreads * kRun;
+    auto load = [&](int c, float (&h)[kRun]) __attribute__((always_inline)) {
+        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.x) + row * a.ldx + c, a.D - c), h);
+        if (a.residual == nullptr)
+            return;
+        float r[kRun];
+        widen_run<T>(
+            load_run<B, kRun>(static_cast<const B *>(a.residual) + row * a.ldr + c, a.D - c), r);
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            h[e] += r[e];
+    };
+    float ss[1] = {0.0f};
+    for (int c = threadIdx.x * kRun; c < a.D; c += step) {
+        float h[kRun];
+        load(c, h);
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            ss[0] = fmaf(h[e], h[e], ss[0]);
+    }
+    int turn = 0;
+    group_sums<kNormThreads>(ss, part, turn);
+    const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
+    for (int c0 = 0; c0 < a.D; c0 += step) {       // the same trips on every lane
+        const int c = c0 + threadIdx.x * kRun;
+        float h[kRun];
+        load(c, h);
+        Packed<B, kRun> w = {};
+        if (a.weight != nullptr)
+            w = load_run<B, kRun>(static_cast<const B *>(a.weight) + c, a.D - c);
+        if (a.sum != nullptr && c < a.D)
+            store_run<B, kRun>(static_cast<B *>(a.sum) + row * a.ldh + c, a.D - c,
+                               narrow_run<T, kRun>(h));
+        norm_out<T, QUANT>(a, row, c, r, h, w);
+    }
+}
+
+// ---- gradient --------------------------------------------------------------
+
+struct NormGrad {
+    const void *dy, *h;
+    const void *weight;      // or null
+    const void *dh;          // or null
+    void *dx;
+    float *dw_partial;       // [rows of workgroups][D], or null
+    float *r;                // [N]: 1 / rms of each row, for wide rows' dw
+    int64_t ldy, ldh, lddh, ldx;
+    int N, D;
+    float eps;
+};
+
+// Rows of a workgroup, one after another (kRows at a time): dx from the row's
+// two sums, dw summed in registers over the workgroup's rows in their order,
+// then over its groups in LDS.
+template <typename T, int G, int R>
+__global__ __launch_bounds__(kNormThreads)
+void norm_grad_kernel(const NormGrad a) {
+    typedef typename T::bits B;
+    constexpr int kRows = kNormThreads / G;
+    __shared__ float part[2][2][4];
+    __shared__ float across[G < kNormThreads ? kNormThreads * kRun : 1];
+    const int lane = threadIdx.x % G, group = threadIdx.x / G;
+    float dw[R][kRun], w[R][kRun];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * G + lane) * kRun;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+            dw[i][e] = 0.0f;
+            w[i][e] = 1.0f;
+        }
+        if (a.weight != nullptr)
+            widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.weight) + c, a.D - c), w[i]);
+    }
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    int turn = 0;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < a.N;
+         row0 += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t row = row0 + group;
+        const bool real = row < a.N;
+        Packed<B, kRun> ph[R], py[R], pd[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * G + lane) * kRun;
+            const int n = real ? a.D - c : 0;
+            ph[i] = load_run<B, kRun>(static_cast<const B *>(a.h) + row * a.ldh + c, n);
+            py[i] = load_run<B, kRun>(static_cast<const B *>(a.dy) + row * a.ldy + c, n);
+            pd[i] = Packed<B, kRun>{};
+            if (a.dh != nullptr)
+                pd[i] = load_run<B, kRun>(static_cast<const B *>(a.dh) + row * a.lddh + c, n);
+        }
+        float h[R][kRun], y[R][kRun], s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            widen_run<T>(ph[i], h[i]);
+            widen_run<T>(py[i], y[i]);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) {
+                s[0] = fmaf(h[i][e], h[i][e], s[0]);
+                s[1] = fmaf(y[i][e] * w[i][e], h[i][e], s[1]);
+            }
+        }
+        group_sums<G>(s, part, turn);
+        const float r = 1.0f / sqrtf(s[0] / static_cast<float>(a.D) + a.eps);
+        const float k = (s[1] * inv_d * r) * r;      // dx = r (g - h k) + dh
+        if (!real)
+            continue;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * G + lane) * kRun;
+            float d[kRun], v[kRun];
+            widen_run<T>(pd[i], d);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) {
+                v[e] = r * fmaf(-h[i][e], k, y[i][e] * w[i][e]) + d[e];
+                dw[i][e] = fmaf(y[i][e] * h[i][e], r, dw[i][e]);
+            }
+            if (c < a.D)
+                store_run<B, kRun>(static_cast<B *>(a.dx) + row * a.ldx + c, a.D - c,
+                                   narrow_run<T, kRun>(v));
+        }
+    }
+    if (a.dw_partial == nullptr)
+        return;
+    float *out = a.dw_partial + static_cast<int64_t>(blockIdx.x) * a.D;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * G + lane) * kRun;
+        if constexpr (G < kNormThreads) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                across[e * kNormThreads + threadIdx.x] = dw[i][e];
+            __syncthreads();
+            if (group == 0)
+#pragma unroll
+                for (int e = 0; e < kRun; ++e)
+                    for (int q = 1; q < kRows; ++q)
+                        dw[i][e] += across[e * kNormThreads + q * G + lane];
+        }
+        if (group == 0 && c < a.D) {
+            Packed<float, kRun> p;
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                p.v[e] = dw[i][e];
+            store_run<float, kRun>(out + c, a.D - c, p);
+        }
+    }
+}
+
+// Wide rows: dx by two readings of the row (the second from the caches).
+template <typename T>
+__global__ __launch_bounds__(kNormThreads)
+void norm_grad_long_kernel(const NormGrad a, int64_t first) {
+    typedef typename T::bits B;
+    __shared__ float part[2][2][4];
+    const int64_t row = first + blockIdx.x;
+    auto load = [&](const void *p, int64_t ld, int c, float (&v)[kRun])
+                    __attribute__((always_inline)) {
+        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(p) + row * ld + c, a.D - c), v);
+    };
+    auto load_g = [&](int c, float (&g)[kRun]) __attribute__((always_inline)) {
+        load(a.dy, a.ldy, c, g);
+        if (a.weight == nullptr)
+            return;
+        float w[kRun];
+        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.weight) + c, a.D - c), w);
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            g[e] *= w[e];
+    };
+    float s[2] = {0.0f, 0.0f};
+    for (int c = threadIdx.x * kRun; c < a.D; c += kNormThreads * kRun) {
+        float h[kRun], g[kRun];
+        load(a.h, a.ldh, c, h);
+        load_g(c, g);
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+            s[0] = fmaf(h[e], h[e], s[0]);
+            s[1] = fmaf(g[e], h[e], s[1]);
+        }
+    }
+    int turn = 0;
+    group_sums<kNormThreads>(s, part, turn);
+    const float r = 1.0f / sqrtf(s[0] / static_cast<float>(a.D) + a.eps);
+    const float k = (s[1] / static_cast<float>(a.D) * r) * r;
+    if (a.r != nullptr && threadIdx.x == 0)
+        a.r[row] = r;
+    for (int c = threadIdx.x * kRun; c < a.D; c += kNormThreads * kRun) {
+        float h[kRun], g[kRun], d[kRun] = {};
+        load(a.h, a.ldh, c, h);
+        load_g(c, g);
+        if (a.dh != nullptr)
+            load(a.dh, a.lddh, c, d);
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            g[e] = r * fmaf(-h[e], k, g[e]) + d[e];
+        store_run<B, kRun>(static_cast<B *>(a.dx) + row * a.ldx + c, a.D - c,
+                           narrow_run<T, kRun>(g));
+    }
+}
+
+// Wide rows: dw's partial sums over a workgroup's rows, a run of columns to each
+// lane.
+template <typename T>
+__global__ __launch_bounds__(kNormThreads)
+void norm_columns_kernel(const NormGrad a, int rows_per_wg) {
+    typedef typename T::bits B;
+    const int c = (blockIdx.y * kNormThreads + threadIdx.x) * kRun;
+    if (c >= a.D)
+        return;
+    const int64_t end = min(static_cast<int64_t>(a.N),
+                            (static_cast<int64_t>(blockIdx.x) + 1) * rows_per_wg);
+    float dw[kRun] = {};
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_wg; row < end; ++row) {
+        float h[kRun], y[kRun];
+        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.h) + row * a.ldh + c, a.D - c), h);
+        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.dy) + row * a.ldy + c, a.D - c), y);
+        const float r = a.r[row];
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            dw[e] = fmaf(y[e] * h[e], r, dw[e]);
+    }
+    Packed<float, kRun> p;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+        p.v[e] = dw[e];
+    store_run<float, kRun>(a.dw_partial + static_cast<int64_t>(blockIdx.x) * a.D + c, a.D - c, p);
+}
+
+// dw[c] = sum of the partials of column c: kJoinCols columns to a workgroup,
+// kJoinShares threads to a column, joined in LDS in their order.
+constexpr int kJoinCols = 32;
+constexpr int kJoinShares = 32;
+template <typename T>
+__global__ __launch_bounds__(kJoinCols * kJoinShares)
+void norm_join_kernel(const float *partial, int rows, int D, void *dw) {
+    __shared__ float sums[kJoinShares][kJoinCols + 1];
+    const int c = threadIdx.x % kJoinCols, share = threadIdx.x / kJoinCols;
+    const int col = blockIdx.x * kJoinCols + c;
+    float v = 0.0f;
+    if (col < D)
+        for (int r = share; r < rows; r += kJoinShares)
+            v += partial[static_cast<int64_t>(r) * D + col];
+    sums[share][c] = v;
+    __syncthreads();
+    if (share != 0 || col >= D)
+        return;
+    for (int q = 1; q < kJoinShares; ++q)
+        v += sums[q][c];
+    static_cast<typename T::bits *>(dw)[col] = T::narrow(v);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256)
+void norm_zero_kernel(typename T::bits *p, int n) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < n)
+        p[i] = T::narrow(0.0f);
+}
+
+// ---- quantisation by blocks ------------------------------------------------
+
+struct Quantize {
+    const void *x;
+    uint8_t *q;
+    float *scales;
+    int64_t ldx, ldq, lds;
+    int N, D;
+};
+
+// A tile of 128 rows x 128 columns to a workgroup, all of it in registers: 16
+// lanes across a row, 16 rows at a time.  ROWS (of a block): 1, each row's 16
+// lanes have its scale; 128, the workgroup joins them.
+template <typename T, int ROWS>
+__global__ __launch_bounds__(kNormThreads)
+void quantize_kernel(const Quantize a) {
+    typedef typename T::bits B;
+    constexpr int kAtOnce = kNormThreads / kLanesPerBlock;
+    constexpr int kPasses = kFp8Block / kAtOnce;
+    __shared__ uint32_t part[2][kNormThreads / 64];
+    const int across = (a.D + kFp8Block - 1) / kFp8Block;
+    const int64_t tiles = (static_cast<int64_t>(a.N) + kFp8Block - 1) / kFp8Block * across;
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int b = static_cast<int>(t % across);
+        const int64_t row0 = t / across * kFp8Block + threadIdx.x / kLanesPerBlock;
+        const int c = b * kFp8Block + threadIdx.x % kLanesPerBlock * kRun;
+        const int n = a.D - c;
+        Packed<B, kRun> p[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int64_t row = row0 + i * kAtOnce;
+            p[i] = load_run<B, kRun>(static_cast<const B *>(a.x) + row * a.ldx + c,
+                                     row < a.N ? n : 0);
+        }
+        uint32_t most[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            most[i] = 0;
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                most[i] = max(most[i], magnitude(T::widen(p[i].v[e])));
+        }
+        if constexpr (ROWS == kFp8Block) {
+            uint32_t m = most[0];
+#pragma unroll
+            for (int i = 1; i < kPasses; ++i)
+                m = max(m, most[i]);
+            m = block_most<64>(m);
+            if ((threadIdx.x & 63) == 0)
+                part[turn][threadIdx.x >> 6] = m;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kNormThreads / 64; ++w)
+                m = max(m, part[turn][w]);
+            turn ^= 1;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i)
+                most[i] = m;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i)
+                most[i] = block_most<kLanesPerBlock>(most[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int64_t row = row0 + i * kAtOnce;
+            if (row >= a.N || n <= 0)
+                continue;
+            const float s = fp8_scale(most[i]);
+            float v[kRun];
+            widen_run<T>(p[i], v);
+            store_fp8_run(a.q + row * a.ldq + c, n, v, 1.0f / s);
+            if (c % kFp8Block == 0 && row % ROWS == 0)
+                a.scales[row / ROWS * a.lds + b] = s;
+        }
+    }
+}
+
+// ---- launch ----------------------------------------------------------------
+
+// A launch has less than 2^32 threads.
+constexpr int64_t kMaxGrid = int64_t(1) << 23;
+
+template <typename T, bool QUANT, int G, int R>
+hipError_t launch_norm(Norm a, hipStream_t stream) {
+    constexpr int kRows = kNormThreads / G;
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < a.N && e == hipSuccess; first += kMaxGrid * kRows) {
+        a.first = first;
+        const int64_t wgs = std::min<int64_t>(kMaxGrid, (a.N - first + kRows - 1) / kRows);
+        hipLaunchKernelGGL((norm_kernel<T, QUANT, G, R>), dim3(static_cast<unsigned>(wgs)),
+                           dim3(kNormThreads), 0, stream, a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <typename T, bool QUANT>
+hipError_t run_norm(Norm a, hipStream_t stream) {
+    const int64_t runs = (static_cast<int64_t>(a.D) + kRun - 1) / kRun;
+    if (runs <= 16)
+        return launch_norm<T, QUANT, 16, 1>(a, stream);
+    if (runs <= 32)
+        return launch_norm<T, QUANT, 16, 2>(a, stream);
+    if (runs <= 64)
+        return launch_norm<T, QUANT, 64, 1>(a, stream);
+    if (runs <= 128)
+        return launch_norm<T, QUANT, 64, 2>(a, stream);
+    if (runs <= 256)
+        return launch_norm<T, QUANT, 256, 1>(a, stream);
+    if (runs <= 512)
+        return launch_norm<T, QUANT, 256, 2>(a, stream);
+    if (runs <= 1024)
+        return launch_norm<T, QUANT, 256, 4>(a, stream);
+    if (runs <= kMaxHeld / kRun)
+        return launch_norm<T, QUANT, 256, 8>(a, stream);
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < a.N && e == hipSuccess; first += kMaxGrid) {
+        a.first = first;
+        hipLaunchKernelGGL((norm_long_kernel<T, QUANT>),
+                           dim3(static_cast<unsigned>(std::min<int64_t>(kMaxGrid, a.N - first))),
+                           dim3(kNormThreads), 0, stream, a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <typename T>
+hipError_t run_norm(const Norm &a, hipStream_t stream) {
+    return a.q != nullptr ? run_norm<T, true>(a, stream) : run_norm<T, false>(a, stream);
+}
+
+// How the rows of a gradient are divided: workgroups (each leaves one row of
+// dw's partial sums) and, for wide rows, how many rows each takes.
+struct NormGradPlan {
+    bool wide;
+    int rows_at_once;        // of a workgroup
+    int wgs, rows_per_wg;
+    NormGradPlan(int64_t N, int64_t D, int compute_units) : wide(D > kMaxHeld) {
+        const int64_t runs = (D + kRun - 1) / kRun;
+        rows_at_once = wide || runs > 128 ? 1 : runs > 32 ? 4 : 16;
+        const int64_t most = wide ? 64 : 4 * compute_units;
+        wgs = static_cast<int>(std::min<int64_t>(most, (N + rows_at_once - 1) / rows_at_once));
+        rows_per_wg = static_cast<int>((N + wgs - 1) / wgs);
+        if (wide)
+            wgs = static_cast<int>((N + rows_per_wg - 1) / rows_per_wg);
+    }
+    size_t partial_bytes(int64_t D) const { return static_cast<size_t>(wgs) * D * sizeof(float); }
+};
+
+template <typename T>
+hipError_t run_norm_grad(const NormGrad &a, const NormGradPlan &p, void *dw, hipStream_t stream) {
+    const int64_t runs = (static_cast<int64_t>(a.D) + kRun - 1) / kRun;
+    const dim3 grid(p.wgs), block(kNormThreads);
+    hipError_t e = hipSuccess;
+    if (p.wide) {
+        for (int64_t first = 0; first < a.N && e == hipSuccess; first += kMaxGrid) {
+            const int64_t wgs = std::min<int64_t>(kMaxGrid, a.N - first);
+            hipLaunchKernelGGL((norm_grad_long_kernel<T>), dim3(static_cast<unsigned>(wgs)), block,
+                               0, stream, a, first);
+            e = hipGetLastError();
+        }
+        if (e == hipSuccess && dw != nullptr) {
+            const unsigned across = static_cast<unsigned>((runs + kNormThreads - 1) / kNormThreads);
+            hipLaunchKernelGGL((norm_columns_kernel<T>), dim3(p.wgs, across), block, 0, stream, a,
+                               p.rows_per_wg);
+            e = hipGetLastError();
+        }
+    } else {
+        if (runs <= 16)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 16, 1>), grid, block, 0, stream, a);
+        else if (runs <= 32)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 16, 2>), grid, block, 0, stream, a);
+        else if (runs <= 64)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 64, 1>), grid, block, 0, stream, a);
+        else if (runs <= 128)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 64, 2>), grid, block, 0, stream, a);
+        else if (runs <= 256)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 1>), grid, block, 0, stream, a);
+        else if (runs <= 512)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 2>), grid, block, 0, stream, a);
+        else if (runs <= 1024)
+            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 4>), grid, block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 8>), grid, block, 0, stream, a);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && dw != nullptr) {
+        hipLaunchKernelGGL((norm_join_kernel<T>), dim3((a.D + kJoinCols - 1) / kJoinCols),
+                           dim3(kJoinCols * kJoinShares), 0, stream, a.dw_partial, p.wgs, a.D, dw);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <typename T>
+hipError_t run_zero(void *p, int64_t n, hipStream_t stream) {
+    hipLaunchKernelGGL((norm_zero_kernel<T>), dim3(static_cast<unsigned>((n + 255) / 256)),
+                       dim3(256), 0, stream, static_cast<typename T::bits *>(p),
+                       static_cast<int>(n));
+    return hipGetLastError();
+}
+
+template <typename T, int ROWS>
+hipError_t launch_quantize(const Quantize &a, hipStream_t stream) {
+    const int64_t tiles = (static_cast<int64_t>(a.N) + kFp8Block - 1) / kFp8Block *
+                          ((a.D + kFp8Block - 1) / kFp8Block);
+    hipLaunchKernelGGL((quantize_kernel<T, ROWS>),
+                       dim3(static_cast<unsigned>(std::min(tiles, kMaxGrid))), dim3(kNormThreads),
+                       0, stream, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_quantize(const Quantize &a, int rows, hipStream_t stream) {
+    return rows == 1 ? launch_quantize<T, 1>(a, stream) : launch_quantize<T, kFp8Block>(a, stream);
+}
+
+// ---- checks ----------------------------------------------------------------
+
+kmeans_status_t check_sizes(int64_t N, int64_t D, int32_t dtype) {
+    if (N < 0 || D < 1)
+        return fail(KMEANS_ERR_INVALID_ARG, "N=%lld must be >= 0 and D=%lld >= 1",
+                    static_cast<long long>(N), static_cast<long long>(D));
+    if (dtype < KMEANS_BF16 || dtype > KMEANS_FP32)
+        return fail(KMEANS_ERR_INVALID_ARG, "dtype=%d is not a kmeans_dtype_t", dtype);
+    if (N > kMaxRows || D > kMaxNormWidth)
+        return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld or D=%lld too large (max %lld, %lld)",
+                    static_cast<long long>(N), static_cast<long long>(D),
+                    static_cast<long long>(kMaxRows), static_cast<long long>(kMaxNormWidth));
+    return KMEANS_OK;
+}
+
+}  // namespace
+
+kmeans_status_t check_matrix(const char *name, const void *p, int64_t cols, int64_t ld,
+                             size_t element) {
+    if (p == nullptr)
+        return fail(KMEANS_ERR_INVALID_ARG, "null pointer argument (%s)", name);
+    if (!aligned(p, element))
+        return fail(KMEANS_ERR_ALIGNMENT, "%s must be %zu-byte aligned", name, element);
+    if (ld < cols)
+        return fail(KMEANS_ERR_INVALID_ARG, "%s: row stride %lld below the row length %lld", name,
+                    static_cast<long long>(ld), static_cast<long long>(cols));
+    if (ld > kMaxRows)
+        return fail(KMEANS_ERR_UNSUPPORTED, "%s: row stride %lld too large (max %lld)", name,
+                    static_cast<long long>(ld), static_cast<long long>(kMaxRows));
+    return KMEANS_OK;
+}
+
+kmeans_status_t check_array(const char *name, const void *p, size_t element) {
+    if (!aligned(p, element))
+        return fail(KMEANS_ERR_ALIGNMENT, "%s must be %zu-byte aligned", name, element);
+    return KMEANS_OK;
+}
+
+}  // namespace kmeans
+
+// ---- C entry points --------------------------------------------------------
+
+extern "C" kmeans_status_t kmeans_rms_norm(const void *X, int64_t x_stride, const void *residual,
+                                           int64_t residual_stride, const void *weight, int64_t N,
+                                           int64_t D, int32_t dtype, float eps, void *sum,
+                                           int64_t sum_stride, void *Y, int64_t y_stride, void *Q,
+                                           int64_t q_stride, float *scales, int64_t scales_stride,
+                                           hipStream_t stream) {
+    using namespace kmeans;
+    kmeans_status_t st = check_sizes(N, D, dtype);
+    if (st != KMEANS_OK)
+        return st;
+    if (!(eps >= 0.0f))
+        return fail(KMEANS_ERR_INVALID_ARG, "eps=%g must be >= 0", static_cast<double>(eps));
+    if (N == 0)
+        return ok();
+    const size_t size = dtype_size(dtype);
+    if ((Y != nullptr) == (Q != nullptr))
+        return fail(KMEANS_ERR_INVALID_ARG, "one of Y=%p and Q=%p must be given", Y, Q);
+    if ((st = check_matrix("X", X, D, x_stride, size)) != KMEANS_OK ||
+        (residual && (st = check_matrix("residual", residual, D, residual_stride, size)) != KMEANS_OK) ||
+        (st = check_array("weight", weight, size)) != KMEANS_OK ||
+        (sum && (st = check_matrix("sum", sum, D, sum_stride, size)) != KMEANS_OK) ||
+        (Y && (st = check_matrix("Y", Y, D, y_stride, size)) != KMEANS_OK) ||
+        (Q && (st = check_matrix("Q", Q, D, q_stride, 1)) != KMEANS_OK) ||
+        (Q && (st = check_matrix("scales", scales, fp8_blocks(D), scales_stride, 4)) != KMEANS_OK))
+        return st;
+    const Norm a{X, residual, weight, sum, Y, static_cast<uint8_t *>(Q), scales, x_stride,
+                 residual_stride, sum_stride, y_stride, q_stride, scales_stride, 0,
+                 static_cast<int>(N), static_cast<int>(D), eps};
+    const hipError_t e = dtype == KMEANS_BF16   ? run_norm<Bf16>(a, stream)
+                         : dtype == KMEANS_FP16 ? run_norm<Fp16>(a, stream)
+                                                : run_norm<Fp32>(a, stream);
+    if (e != hipSuccess)
+        return fail(KMEANS_ERR_HIP, "norm launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+extern "C" kmeans_status_t kmeans_rms_norm_grad(const void *dY, int64_t dy_stride, const void *H,
+                                                int64_t h_stride, const void *weight,
+                                                const void *dH, int64_t dh_stride, int64_t N,
+                                                int64_t D, int32_t dtype, float eps, void *dX,
+                                                int64_t dx_stride, void *dweight,
+                                                hipStream_t stream) {
+    using namespace kmeans;
+    kmeans_status_t st = check_sizes(N, D, dtype);
+    if (st != KMEANS_OK)
+        return st;
+    if (!(eps >= 0.0f))
+        return fail(KMEANS_ERR_INVALID_ARG, "eps=%g must be >= 0", static_cast<double>(eps));
+    const size_t size = dtype_size(dtype);
+    if ((st = check_array("dweight", dweight, size)) != KMEANS_OK)
+        return st;
+    if (N == 0) {
+        if (dweight == nullptr)
+            return ok();
+        const hipError_t e = dtype == KMEANS_FP32 ? run_zero<Fp32>(dweight, D, stream)
+                                                  : run_zero<Bf16>(dweight, D, stream);
+        if (e != hipSuccess)
+            return fail(KMEANS_ERR_HIP, "norm gradient launch failed: %s", hipGetErrorString(e));
+        return ok();
+    }
+    if ((st = check_matrix("dY", dY, D, dy_stride, size)) != KMEANS_OK ||
+        (st = check_matrix("H", H, D, h_stride, size)) != KMEANS_OK ||
+        (st = check_array("weight", weight, size)) != KMEANS_OK ||
+        (dH && (st = check_matrix("dH", dH, D, dh_stride, size)) != KMEANS_OK) ||
+        (st = check_matrix("dX", dX, D, dx_stride, size)) != KMEANS_OK)
+        return st;
+    const NormGradPlan p(N, D, device_compute_units());
+    const size_t r_bytes = p.wide ? (static_cast<size_t>(N) * sizeof(float) + 255) / 256 * 256 : 0;
+    NormGrad a{dY, H, weight, dH, dX, nullptr, nullptr, dy_stride, h_stride, dh_stride, dx_stride,
+               static_cast<int>(N), static_cast<int>(D), eps};
+    std::optional<WorkspaceLease> lease;
+    if (dweight != nullptr) {
+        const size_t bytes = r_bytes + p.partial_bytes(D);
+        lease.emplace(stream, bytes);
+        if (lease->error() != hipSuccess)
+            return fail(KMEANS_ERR_NO_MEMORY, "workspace of %zu bytes: %s", bytes,
+                        hipGetErrorString(lease->error()));
+        char *ws = static_cast<char *>(lease->ptr());
+        a.r = p.wide ? reinterpret_cast<float *>(ws) : nullptr;
+        a.dw_partial = reinterpret_cast<float *>(ws + r_bytes);
+    }
+    const hipError_t e = dtype == KMEANS_BF16   ? run_norm_grad<Bf16>(a, p, dweight, stream)
+                         : dtype == KMEANS_FP16 ? run_norm_grad<Fp16>(a, p, dweight, stream)
+                                                : run_norm_grad<Fp32>(a, p, dweight, stream);
+    if (e != hipSuccess)
+        return fail(KMEANS_ERR_HIP, "norm gradient launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+extern "C" kmeans_status_t kmeans_quantize(const void *X, int64_t x_stride, int64_t N, int64_t D,
+                                           int32_t dtype, int32_t block_rows, void *Q,
+                                           int64_t q_stride, float *scales, int64_t scales_stride,
+                                           hipStream_t stream) {
+    using namespace kmeans;
+    kmeans_status_t st = check_sizes(N, D, dtype);
+    if (st != KMEANS_OK)
+        return st;
+    if (block_rows != 1 && block_rows != kFp8Block)
+        return fail(KMEANS_ERR_INVALID_ARG, "block_rows=%d must be 1 or %d", block_rows, kFp8Block);
+    if (N == 0)
+        return ok();
+    if ((st = check_matrix("X", X, D, x_stride, dtype_size(dtype))) != KMEANS_OK ||
+        (st = check_matrix("Q", Q, D, q_stride, 1)) != KMEANS_OK ||
+        (st = check_matrix("scales", scales, fp8_blocks(D), scales_stride, 4)) != KMEANS_OK)
+        return st;
+    const Quantize a{X, static_cast<uint8_t *>(Q), scales, x_stride, q_stride, scales_stride,
+                     static_cast<int>(N), static_cast<int>(D)};
+    const hipError_t e = dtype == KMEANS_BF16   ? run_quantize<Bf16>(a, block_rows, stream)
+                         : dtype == KMEANS_FP16 ? run_quantize<Fp16>(a, block_rows, stream)
+                                                : run_quantize<Fp32>(a, block_rows, stream);
+    if (e != hipSuccess)
+        return fail(KMEANS_ERR_HIP, "quantize launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
