@@ -564,7 +564,7 @@ typedef struct {
  * counted; a row that has no other gets the label -1 (for which kmeans_lookup
  * gives zeros).  Logits of +infinity share the row between them.  A temperature
  * that is 0 (in the array also one below 0 or NaN) gives the lowest index of the
- * largest logit.  Array values beyond their ranges count as the nearest in range,
+ * largest logit, one between 0 and 2^-120 counts as 2^-120.  Array values beyond their ranges count as the nearest in range,
  * a NaN as no limit; a uniform below 0 or NaN counts as 0, one of 1 or more gives
  * the last label kept.
  *

@@ -647,28 +647,27 @@ def kmeans_clip_gradients(grads, max_norm: float, out=None, norm=None, stream=No
 # ---- predicting labels ----
 
 FP8_BLOCK = 128
-_FP8 = None
+_FP8 = _F32 = None
 
 
-def _fp8_rows(t, name, device=None, shape=None):
-    """Check rows of 8-bit values; their stride."""
-    global _FP8
+def _types():
+    """float8_e4m3fn and float32, looked up once."""
+    global _FP8, _F32
     import torch
-    if _FP8 is None:
-        _FP8 = torch.float8_e4m3fn
+    _FP8, _F32 = torch.float8_e4m3fn, torch.float32
+
+
+def _typed_rows(t, name, dtype, index, shape=None):
+    """Check rows of `dtype` on GPU `index`; their stride."""
     stride = _rows(t, name, shape=shape)
-    if t.dtype is not _FP8 or (device is not None and t.get_device() != device.index):
-        raise ValueError(f"{name} must be {_FP8} on {device or 'one GPU'} "
-                         f"(got {t.dtype} on {t.device})")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on cuda:{index} (got {t.dtype} on {t.device})")
     return stride
 
 
-def _scale_rows(t, name, device, shape):
-    import torch
-    stride = _rows(t, name, shape=shape)
-    if t.dtype is not torch.float32 or t.get_device() != device.index:
-        raise ValueError(f"{name} must be float32 on {device} (got {t.dtype} on {t.device})")
-    return stride
+def _as_rows(t, name):
+    """Like _flat, quick for a matrix."""
+    return t if getattr(t, "ndim", 0) == 2 else _flat(t, name)
 
 
 def _blocks(D: int) -> int:
@@ -692,52 +691,59 @@ def kmeans_rms_norm(X, weight=None, residual=None, eps: float = 1e-6, quantize: 
     128 columns (``scales``: ``[..., ceil(D / 128)]``).  Returns ``Y`` or ``(Y,
     scales)``, and ``H`` after it where there is a residual (``sum``: its
     tensor, which may be ``residual`` itself)."""
-    import torch
-    lead, D = X.shape[:-1], X.shape[-1]
-    x = _flat(X, "X")
+    x = _as_rows(X, "X")
     x_stride = _rows(x, "X")
     code = _dtype(x, "X")
-    N = x.shape[0]
+    N, D = x.shape
+    lead = X.shape[:-1] if x is not X else (N,)
     if weight is not None:
         weight = _gain(weight, D, x)
     r, r_stride, h, h_stride = None, 0, None, 0
     if residual is not None:
-        r = _flat(residual, "residual")
+        r = _as_rows(residual, "residual")
         r_stride = _rows(r, "residual", like=x, shape=(N, D))
         r = r.data_ptr()
         if sum is None:
             sum = x.new_empty((*lead, D))
-        h = _flat(sum, "sum")
-        h_stride = _rows(h, "sum", like=x, shape=(N, D))
-        h = h.data_ptr()
+            h_stride = D
+        else:
+            h_stride = _rows(_as_rows(sum, "sum"), "sum", like=x, shape=(N, D))
+        h = sum.data_ptr()
     elif sum is not None:
         raise ValueError("sum needs residual")
     y, y_stride, q, q_stride, s, s_stride = None, 0, None, 0, None, 0
     if quantize:
+        if _FP8 is None:
+            _types()
+        blocks = (D + FP8_BLOCK - 1) // FP8_BLOCK
         if out is None:
-            out = torch.empty((*lead, D), dtype=torch.float8_e4m3fn, device=x.device)
-        q = _flat(out, "out")
-        q_stride = _fp8_rows(q, "out", x.device, (N, D))
-        q = q.data_ptr()
+            out = x.new_empty((*lead, D), dtype=_FP8)
+            q_stride = D
+        else:
+            q_stride = _typed_rows(_as_rows(out, "out"), "out", _FP8, x.get_device(), (N, D))
+        q = out.data_ptr()
         if scales is None:
-            scales = torch.empty((*lead, _blocks(D)), dtype=torch.float32, device=x.device)
-        s = _flat(scales, "scales")
-        s_stride = _scale_rows(s, "scales", x.device, (N, _blocks(D)))
-        s = s.data_ptr()
+            scales = x.new_empty((*lead, blocks), dtype=_F32)
+            s_stride = blocks
+        else:
+            s_stride = _typed_rows(_as_rows(scales, "scales"), "scales", _F32, x.get_device(),
+                                   (N, blocks))
+        s = scales.data_ptr()
     else:
         if scales is not None:
             raise ValueError("scales need quantize=True")
         if out is None:
             out = x.new_empty((*lead, D))
-        y = _flat(out, "out")
-        y_stride = _rows(y, "out", like=x, shape=(N, D))
-        y = y.data_ptr()
+            y_stride = D
+        else:
+            y_stride = _rows(_as_rows(out, "out"), "out", like=x, shape=(N, D))
+        y = out.data_ptr()
     lib = load_library()
     _launch(lib.kmeans_rms_norm, x.device, stream, x.data_ptr(), x_stride, r, r_stride, weight, N,
             D, code, eps, h, h_stride, y, y_stride, q, q_stride, s, s_stride)
-    got = (out, scales) if quantize else (out,)
-    got = got if residual is None else (*got, sum)
-    return got if len(got) > 1 else out
+    if residual is not None:
+        return (out, scales, sum) if quantize else (out, sum)
+    return (out, scales) if quantize else out
 
 
 def kmeans_rms_norm_grad(dY, H, weight=None, eps: float = 1e-6, dH=None, need_dw: bool = True,
@@ -747,24 +753,25 @@ def kmeans_rms_norm_grad(dY, H, weight=None, eps: float = 1e-6, dH=None, need_dw
     there was no residual); ``dH``: the gradient that reaches the sum along the
     residual path, added to ``dX``, which is the residual's gradient too.
     ``dweight`` is ``None`` without a weight or with ``need_dw`` false."""
-    shape = H.shape
-    H = _flat(H, "H")
-    h_stride = _rows(H, "H")
-    code = _dtype(H, "H")
-    N, D = H.shape
-    dY = _flat(dY, "dY")
-    y_stride = _rows(dY, "dY", like=H, shape=(N, D))
+    h = _as_rows(H, "H")
+    h_stride = _rows(h, "H")
+    code = _dtype(h, "H")
+    N, D = h.shape
+    dY = _as_rows(dY, "dY")
+    y_stride = _rows(dY, "dY", like=h, shape=(N, D))
     d, d_stride = None, 0
     if dH is not None:
-        d = _flat(dH, "dH")
-        d_stride = _rows(d, "dH", like=H, shape=(N, D))
+        d = _as_rows(dH, "dH")
+        d_stride = _rows(d, "dH", like=h, shape=(N, D))
         d = d.data_ptr()
-    dw = H.new_empty(D) if weight is not None and need_dw else None
+    dw = None
     if weight is not None:
-        weight = _gain(weight, D, H)
-    dX = H.new_empty(shape)
+        if need_dw:
+            dw = h.new_empty(D)
+        weight = _gain(weight, D, h)
+    dX = h.new_empty(H.shape)
     lib = load_library()
-    _launch(lib.kmeans_rms_norm_grad, H.device, stream, dY.data_ptr(), y_stride, H.data_ptr(),
+    _launch(lib.kmeans_rms_norm_grad, h.device, stream, dY.data_ptr(), y_stride, h.data_ptr(),
             h_stride, weight, d, d_stride, N, D, code, eps, dX.data_ptr(), D, _ptr(dw))
     return dX, dw
 
@@ -772,19 +779,24 @@ def kmeans_rms_norm_grad(dY, H, weight=None, eps: float = 1e-6, dH=None, need_dw
 def kmeans_quantize(X, rows: int = 1, out=None, scales=None, stream=None):
     """``X`` (``[N, D]`` bf16, fp16 or fp32) as ``float8_e4m3fn`` values with an
     fp32 scale for each block of ``rows`` (1 or 128) x 128: ``(Q, scales)``."""
-    import torch
     x_stride = _rows(X, "X")
     code = _dtype(X, "X")
     N, D = X.shape
     if rows not in (1, FP8_BLOCK):
         raise ValueError(f"rows must be 1 or {FP8_BLOCK} (got {rows})")
-    n = -(-N // rows)
+    if _FP8 is None:
+        _types()
+    shape = (-(-N // rows), _blocks(D))
     if out is None:
-        out = torch.empty((N, D), dtype=torch.float8_e4m3fn, device=X.device)
-    q_stride = _fp8_rows(out, "out", X.device, (N, D))
+        out = X.new_empty((N, D), dtype=_FP8)
+        q_stride = D
+    else:
+        q_stride = _typed_rows(out, "out", _FP8, X.get_device(), (N, D))
     if scales is None:
-        scales = torch.empty((n, _blocks(D)), dtype=torch.float32, device=X.device)
-    s_stride = _scale_rows(scales, "scales", X.device, (n, _blocks(D)))
+        scales = X.new_empty(shape, dtype=_F32)
+        s_stride = shape[1]
+    else:
+        s_stride = _typed_rows(scales, "scales", _F32, X.get_device(), shape)
     lib = load_library()
     _launch(lib.kmeans_quantize, X.device, stream, X.data_ptr(), x_stride, N, D, code, rows,
             out.data_ptr(), q_stride, scales.data_ptr(), s_stride)
@@ -799,40 +811,43 @@ def kmeans_linear_fp8(X, x_scales, W, w_scales, bias=None, residual=None,
     ``[F, D]`` with ``w_scales`` ``[ceil(F / 128), ceil(D / 128)]`` (``rows=128``).
     ``dtype``: of ``Y``, bias and residual (bfloat16 when not given, or
     ``out``'s)."""
-    import torch
-    lead = X.shape[:-1]
-    X = _flat(X, "X")
-    x_stride = _fp8_rows(X, "X")
-    device = X.device
-    N, D = X.shape
-    w_stride = _fp8_rows(W, "W", device)
+    if _FP8 is None:
+        _types()
+    x = _as_rows(X, "X")
+    index = x.get_device()
+    x_stride = _typed_rows(x, "X", _FP8, index)
+    N, D = x.shape
+    w_stride = _typed_rows(W, "W", _FP8, index)
     F, d = W.shape
     if d != D:
         raise ValueError(f"X has D={D} but W has D={d}")
-    sx = _flat(x_scales, "x_scales")
-    xs_stride = _scale_rows(sx, "x_scales", device, (N, _blocks(D)))
-    ws_stride = _scale_rows(w_scales, "w_scales", device, (_blocks(F), _blocks(D)))
+    sx = _as_rows(x_scales, "x_scales")
+    blocks = (D + FP8_BLOCK - 1) // FP8_BLOCK
+    xs_stride = _typed_rows(sx, "x_scales", _F32, index, (N, blocks))
+    ws_stride = _typed_rows(w_scales, "w_scales", _F32, index, (_blocks(F), blocks))
     act = _activation(activation)
     if out is None:
-        out = torch.empty((*lead, F), dtype=dtype or torch.bfloat16, device=device)
-    elif dtype is not None and out.dtype is not dtype:
-        raise ValueError(f"out must be {dtype} (got {out.dtype})")
-    y = _flat(out, "out")
-    y_stride = _rows(y, "out", shape=(N, F))
-    if y.get_device() != device.index:
-        raise ValueError(f"out must be on {device} (got {y.device})")
-    code = _dtype(y, "out")
+        if dtype is None:
+            import torch
+            dtype = torch.bfloat16
+        out = x.new_empty((N, F) if x is X else (*X.shape[:-1], F), dtype=dtype)
+        y_stride = F
+    else:
+        if dtype is not None and out.dtype is not dtype:
+            raise ValueError(f"out must be {dtype} (got {out.dtype})")
+        y_stride = _typed_rows(_as_rows(out, "out"), "out", out.dtype, index, (N, F))
+    code = _dtype(out, "out")
     if bias is not None:
-        bias = _bias(bias, F, y).data_ptr()
+        bias = _bias(bias, F, out).data_ptr()
     r, r_stride = None, 0
     if residual is not None:
-        r = _flat(residual, "residual")
-        r_stride = _rows(r, "residual", like=y, shape=(N, F))
+        r = _as_rows(residual, "residual")
+        r_stride = _rows(r, "residual", like=out, shape=(N, F))
         r = r.data_ptr()
     lib = load_library()
-    _launch(lib.kmeans_linear_fp8, device, stream, X.data_ptr(), x_stride, sx.data_ptr(), xs_stride,
-            W.data_ptr(), w_stride, w_scales.data_ptr(), ws_stride, bias, r, r_stride, N, D, F,
-            code, act, y.data_ptr(), y_stride)
+    _launch(lib.kmeans_linear_fp8, x.device, stream, x.data_ptr(), x_stride, sx.data_ptr(),
+            xs_stride, W.data_ptr(), w_stride, w_scales.data_ptr(), ws_stride, bias, r, r_stride, N,
+            D, F, code, act, out.data_ptr(), y_stride)
     return out
 
 
