@@ -89,17 +89,15 @@ __device__ __forceinline__ f32x4 mfma_block(const Widened &a, const Widened &b) 
 // outputs over one split of k, in S stages, as linear_tile_kernel does.  A
 // staged tile is one block of k: its scales come with it, one copy of 64 values
 // to a wave (first the rows of X in the order in which lanes need them, then the
-// columns).  A tile is worked in phases of HB P blocks against all TJ Q blocks;
-// a phase's P fragments are read one phase ahead.
+// columns).  A tile is worked in phases of one P block against all TJ Q blocks; a
+// phase's P fragment is read one phase ahead.  A product is scaled and added two
+// products after its own, so that no instruction waits for the matrix pipe.
 template <typename T, int WI, int WJ, int TI, int TJ, int S>
 __global__ __launch_bounds__(WI * WJ * 64, 2)
 void linear_fp8_kernel(const Product g, const Scales sc) {
     constexpr bool EXACT = sizeof(typename T::bits) == 4;
     constexpr int kThreads = WI * WJ * 64;
     constexpr int RI = WI * TI * 16, RJ = WJ * TJ * 16;
-    constexpr int HB = TI > 4 ? 1 : 2;        // P blocks of one phase
-    constexpr int NP = TI / HB;               // phases per tile
-    static_assert(TI % HB == 0 && NP % 2 == 0, "phases alternate fragment buffers");
     static_assert(RI + RJ <= kThreads, "one copy of scales to a wave");
     typedef Bf16 Pair;                        // two 8-bit values
     typedef TileMap<false, RI> PMap;
@@ -117,16 +115,18 @@ void linear_fp8_kernel(const Product g, const Scales sc) {
     __shared__ __attribute__((aligned(16))) uint8_t s1[kScaleBytes];
     __shared__ __attribute__((aligned(16))) uint8_t s2[S > 2 ? kScaleBytes : 16];
     __shared__ __attribute__((aligned(16))) uint8_t s3[S > 2 ? kScaleBytes : 16];
-    auto p_stage = [&](auto i) KM_INLINE -> uint8_t * {
-        constexpr int n = decltype(i)::value % S;
+    // Stages by number: one known at compile time, so that the compiler can tell an
+    // LDS read of one stage from a copy into another.
+    auto p_stage = [&](int i) KM_INLINE -> uint8_t * {
+        const int n = i % S;
         return n == 0 ? p0 : n == 1 ? p1 : n == 2 ? p2 : p3;
     };
-    auto q_stage = [&](auto i) KM_INLINE -> uint8_t * {
-        constexpr int n = decltype(i)::value % S;
+    auto q_stage = [&](int i) KM_INLINE -> uint8_t * {
+        const int n = i % S;
         return n == 0 ? q0 : n == 1 ? q1 : n == 2 ? q2 : q3;
     };
-    auto s_stage = [&](auto i) KM_INLINE -> uint8_t * {
-        constexpr int n = decltype(i)::value % S;
+    auto s_stage = [&](int i) KM_INLINE -> uint8_t * {
+        const int n = i % S;
         return n == 0 ? s0 : n == 1 ? s1 : n == 2 ? s2 : s3;
     };
 
@@ -173,7 +173,7 @@ void linear_fp8_kernel(const Product g, const Scales sc) {
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<float *>(scale_base + t), 0, 0x7fffffff, 0x00020000);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (KM_LDS void *)(stage + wave * 256), 4,
-                                                 scale_off, 0, 0, 0);
+                                                 t < tiles ? scale_off : kOutOfRange, 0, 0, 0);
 #endif
     };
 
@@ -183,15 +183,12 @@ void linear_fp8_kernel(const Product g, const Scales sc) {
 #pragma unroll
         for (int b = 0; b < TJ; ++b)
             acc[a][b] = f32x4{0, 0, 0, 0};
-    Halves pf[2][HB], qf[TJ];
+    Halves pf[2], qf[TJ];
     float scale[TI];
 
-    auto read_p = [&](const uint8_t *pst, int ph) KM_INLINE {
-#pragma unroll
-        for (int a = 0; a < HB; ++a) {
-            pf[ph & 1][a].lo = __builtin_bit_cast(u32x4, pr.read(pst, ph * HB + a, 0));
-            pf[ph & 1][a].hi = __builtin_bit_cast(u32x4, pr.read(pst, ph * HB + a, 1));
-        }
+    auto read_p = [&](const uint8_t *pst, int a) KM_INLINE {
+        pf[a & 1].lo = __builtin_bit_cast(u32x4, pr.read(pst, a, 0));
+        pf[a & 1].hi = __builtin_bit_cast(u32x4, pr.read(pst, a, 1));
     };
     auto read_q = [&](const uint8_t *qst, int b) KM_INLINE {
         qf[b].lo = __builtin_bit_cast(u32x4, qr.read(qst, b, 0));
@@ -207,74 +204,86 @@ void linear_fp8_kernel(const Product g, const Scales sc) {
                 scale[a + c] = x[c] * w;
         }
     };
-    auto multiply = [&](int ph, int b) KM_INLINE {
+    // Product n of the tile (block n / TJ of P with block n % TJ of Q), and the
+    // sum that the one before the last goes to.
+    f32x4 made[3];
+    auto add = [&](int n) KM_INLINE {
 #pragma unroll
-        for (int a = 0; a < HB; ++a) {
-            f32x4 v;
-            if constexpr (EXACT)
-                v = mfma_block(widen_block(qf[b]), widen_block(pf[ph & 1][a]));
-            else
-                v = mfma_block(qf[b], pf[ph & 1][a]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                acc[ph * HB + a][b][c] = fmaf(v[c], scale[ph * HB + a], acc[ph * HB + a][b][c]);
-        }
+        for (int c = 0; c < 4; ++c)
+            acc[n / TJ][n % TJ][c] = fmaf(made[n % 3][c], scale[n / TJ], acc[n / TJ][n % TJ][c]);
+    };
+    auto multiply = [&](int n) KM_INLINE {
+        if constexpr (EXACT)
+            made[n % 3] = mfma_block(widen_block(qf[n % TJ]), widen_block(pf[n / TJ & 1]));
+        else
+            made[n % 3] = mfma_block(qf[n % TJ], pf[n / TJ & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (n >= 2)
+            add(n - 2);
     };
     constexpr int kCopies = decltype(ps)::kPieces + decltype(qs)::kPieces + 1;
-    auto issue = [&](auto full, int t, auto at) KM_INLINE {
-        ps.template issue<decltype(full)::value>(t, p_stage(at));
-        qs.template issue<decltype(full)::value>(t, q_stage(at));
-        issue_scales(t, s_stage(at));
+    // Tile t's copies.  What lies past the range of k is copied as zeros, whole
+    // tiles behind the last one too: the loop below needs no other form for its
+    // end (which would cost it registers: with one, 16384 x 4096 x 4096 took 408
+    // us).
+    auto issue_piece = [&](auto &st, int u, int t, uint8_t *stage) KM_INLINE {
+#if defined(__HIP_DEVICE_COMPILE__)
+        typedef std::remove_reference_t<decltype(st)> Stage;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<typename Pair::bits *>(st.base + static_cast<int64_t>(t) * kTileK), 0,
+            0x7fffffff, 0x00020000);
+        int r, c;
+        st.piece(u, r, c);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (KM_LDS void *)(stage + wave * (Stage::kPieces * 1024) + u * 1024), 16,
+            c * 8 < k_len - t * kTileK ? st.off[u] : kOutOfRange, 0, 0, 0);
+#endif
     };
-    // Tile t, in stage at % S.  FULL: tiles t + 1 .. t + S exist and t + S is a
-    // whole one.
-    auto step = [&](auto full, auto at, int t) KM_INLINE {
-        constexpr bool FULL = decltype(full)::value;
-        constexpr int n = decltype(at)::value;
+    // Copy i of kCopies.
+    auto issue_copy = [&](int i, int t, int at) KM_INLINE {
+        constexpr int kP = decltype(ps)::kPieces, kQ = decltype(qs)::kPieces;
+        if (i < kP)
+            issue_piece(ps, i, t, p_stage(at));
+        else if (i < kP + kQ)
+            issue_piece(qs, i - kP, t, q_stage(at));
+        else
+            issue_scales(t, s_stage(at));
+    };
+    // Tile t, in stage at % S.
+    auto step = [&](auto at, int t) KM_INLINE {
 #pragma unroll
-        for (int ph = 0; ph + 1 < NP; ++ph) {
-            read_p(p_stage(at), ph + 1);
+        for (int a = 0; a + 1 < TI; ++a) {
+            read_p(p_stage(at), a + 1);
 #pragma unroll
             for (int b = 0; b < TJ; ++b)
-                multiply(ph, b);
-            __builtin_amdgcn_sched_barrier(0);
+                multiply(a * TJ + b);
         }
-        if (!FULL && t + 1 >= tiles) {
-#pragma unroll
-            for (int b = 0; b < TJ; ++b)
-                multiply(NP - 1, b);
-            return;
-        }
-        wait_vmem<FULL ? (S - 2) * kCopies : 0>();
+        wait_vmem<(S - 2) * kCopies>();
         lds_barrier();
-        // A Q fragment is read again as soon as its last product is on its way.
+        // A Q fragment is read again as soon as its last product is on its way,
+        // and the copies of tile t + S go between the products too.
 #pragma unroll
         for (int b = 0; b < TJ; ++b) {
-            multiply(NP - 1, b);
-            read_q(q_stage(Index<n + 1>{}), b);
+            multiply((TI - 1) * TJ + b);
+            read_q(q_stage(at + 1), b);
+            if (b == 0)
+                read_p(p_stage(at + 1), 0);
+#pragma unroll
+            for (int i = b * kCopies / TJ; i < (b + 1) * kCopies / TJ; ++i)
+                issue_copy(i, t + S, at);
         }
-        read_p(p_stage(Index<n + 1>{}), 0);
-        read_scales(s_stage(Index<n + 1>{}));
-        if (FULL || t + S < tiles)
-            issue(full, t + S, at);
+        add(TI * TJ - 2);
+        add(TI * TJ - 1);
+        read_scales(s_stage(at + 1));
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto start = [&](auto at) KM_INLINE {
-        if (decltype(at)::value < tiles)
-            issue(std::false_type{}, decltype(at)::value, at);
-    };
 
-    start(Index<0>{});
-    start(Index<1>{});
-    if constexpr (S > 2) {
-        start(Index<2>{});
-        start(Index<3>{});
-    }
-    // All stages were started: only the first need have landed.
-    if (tiles >= S)
-        wait_vmem<(S - 1) * kCopies>();
-    else
-        wait_vmem<0>();
+#pragma unroll
+    for (int t = 0; t < S; ++t)
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            issue_copy(i, t, t);
+    wait_vmem<(S - 1) * kCopies>();       // the first tile has landed
     lds_barrier();
     read_p(p0, 0);
 #pragma unroll
@@ -282,26 +291,24 @@ void linear_fp8_kernel(const Product g, const Scales sc) {
         read_q(q0, b);
     read_scales(s0);
     int t = 0;
-    const int full = k_len / kTileK;
-    for (; t + 2 * S - 1 < full; t += S) {
-        step(std::true_type{}, Index<0>{}, t);
-        step(std::true_type{}, Index<1>{}, t + 1);
+#pragma unroll 1
+    for (; t + S <= tiles; t += S) {
+        step(Index<0>{}, t);
+        step(Index<1>{}, t + 1);
         if constexpr (S > 2) {
-            step(std::true_type{}, Index<2>{}, t + 2);
-            step(std::true_type{}, Index<3>{}, t + 3);
+            step(Index<2>{}, t + 2);
+            step(Index<3>{}, t + 3);
         }
     }
-    for (; t < tiles; t += S) {
-        step(std::false_type{}, Index<0>{}, t);
+    if (t < tiles)
+        step(Index<0>{}, t);
+    if constexpr (S > 2) {
         if (t + 1 < tiles)
-            step(std::false_type{}, Index<1>{}, t + 1);
-        if constexpr (S > 2) {
-            if (t + 2 < tiles)
-                step(std::false_type{}, Index<2>{}, t + 2);
-            if (t + 3 < tiles)
-                step(std::false_type{}, Index<3>{}, t + 3);
-        }
+            step(Index<1>{}, t + 1);
+        if (t + 2 < tiles)
+            step(Index<2>{}, t + 2);
     }
+    wait_vmem<0>();                       // of the zeros, before the stages are used again
 
     if (g.splits > 1) {
         float *part = g.partial + static_cast<int64_t>(split) * g.I * g.J;
