@@ -521,27 +521,25 @@ void linear_fp8_rows_kernel(const Product g, const Scales sc) {
 // ---- rows that the copies do not take --------------------------------------
 
 // Rows of `cols` bytes laid out anew, `ld` apart (a multiple of 16, zeros behind
-// the last value), up to two matrices in one launch.
+// the last value), up to two matrices in one launch: kLayoutLanes lanes to a row.
 struct Layout {
     const uint8_t *from;
     uint8_t *to;
     int64_t ld_from, ld;
-    int64_t pieces;          // 16 bytes each; none: nothing to do
-    int cols;
+    int rows, cols;          // no rows: nothing to do
+    int wgs;
 };
+constexpr int kLayoutLanes = 32;
+constexpr int kLayoutRows = 256 / kLayoutLanes;
 __global__ __launch_bounds__(256)
 void linear_fp8_layout_kernel(const Layout a, const Layout b) {
-    const int64_t total = a.pieces + b.pieces;
-    for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < total;
-         x += static_cast<int64_t>(gridDim.x) * 256) {
-        const bool second = x >= a.pieces;
-        const Layout &m = second ? b : a;
-        const int64_t y = second ? x - a.pieces : x;
-        const int64_t row = y / (m.ld / 16);
-        const int c = static_cast<int>(y % (m.ld / 16)) * 16;
-        *reinterpret_cast<u32x4 *>(m.to + row * m.ld + c) =
-            load_bytes(m.from + row * m.ld_from + c, m.cols - c);
-    }
+    const bool second = static_cast<int>(blockIdx.x) >= a.wgs;
+    const Layout &m = second ? b : a;
+    const int first = (blockIdx.x - (second ? a.wgs : 0)) * kLayoutRows + threadIdx.x / kLayoutLanes;
+    for (int64_t row = first; row < m.rows; row += static_cast<int64_t>(m.wgs) * kLayoutRows)
+        for (int c = threadIdx.x % kLayoutLanes * 16; c < m.ld; c += kLayoutLanes * 16)
+            *reinterpret_cast<u32x4 *>(m.to + row * m.ld + c) =
+                load_bytes(m.from + row * m.ld_from + c, m.cols - c);
 }
 
 // ---- launch ----------------------------------------------------------------
@@ -618,11 +616,12 @@ bool takes_copies(const void *p, int64_t ld, int64_t cols) {
 // Plans the new layout of rows [rows][D] at workspace offset `at`, or leaves
 // them as they are.
 Layout layout_of(const void *p, int64_t ld, int64_t rows, int64_t D, size_t &at) {
-    Layout m{static_cast<const uint8_t *>(p), nullptr, ld, ld, 0, static_cast<int>(D)};
+    Layout m{static_cast<const uint8_t *>(p), nullptr, ld, ld, 0, static_cast<int>(D), 0};
     if (takes_copies(p, ld, D))
         return m;
     m.ld = (D + 15) / 16 * 16;
-    m.pieces = rows * (m.ld / 16);
+    m.rows = static_cast<int>(rows);
+    m.wgs = static_cast<int>(std::min<int64_t>((rows + kLayoutRows - 1) / kLayoutRows, 4096));
     m.to = reinterpret_cast<uint8_t *>(at);             // an offset until the lease
     at += align_up(static_cast<size_t>(rows) * m.ld);
     return m;
@@ -719,18 +718,17 @@ extern "C" kmeans_status_t kmeans_linear_fp8(const void *X, int64_t x_stride, co
             g.partial = reinterpret_cast<float *>(ws + part_at);
         }
         for (Layout *m : {&x, &w})
-            if (m->pieces > 0)
+            if (m->rows > 0)
                 m->to = reinterpret_cast<uint8_t *>(ws + reinterpret_cast<size_t>(m->to));
-        if (x.pieces + w.pieces > 0) {
-            const int64_t wgs = std::min<int64_t>((x.pieces + w.pieces + 255) / 256, 8192);
-            hipLaunchKernelGGL(linear_fp8_layout_kernel, dim3(static_cast<unsigned>(wgs)),
-                               dim3(256), 0, stream, x, w);
+        if (x.wgs + w.wgs > 0) {
+            hipLaunchKernelGGL(linear_fp8_layout_kernel, dim3(x.wgs + w.wgs), dim3(256), 0, stream,
+                               x, w);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess)
                 return fail(KMEANS_ERR_HIP, "layout launch failed: %s", hipGetErrorString(e));
         }
-        g.P = x.pieces > 0 ? x.to : X;
-        g.Q = w.pieces > 0 ? w.to : W;
+        g.P = x.rows > 0 ? x.to : X;
+        g.Q = w.rows > 0 ? w.to : W;
         g.ldp = x.ld / 2;
         g.ldq = w.ld / 2;
     }
