@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <optional>
+#include <type_traits>
 
 #include "kmeans_fp8.h"
 #include "kmeans_internal.h"
@@ -26,38 +27,49 @@ constexpr int64_t kMaxNormWidth = 1 << 20;
 constexpr int kNormThreads = 256;
 constexpr int kRun = 8;                  // values a lane takes at once
 constexpr int kLanesPerBlock = kFp8Block / kRun;
-// Widest row that a group of 256 lanes holds in registers; wider ones are read
-// twice.
-constexpr int64_t kMaxHeld = 256 * 8 * kRun;
+// Widest row that a workgroup holds in registers; wider ones are read twice.
+constexpr int64_t kMaxHeld = 1024 * 2 * kRun;
 
 // ---- sums over the G lanes that share a row --------------------------------
 
+// Workgroup for G lanes to a row: one row, or several side by side.
+constexpr int threads_for(int G) { return G > kNormThreads ? G : kNormThreads; }
+
 // The group's totals of M values, on each of its lanes.  Groups wider than a
-// wave meet in `part` ([2][M][4], two halves in turn: a call may begin while
-// other waves still read the one before it, and a third cannot, since the
-// second's barrier lies between).
+// wave meet in LDS (two places in turn: a call may begin while other waves still
+// read the one before it, and a third cannot, since the second's barrier lies
+// between).
 template <int G, int M>
-__device__ __forceinline__ void group_sums(float (&v)[M], float (*part)[M][4], int &turn) {
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int x = (G < 64 ? G : 64) / 2; x >= 1; x >>= 1)
-            v[m] += __shfl_xor(v[m], x, 64);
-    if constexpr (G > 64) {
-        static_assert(G == 256, "four waves to a row");
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-                part[turn][m][wave] = v[m];
-        }
-        __syncthreads();
+struct GroupSums {
+    static constexpr int kGroups = threads_for(G) / G;
+    static constexpr int kWaves = G > 64 ? G / 64 : 1;
+    float part[G > 64 ? 2 : 1][kGroups][kWaves][M];
+
+    __device__ __forceinline__ void join(float (&v)[M], int &turn) {
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            v[m] = (part[turn][m][0] + part[turn][m][1]) + (part[turn][m][2] + part[turn][m][3]);
-        turn ^= 1;
+#pragma unroll
+            for (int x = (G < 64 ? G : 64) / 2; x >= 1; x >>= 1)
+                v[m] += __shfl_xor(v[m], x, 64);
+        if constexpr (G > 64) {
+            const int group = threadIdx.x / G, wave = threadIdx.x % G / 64;
+            if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    part[turn][group][wave][m] = v[m];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                v[m] = part[turn][group][0][m];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w)
+                    v[m] += part[turn][group][w][m];
+            }
+            turn ^= 1;
+        }
     }
-}
+};
 
 // ---- forward ---------------------------------------------------------------
 
@@ -119,11 +131,11 @@ __device__ __forceinline__ void norm_out(const Norm &a, int64_t row, int c, floa
 
 // G lanes to a row, R runs to a lane: run i of the row is lane i % G's.
 template <typename T, bool QUANT, int G, int R>
-__global__ __launch_bounds__(kNormThreads)
+__global__ __launch_bounds__(threads_for(G))
 void norm_kernel(const Norm a) {
     typedef typename T::bits B;
-    __shared__ float part[2][1][4];
-    constexpr int kRows = kNormThreads / G;
+    __shared__ GroupSums<G, 1> sums;
+    constexpr int kRows = threads_for(G) / G;
     const int lane = threadIdx.x % G;
     const int64_t row = a.first + static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G;
     const bool real = row < a.N;
@@ -169,7 +181,7 @@ void norm_kernel(const Norm a) {
                                narrow_run<T, kRun>(h[i]));
     }
     int turn = 0;
-    group_sums<G>(ss, part, turn);
+    sums.join(ss, turn);
     const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
     if (!real)                   // whole groups of lanes
         return;
@@ -185,7 +197,7 @@ template <typename T, bool QUANT>
 __global__ __launch_bounds__(kNormThreads)
 void norm_long_kernel(const Norm a) {
     typedef typename T::bits B;
-    __shared__ float part[2][1][4];
+    __shared__ GroupSums<kNormThreads, 1> sums;
     const int64_t row = a.first + blockIdx.x;
     const int step = kNormThreads * kRun;
     auto load = [&](int c, float (&h)[kRun]) __attribute__((always_inline)) {
@@ -208,7 +220,7 @@ void norm_long_kernel(const Norm a) {
             ss[0] = fmaf(h[e], h[e], ss[0]);
     }
     int turn = 0;
-    group_sums<kNormThreads>(ss, part, turn);
+    sums.join(ss, turn);
     const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.D) + a.eps);
     for (int c0 = 0; c0 < a.D; c0 += step) {       // the same trips on every lane
         const int c = c0 + threadIdx.x * kRun;
@@ -240,74 +252,99 @@ struct NormGrad {
 
 // Rows of a workgroup, one after another (kRows at a time): dx from the row's
 // two sums, dw summed in registers over the workgroup's rows in their order,
-// then over its groups in LDS.
-template <typename T, int G, int R>
-__global__ __launch_bounds__(kNormThreads)
+// then over its groups in LDS.  The next row is on its way while this one is
+// worked, where registers hold both (R = 1); rows stay in their own type for
+// that.  As many workgroups as the CUs hold (16 waves each): 16384 x 4096 bf16
+// with dh 108 us (537 MB, 5.0 TB/s), 119 with twice and 149 with half as many,
+// and 171 with 256 lanes to a row.  WHOLE: D is a multiple of 8, and no run is
+// cut short (50021 x 321 fp32 48 us, 193 MB; 52 with its last runs loaded whole
+// and shifted).
+template <typename T, int G, int R, bool WHOLE>
+__global__ __launch_bounds__(threads_for(G))
 void norm_grad_kernel(const NormGrad a) {
     typedef typename T::bits B;
-    constexpr int kRows = kNormThreads / G;
-    __shared__ float part[2][2][4];
-    __shared__ float across[G < kNormThreads ? kNormThreads * kRun : 1];
+    typedef Packed<B, kRun> Run;
+    constexpr int kThreads = threads_for(G);
+    constexpr int kRows = kThreads / G;
+    __shared__ GroupSums<G, 2> sums;
+    __shared__ float across[kRows > 1 ? kThreads * kRun : 1];
     const int lane = threadIdx.x % G, group = threadIdx.x / G;
-    float dw[R][kRun], w[R][kRun];
+    auto fetch = [&](const void *p, int64_t at, int c, bool real) __attribute__((always_inline)) {
+        const B *q = static_cast<const B *>(p) + at + c;
+        if constexpr (WHOLE)
+            return real && c < a.D ? load_packed<B, kRun>(q) : Run{};
+        else
+            return load_run<B, kRun>(q, real ? a.D - c : 0);
+    };
+    float dw[R][kRun] = {};
+    Run w[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int c = (i * G + lane) * kRun;
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-            dw[i][e] = 0.0f;
-            w[i][e] = 1.0f;
-        }
+    for (int i = 0; i < R; ++i)
         if (a.weight != nullptr)
-            widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.weight) + c, a.D - c), w[i]);
-    }
-    const float inv_d = 1.0f / static_cast<float>(a.D);
-    int turn = 0;
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < a.N;
-         row0 += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t row = row0 + group;
+            w[i] = fetch(a.weight, 0, (i * G + lane) * kRun, true);
+    Run h[R], y[R], d[R];
+    auto load = [&](int64_t row) __attribute__((always_inline)) {
         const bool real = row < a.N;
-        Packed<B, kRun> ph[R], py[R], pd[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int c = (i * G + lane) * kRun;
-            const int n = real ? a.D - c : 0;
-            ph[i] = load_run<B, kRun>(static_cast<const B *>(a.h) + row * a.ldh + c, n);
-            py[i] = load_run<B, kRun>(static_cast<const B *>(a.dy) + row * a.ldy + c, n);
-            pd[i] = Packed<B, kRun>{};
+            h[i] = fetch(a.h, row * a.ldh, c, real);
+            y[i] = fetch(a.dy, row * a.ldy, c, real);
+            d[i] = Run{};
             if (a.dh != nullptr)
-                pd[i] = load_run<B, kRun>(static_cast<const B *>(a.dh) + row * a.lddh + c, n);
+                d[i] = fetch(a.dh, row * a.lddh, c, real);
         }
-        float h[R][kRun], y[R][kRun], s[2] = {0.0f, 0.0f};
+    };
+    auto gain = [&](int i, int e) __attribute__((always_inline)) {
+        return a.weight != nullptr ? T::widen(w[i].v[e]) : 1.0f;
+    };
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+    int turn = 0;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
+    load(row);
+    for (; row - group < a.N; row += stride) {
+        Run h0[R], y0[R], d0[R];
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            widen_run<T>(ph[i], h[i]);
-            widen_run<T>(py[i], y[i]);
+            h0[i] = h[i];
+            y0[i] = y[i];
+            d0[i] = d[i];
 #pragma unroll
             for (int e = 0; e < kRun; ++e) {
-                s[0] = fmaf(h[i][e], h[i][e], s[0]);
-                s[1] = fmaf(y[i][e] * w[i][e], h[i][e], s[1]);
+                const float x = T::widen(h0[i].v[e]);
+                s[0] = fmaf(x, x, s[0]);
+                s[1] = fmaf(T::widen(y0[i].v[e]) * gain(i, e), x, s[1]);
             }
         }
-        group_sums<G>(s, part, turn);
+        if (R == 1)
+            load(row + stride);
+        sums.join(s, turn);
         const float r = 1.0f / sqrtf(s[0] / static_cast<float>(a.D) + a.eps);
         const float k = (s[1] * inv_d * r) * r;      // dx = r (g - h k) + dh
-        if (!real)
-            continue;
+        if (row < a.N) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int c = (i * G + lane) * kRun;
-            float d[kRun], v[kRun];
-            widen_run<T>(pd[i], d);
+            for (int i = 0; i < R; ++i) {
+                const int c = (i * G + lane) * kRun;
+                float v[kRun];
 #pragma unroll
-            for (int e = 0; e < kRun; ++e) {
-                v[e] = r * fmaf(-h[i][e], k, y[i][e] * w[i][e]) + d[e];
-                dw[i][e] = fmaf(y[i][e] * h[i][e], r, dw[i][e]);
+                for (int e = 0; e < kRun; ++e) {
+                    const float x = T::widen(h0[i].v[e]), g = T::widen(y0[i].v[e]);
+                    v[e] = r * fmaf(-x, k, g * gain(i, e)) + T::widen(d0[i].v[e]);
+                    dw[i][e] = fmaf(g * x, r, dw[i][e]);
+                }
+                B *o = static_cast<B *>(a.dx) + row * a.ldx + c;
+                if constexpr (WHOLE) {
+                    if (c < a.D)
+                        store_packed<B, kRun>(o, narrow_run<T, kRun>(v));
+                } else if (c < a.D) {
+                    store_run<B, kRun>(o, a.D - c, narrow_run<T, kRun>(v));
+                }
             }
-            if (c < a.D)
-                store_run<B, kRun>(static_cast<B *>(a.dx) + row * a.ldx + c, a.D - c,
-                                   narrow_run<T, kRun>(v));
         }
+        if (R > 1)
+            load(row + stride);
     }
     if (a.dw_partial == nullptr)
         return;
@@ -315,17 +352,17 @@ void norm_grad_kernel(const NormGrad a) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int c = (i * G + lane) * kRun;
-        if constexpr (G < kNormThreads) {
+        if constexpr (kRows > 1) {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < kRun; ++e)
-                across[e * kNormThreads + threadIdx.x] = dw[i][e];
+                across[e * kThreads + threadIdx.x] = dw[i][e];
             __syncthreads();
             if (group == 0)
 #pragma unroll
                 for (int e = 0; e < kRun; ++e)
                     for (int q = 1; q < kRows; ++q)
-                        dw[i][e] += across[e * kNormThreads + q * G + lane];
+                        dw[i][e] += across[e * kThreads + q * G + lane];
         }
         if (group == 0 && c < a.D) {
             Packed<float, kRun> p;
@@ -342,7 +379,7 @@ template <typename T>
 __global__ __launch_bounds__(kNormThreads)
 void norm_grad_long_kernel(const NormGrad a, int64_t first) {
     typedef typename T::bits B;
-    __shared__ float part[2][2][4];
+    __shared__ GroupSums<kNormThreads, 2> sums;
     const int64_t row = first + blockIdx.x;
     auto load = [&](const void *p, int64_t ld, int c, float (&v)[kRun])
                     __attribute__((always_inline)) {
@@ -370,7 +407,7 @@ void norm_grad_long_kernel(const NormGrad a, int64_t first) {
         }
     }
     int turn = 0;
-    group_sums<kNormThreads>(s, part, turn);
+    sums.join(s, turn);
     const float r = 1.0f / sqrtf(s[0] / static_cast<float>(a.D) + a.eps);
     const float k = (s[1] / static_cast<float>(a.D) * r) * r;
     if (a.r != nullptr && threadIdx.x == 0)
@@ -530,17 +567,19 @@ void quantize_kernel(const Quantize a) {
 // ---- launch ----------------------------------------------------------------
 
 // A launch has less than 2^32 threads.
-constexpr int64_t kMaxGrid = int64_t(1) << 23;
+constexpr int64_t kMaxThreads = int64_t(1) << 31;
+constexpr int64_t kMaxGrid = kMaxThreads / kNormThreads;
 
 template <typename T, bool QUANT, int G, int R>
 hipError_t launch_norm(Norm a, hipStream_t stream) {
-    constexpr int kRows = kNormThreads / G;
+    constexpr int kRows = threads_for(G) / G;
+    constexpr int64_t kMaxGrid = kMaxThreads / threads_for(G);
     hipError_t e = hipSuccess;
     for (int64_t first = 0; first < a.N && e == hipSuccess; first += kMaxGrid * kRows) {
         a.first = first;
         const int64_t wgs = std::min<int64_t>(kMaxGrid, (a.N - first + kRows - 1) / kRows);
         hipLaunchKernelGGL((norm_kernel<T, QUANT, G, R>), dim3(static_cast<unsigned>(wgs)),
-                           dim3(kNormThreads), 0, stream, a);
+                           dim3(threads_for(G)), 0, stream, a);
         e = hipGetLastError();
     }
     return e;
@@ -552,7 +591,7 @@ hipError_t run_norm(Norm a, hipStream_t stream) {
     if (runs <= 16)
         return launch_norm<T, QUANT, 16, 1>(a, stream);
     if (runs <= 32)
-        return launch_norm<T, QUANT, 16, 2>(a, stream);
+        return launch_norm<T, QUANT, 32, 1>(a, stream);
     if (runs <= 64)
         return launch_norm<T, QUANT, 64, 1>(a, stream);
     if (runs <= 128)
@@ -560,11 +599,11 @@ hipError_t run_norm(Norm a, hipStream_t stream) {
     if (runs <= 256)
         return launch_norm<T, QUANT, 256, 1>(a, stream);
     if (runs <= 512)
-        return launch_norm<T, QUANT, 256, 2>(a, stream);
+        return launch_norm<T, QUANT, 512, 1>(a, stream);
     if (runs <= 1024)
-        return launch_norm<T, QUANT, 256, 4>(a, stream);
+        return launch_norm<T, QUANT, 1024, 1>(a, stream);
     if (runs <= kMaxHeld / kRun)
-        return launch_norm<T, QUANT, 256, 8>(a, stream);
+        return launch_norm<T, QUANT, 1024, 2>(a, stream);
     hipError_t e = hipSuccess;
     for (int64_t first = 0; first < a.N && e == hipSuccess; first += kMaxGrid) {
         a.first = first;
@@ -589,8 +628,11 @@ struct NormGradPlan {
     int wgs, rows_per_wg;
     NormGradPlan(int64_t N, int64_t D, int compute_units) : wide(D > kMaxHeld) {
         const int64_t runs = (D + kRun - 1) / kRun;
-        rows_at_once = wide || runs > 128 ? 1 : runs > 32 ? 4 : 16;
-        const int64_t most = wide ? 64 : 4 * compute_units;
+        int lanes = 16;                      // of a row: norm_grad_kernel's G
+        while (lanes < 1024 && lanes < runs)
+            lanes *= 2;
+        rows_at_once = wide ? 1 : threads_for(lanes) / lanes;
+        const int64_t most = wide ? 64 : 1024 / threads_for(lanes) * compute_units;
         wgs = static_cast<int>(std::min<int64_t>(most, (N + rows_at_once - 1) / rows_at_once));
         rows_per_wg = static_cast<int>((N + wgs - 1) / wgs);
         if (wide)
@@ -598,6 +640,9 @@ struct NormGradPlan {
     }
     size_t partial_bytes(int64_t D) const { return static_cast<size_t>(wgs) * D * sizeof(float); }
 };
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 template <typename T>
 hipError_t run_norm_grad(const NormGrad &a, const NormGradPlan &p, void *dw, hipStream_t stream) {
@@ -618,22 +663,31 @@ hipError_t run_norm_grad(const NormGrad &a, const NormGradPlan &p, void *dw, hip
             e = hipGetLastError();
         }
     } else {
+        auto launch = [&](auto lanes, auto held) {
+            constexpr int G = decltype(lanes)::value, R = decltype(held)::value;
+            if (a.D % kRun == 0)
+                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, true>), grid, dim3(threads_for(G)), 0,
+                                   stream, a);
+            else
+                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, false>), grid, dim3(threads_for(G)),
+                                   0, stream, a);
+        };
         if (runs <= 16)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 16, 1>), grid, block, 0, stream, a);
+            launch(Int<16>{}, Int<1>{});
         else if (runs <= 32)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 16, 2>), grid, block, 0, stream, a);
+            launch(Int<32>{}, Int<1>{});
         else if (runs <= 64)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 64, 1>), grid, block, 0, stream, a);
+            launch(Int<64>{}, Int<1>{});
         else if (runs <= 128)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 64, 2>), grid, block, 0, stream, a);
+            launch(Int<128>{}, Int<1>{});
         else if (runs <= 256)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 1>), grid, block, 0, stream, a);
+            launch(Int<256>{}, Int<1>{});
         else if (runs <= 512)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 2>), grid, block, 0, stream, a);
+            launch(Int<512>{}, Int<1>{});
         else if (runs <= 1024)
-            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 4>), grid, block, 0, stream, a);
+            launch(Int<1024>{}, Int<1>{});
         else
-            hipLaunchKernelGGL((norm_grad_kernel<T, 256, 8>), grid, block, 0, stream, a);
+            launch(Int<1024>{}, Int<2>{});
         e = hipGetLastError();
     }
     if (e == hipSuccess && dw != nullptr) {
