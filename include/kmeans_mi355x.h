@@ -559,12 +559,15 @@ typedef struct {
  * the kept exceeds `uniform` times their whole weight.  So a uniform of 0 gives
  * the largest logit, and the result does not decrease in rank as it grows.
  *
- * Weights are multiples of 2^-43 (a label below 2^-44 is never drawn) in 64-bit
- * integers, whose sums are exact.  A logit of -infinity or NaN is never drawn, nor
+ * Weights are held to 2^-43 of the largest and summed in 64-bit integers, exactly,
+ * so that a row's label depends on the row and its settings alone.  A label 32
+ * temperatures or more below the largest logit (about 2^-46 of its weight) is never
+ * drawn.  A logit of -infinity or NaN is never drawn, nor
  * counted; a row that has no other gets the label -1 (for which kmeans_lookup
  * gives zeros).  Logits of +infinity share the row between them.  A temperature
  * that is 0 (in the array also one below 0 or NaN) gives the lowest index of the
- * largest logit, one between 0 and 2^-120 counts as 2^-120.  Array values beyond their ranges count as the nearest in range,
+ * largest logit; one between 0 and 2^-120 counts as 2^-120, one above 2^120 as
+ * that.  Array values beyond their ranges count as the nearest in range,
  * a NaN as no limit; a uniform below 0 or NaN counts as 0, one of 1 or more gives
  * the last label kept.
  *

@@ -7,19 +7,32 @@
 //     label: first in that order whose running weight exceeds u times the
 //            weight of all kept
 //
-// Weights are whole multiples of 2^-43 in 64-bit integers (K < 2^20 of them
-// stay below 2^63), so that every sum is exact and the same in any order, from
-// atomics too: the label depends on the row alone, not on the launch.  A weight
-// is rounded by 2^-44 of the largest one at most.
+// Weights are summed in 64-bit integers, so that every sum is exact and the same
+// in any order, from atomics too: the label depends on the row alone, not on the
+// launch.  A weight is a multiple of 2^-43 of its bin's centre (below); a bin's sum
+// is brought to the scale of the largest weight with one rounding, to 2^-43 of
+// that.  32-bit sums would shift the borders by 1e-7 of the whole and draw other
+// labels in one row of some thousands.
 //
-// All borders (the k-th value, the nucleus's end, the draw) are then one thing:
-// the element at which a running amount (of elements or of weight) reaches a
-// target.  Where few elements can be drawn (the first k, those above min_p) they
-// are gathered and compared with one another.  Otherwise a histogram over 32
-// temperatures below the largest logit finds the bins of the nucleus's end and
-// of the draw, whose elements are gathered and compared.  Where even those are
-// many, they are divided further by the bits of their values and indexes.  No
-// sorting; a row is read two or three times, from the caches after the first.
+// All borders (the k-th value, the nucleus's end, the draw) are one thing: the
+// element at which a running amount (of elements or of weight) reaches a target.
+// Where few elements can be drawn (the first k, those above min_p) they are
+// gathered and compared with one another.  Otherwise a histogram by the distance
+// to a large logit finds the bins of the nucleus's end and of the draw, whose
+// elements are gathered and compared.  Where even those are many, they are
+// divided further by the bits of their values and indexes.  No sorting.
+//
+// The histogram needs no maximum first: its bins lie around the largest of the
+// row's first values, BINS on either side, and the weights within a bin are
+// relative to the bin.  So a row is read from memory once for it (the weights
+// under the loads), and once more, from the caches, to gather.
+//
+// 512 x 65536 fp32, top-p: 67 us (134 MB; 25 us to read them once).  Each workgroup
+// first waits for memory, then for its weights (22 VALU instructions an element,
+// 14 of them fp64), then for the second reading (10 us), and all run in step.
+// Three readings (maximum, weights, borders) took 81 us, five 125.  16 x 32768 with
+// top-k 50: 10 us of which 1.5 read the row, the rest 20 barriers; nucleus and
+// min_p 23.
 #include <math.h>
 #include <stdint.h>
 
@@ -34,18 +47,10 @@ namespace {
 
 constexpr int64_t kMaxLabels = 1 << 20;
 constexpr int kWeightBits = 43;
-constexpr float kSpan = 32.0f;       // temperatures below the largest logit: past
-                                     // 30.5 of them a weight is zero
+constexpr float kSpan = 32.0f;       // temperatures that BINS bins span; labels that
+                                     // far below the largest are never drawn
+constexpr int kFirst = 4096;         // values whose largest the bins lie around
 constexpr int kSmall = 256;          // elements compared with one another
-constexpr int kTable = 128;          // 2^(-i / 128), from its two factors
-constexpr double kEighths[8] = {
-    0x1.0000000000000p+0, 0x1.d5818dcfba487p-1, 0x1.ae89f995ad3adp-1, 0x1.8ace5422aa0dbp-1,
-    0x1.6a09e667f3bcdp-1, 0x1.4bfdad5362a27p-1, 0x1.306fe0a31b715p-1, 0x1.172b83c7d517bp-1};
-constexpr double k128ths[16] = {
-    0x1.0000000000000p+0, 0x1.fd3c22b8f71f1p-1, 0x1.fa7c1819e90d8p-1, 0x1.f7bfdad9cbe14p-1,
-    0x1.f50765b6e4540p-1, 0x1.f252b376bba97p-1, 0x1.efa1bee615a27p-1, 0x1.ecf482d8e67f1p-1,
-    0x1.ea4afa2a490dap-1, 0x1.e7a51fbc74c83p-1, 0x1.e502ee78b3ff6p-1, 0x1.e264614f5a129p-1,
-    0x1.dfc97337b9b5fp-1, 0x1.dd321f301b460p-1, 0x1.da9e603db3285p-1, 0x1.d80e316c98398p-1};
 
 struct Sample {
     const void *logits;
@@ -77,86 +82,112 @@ __device__ __forceinline__ int index_of(uint64_t e) {
     return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e));
 }
 
-template <typename T, int THREADS, int BINS, int LIST>
+// A value that is the same on every lane, into scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) {
+    return __uint_as_float(uniform(__float_as_uint(v)));
+}
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+    return static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32 |
+           uniform(static_cast<uint32_t>(v));
+}
+__device__ __forceinline__ double uniform(double v) {
+    return __longlong_as_double(uniform(static_cast<uint64_t>(__double_as_longlong(v))));
+}
+
+template <typename T, int THREADS, int BINS>
 struct Draw {
     typedef typename T::bits B;
     static constexpr int kWaves = THREADS / 64;
     static constexpr int V = 16 / sizeof(B);         // values of a load
-    static constexpr int kEach = BINS / THREADS;
+    static constexpr int kList = 2 * BINS;
+    static constexpr float kBins = BINS;
 
-    // Few elements and what comes before each of them.
     struct Few {
-        uint64_t element[kSmall], amount[kSmall], before[kSmall];
-        int rank[kSmall];
+        uint64_t element[kSmall];
         int count;
     };
     struct Shared {
-        uint64_t mass[BINS];         // weight by distance to the largest logit
-        uint64_t other[BINS];        // counts, and the finer divisions
-        uint64_t list[LIST];         // all that may belong to the first k
-        Few end, draw;               // around the nucleus's end, around the draw
-        double table[kTable];
+        uint64_t wide[2 * BINS];     // units by bin, then the running weight with
+                                     // each; or all that may belong to the first k
+        uint64_t other[BINS];        // counts, the finer divisions, listed runs
+        Few end, draw, likely;       // around the k-th or the nucleus's end, around
+                                     // the draw, around min_p
+        uint64_t amount[kSmall], before[kSmall];     // of few elements
+        int rank[kSmall];
+        double coarse[2 * BINS / 64], fine[64], lift;   // see factor()
         uint64_t sums[2][kWaves];
         float most[kWaves];
-        uint64_t found_before[2], found_amount[2], found_element;
-        int found[2], count, runs;
+        uint64_t found_before, found_element, found_upto, total;
+        int found, count, runs;
         uint32_t lo, hi;
-    };
-    // A histogram's running sum: this thread's bins and what lies before them.
-    struct Running {
-        uint64_t own[kEach], before, total;
     };
 
     Shared &s;
     const B *row;
     int K, tid;
     float m, scale;                  // largest logit; bins per unit of logit
-    double rate;                     // 128 log2(e) / temperature
+    float ref;                       // the bins lie around it, BINS on either side
+    double rate;                     // bins per unit of logit
     uint64_t limit;                  // elements below it are not among the first k
-    int listed;                      // elements in list, or -1: the row itself
 
-    // f(z, i) for every run of the row: V values from index i on, -infinity past
-    // its end; VALUES of a thread in flight.
-    template <int VALUES, typename F>
-    __device__ __forceinline__ void for_runs(const F &f) const {
-        constexpr int U = VALUES / V;
-        constexpr int kStep = THREADS * VALUES;
-        auto give = [&](const Packed<B, V> &p, int c) __attribute__((always_inline)) {
-            float z[V];
+    // Loads U runs of V values, THREADS V values from one to the next, the first
+    // from c0 on (of the workgroup's block from base on); -infinity past n.
+    template <int U>
+    __device__ __forceinline__ void load_block(Packed<B, V> (&v)[U], int base, int c0, int n) const {
+        if (base + THREADS * V * U <= n) {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                z[e] = c + e < K ? T::widen(p.v[e]) : -INFINITY;
-            f(z, c);
-        };
-#pragma unroll 1
-        for (int base = 0; base < K; base += kStep) {
-            const int c0 = base + tid * V;
-            if (base + kStep <= K) {
-                Packed<B, V> v[U];
+            for (int x = 0; x < U; ++x)
+                v[x] = load_packed<B, V>(row + c0 + x * THREADS * V);
+        } else {
 #pragma unroll
-                for (int x = 0; x < U; ++x)
-                    v[x] = load_packed<B, V>(row + c0 + x * THREADS * V);
-                __builtin_amdgcn_sched_barrier(0);
+            for (int x = 0; x < U; ++x) {
+                const int c = c0 + x * THREADS * V;
 #pragma unroll
-                for (int x = 0; x < U; ++x) {
-                    float z[V];
+                for (int e = 0; e < V; ++e)
+                    v[x].v[e] = T::narrow(-INFINITY);
+                if (c + V <= n)
+                    v[x] = load_packed<B, V>(row + c);
+                else
+                    for (int e = 0; c + e < n; ++e)
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        z[e] = T::widen(v[x].v[e]);
-                    f(z, c0 + x * THREADS * V);
-                }
-            } else {
-#pragma unroll 1
-                for (int c = c0; c < K; c += THREADS * V)
-                    give(load_run<B, V>(row + c, K - c), c);
+                        for (int y = 0; y < V; ++y)
+                            if (y == e)
+                                v[x].v[y] = row[c + e];
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // f(z, i) for every run of the row's first n values: V of them from index i on,
+    // -infinity past the end; VALUES of a thread in flight.
+    template <int VALUES, typename F>
+    __device__ __forceinline__ void for_runs(int n, const F &f) const {
+        constexpr int U = VALUES / V;
+#pragma unroll 1
+        for (int base = 0; base < n; base += THREADS * VALUES) {
+            const int c0 = base + tid * V;
+            Packed<B, V> v[U];
+            load_block(v, base, c0, n);
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                float z[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    z[e] = T::widen(v[x].v[e]);
+                f(z, c0 + x * THREADS * V);
+            }
+        }
+    }
+    template <int VALUES, typename F>
+    __device__ __forceinline__ void for_runs(const F &f) const {
+        for_runs<VALUES>(K, f);
     }
     // f(z, i) for every element with test(z).  Few are expected: a run without
     // any costs no more than the tests.
     template <typename P, typename F>
     __device__ __forceinline__ void for_some(const P &test, const F &f) const {
-        for_runs<32>([&](const float (&z)[V], int i) __attribute__((always_inline)) {
+        for_runs<2 * V>([&](const float (&z)[V], int i) __attribute__((always_inline)) {
             bool any = false;
 #pragma unroll
             for (int e = 0; e < V; ++e)
@@ -169,72 +200,75 @@ struct Draw {
                     f(z[e], i + e);
         });
     }
-    // The same of those that may still be drawn.
+    // The same of those among the first k.
     template <typename P, typename F>
     __device__ __forceinline__ void for_kept(const P &test, const F &f) const {
-        if (listed >= 0) {
-            for (int y = tid; y < listed; y += THREADS) {
-                const uint64_t e = s.list[y];
-                const float z = value_of(static_cast<uint32_t>(e >> 32));
-                if (e >= limit && test(z))
-                    f(z, index_of(e));
-            }
-            return;
-        }
         for_some(test, [&](float z, int i) __attribute__((always_inline)) {
             if (limit == 0 || element_of(key_of(z), i) >= limit)
                 f(z, i);
         });
     }
-    __device__ __forceinline__ bool in_span(float z) const {
-        return place(z) < static_cast<float>(BINS);
-    }
-    // Counts by bin of all that may still be drawn.
-    __device__ __forceinline__ void count_bins() {
-        __syncthreads();
-        clear(s.other);
-        __syncthreads();
-        for_kept([&](float z) __attribute__((always_inline)) { return in_span(z); },
-                 [&](float z, int) __attribute__((always_inline)) {
-                     add(&s.other[static_cast<int>(place(z))], 1);
-                 });
+
+    // Distance to ref in bins, not decreasing as logits do, and a half: a bin's
+    // centre lies at a whole distance, so that logits as good as equal to ref get
+    // the weight one exactly.  NaN of a NaN.
+    __device__ __forceinline__ float place(float z) const { return (ref - z) * scale + 0.5f; }
+    // Whether a logit has a bin, and which.
+    __device__ __forceinline__ bool in_span(float z) const { return fabsf(place(z)) < kBins; }
+    __device__ __forceinline__ int bin_of(float z) const {
+        return static_cast<int>(floorf(place(z))) + BINS;
     }
 
-    // Distance to the largest logit (a finite one) in bins, not decreasing with
-    // it; from BINS on a weight is zero.  NaN of a NaN.
-    __device__ __forceinline__ float place(float z) const { return (m - z) * scale; }
-
-    // exp((z - m) / t) in units of 2^-43, of a logit in a bin.  2^(-y / 128),
-    // y = n + f: a table for n's low bits, its high ones an exponent, and a
-    // polynomial for f (|f| <= 1/2; the term left out is 1e-15 at most).
+    // exp(-d h) in units of 2^-43, d the distance of a logit to its bin's centre in
+    // bins (of h temperatures): the powers of d up to one whose successor is 4e-16
+    // at most.  The last sum puts the integer into the low bits.
+    __device__ __forceinline__ uint64_t unit(float z, int b) const {
+        constexpr double h = kSpan / BINS;
+        constexpr int kTerms = BINS >= 2048 ? 6 : 8;
+        static_assert(BINS >= 512, "terms by the width of a bin");
+        constexpr double one = 8796093022208.0;                      // 2^43
+        constexpr double kMagic = 4503599627370496.0;                // 2^52
+        const double d = fma(static_cast<double>(ref) - static_cast<double>(z), rate,
+                             -static_cast<double>(b - BINS));
+        double c[kTerms];
+        c[0] = one;
+#pragma unroll
+        for (int n = 1; n < kTerms; ++n)
+            c[n] = c[n - 1] * -h / n;
+        double p = c[kTerms - 1];
+#pragma unroll
+        for (int n = kTerms - 2; n >= 1; --n)
+            p = fma(p, d, c[n]);
+        p = fma(p, d, c[0] + kMagic);
+        return __double_as_longlong(p) & 0xfffffffffffffull;
+    }
+    // Weight of a bin's centre against the largest logit: exp(h (distance of the
+    // largest - that of the centre)), from exp(-h i) in two factors and `lift`,
+    // exp(h distance of the largest).
+    __device__ __forceinline__ double factor(int b) const {
+        return s.coarse[b / 64] * s.fine[b % 64] * s.lift;
+    }
+    __device__ __forceinline__ void make_table() {
+        constexpr int kCoarse = 2 * BINS / 64;
+        static_assert(kCoarse + 64 <= THREADS, "one entry to a thread");
+        if (tid < kCoarse + 64) {
+            const int i = tid < kCoarse ? 64 * tid - BINS : tid - kCoarse;
+            (tid < kCoarse ? s.coarse[tid] : s.fine[i]) = exp(-(kSpan / BINS) * i);
+        }
+    }
+    static __device__ __forceinline__ uint64_t whole(double v) {
+        return static_cast<uint64_t>(v + 0.5);
+    }
+    // exp((z - m) / t) in units of 2^-43, of one of few.
     __device__ __forceinline__ uint64_t weight(float z) const {
-        constexpr double kMagic = 6755399441055744.0;                // 1.5 2^52
-        const double y = (static_cast<double>(m) - static_cast<double>(z)) * rate;
-        const double magic = y + kMagic;
-        const int n = static_cast<int>(__double_as_longlong(magic));
-        constexpr double c = 0.69314718055994530942 / kTable;
-        const double f = (magic - kMagic) - y;
-        double p = c * c * c * c / 24;
-        p = fma(p, f, c * c * c / 6);
-        p = fma(p, f, c * c / 2);
-        p = fma(p, f, c);
-        p = fma(p, f, 1.0);
-        const double w = ldexp(p * s.table[n & (kTable - 1)], kWeightBits - (n >> 7));
-        return __double_as_longlong(w + 4503599627370496.0) & 0xfffffffffffffull;   // 2^52
-    }
-    template <bool COUNT>
-    __device__ __forceinline__ uint64_t amount_of(uint64_t e) const {
-        return COUNT ? uint64_t(1) : weight(value_of(static_cast<uint32_t>(e >> 32)));
+        const double x = (static_cast<double>(m) - static_cast<double>(z)) * rate * (kSpan / BINS);
+        return x < kSpan ? whole(exp(-x) * (1ull << kWeightBits)) : 0;
     }
 
-    static __device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
+    __device__ __forceinline__ uint64_t group_sum(uint64_t v) {
 #pragma unroll
         for (int x = 32; x >= 1; x >>= 1)
             v += __shfl_xor(v, x, 64);
-        return v;
-    }
-    __device__ __forceinline__ uint64_t group_sum(uint64_t v) {
-        v = wave_sum(v);
         __syncthreads();
         if ((tid & 63) == 0)
             s.sums[0][tid >> 6] = v;
@@ -243,18 +277,43 @@ struct Draw {
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
             total += s.sums[0][w];
-        return total;
+        return uniform(total);
+    }
+    __device__ __forceinline__ float group_most(float v) {
+#pragma unroll
+        for (int x = 32; x >= 1; x >>= 1)
+            v = fmaxf(v, __shfl_xor(v, x, 64));
+        __syncthreads();
+        if ((tid & 63) == 0)
+            s.most[tid >> 6] = v;
+        __syncthreads();
+        v = s.most[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w)
+            v = fmaxf(v, s.most[w]);
+        return uniform(v);
     }
 
-    // Begins with a barrier: the histogram is whole.
-    __device__ __forceinline__ Running running(const uint64_t *hist) {
-        Running r;
+    // Replaces N bins by the running sums with each of what amount(bin, sum) makes
+    // of them; returns the total.  Begins and ends with a barrier.
+    template <int N, typename F>
+    __device__ __forceinline__ uint64_t run_sums(uint64_t *hist, const F &amount) {
+        constexpr int kEach = N / THREADS;
+        uint64_t own[kEach], v = 0;
         __syncthreads();
-        uint64_t v = 0;
 #pragma unroll
         for (int x = 0; x < kEach; ++x) {
-            r.own[x] = hist[tid * kEach + x];
-            v += r.own[x];
+            own[x] = hist[tid * kEach + x];
+            v |= own[x];
+        }
+        const bool any = __ballot(v != 0) != 0;         // often not: few bins are in use
+        v = 0;
+        if (any) {
+#pragma unroll
+            for (int x = 0; x < kEach; ++x) {
+                own[x] = amount(tid * kEach + x, own[x]);
+                v += own[x];
+            }
         }
         uint64_t run = v;
 #pragma unroll
@@ -265,48 +324,40 @@ struct Draw {
         if ((tid & 63) == 63)
             s.sums[1][tid >> 6] = run;
         __syncthreads();
-        uint64_t total = 0, base = 0;
+        uint64_t total = 0, at = run - v;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             const uint64_t sum = s.sums[1][w];
-            base += w < tid >> 6 ? sum : 0;
+            at += w < tid >> 6 ? sum : 0;
             total += sum;
         }
-        r.before = base + run - v;
-        r.total = total;
-        return r;
-    }
-    // The bins where the running sum reaches two targets (1 to the total), and
-    // the sums before them and their own.
-    __device__ __forceinline__ void find(const Running &r, uint64_t target, uint64_t second) {
-        __syncthreads();
-        uint64_t at = r.before;
 #pragma unroll
         for (int x = 0; x < kEach; ++x) {
-#pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const uint64_t want = which == 0 ? target : second;
-                if (at < want && want <= at + r.own[x]) {
-                    s.found[which] = tid * kEach + x;
-                    s.found_before[which] = at;
-                    s.found_amount[which] = r.own[x];
-                }
-            }
-            at += r.own[x];
+            at += own[x];
+            hist[tid * kEach + x] = at;
         }
         __syncthreads();
+        return uniform(total);
     }
-    // The same for one target in a histogram; false where the total is less.
-    __device__ __forceinline__ bool locate(const uint64_t *hist, uint64_t target) {
-        const Running r = running(hist);
-        if (target == 0 || target > r.total)
-            return false;
-        find(r, target, target);
-        return true;
+    // The first of N bins whose running sum reaches `target` (N: none does): each
+    // lane looks at the last of 64 bins, then at one of those 64.
+    template <int N>
+    __device__ __forceinline__ int find(const uint64_t *sums, uint64_t target) const {
+        const int lane = tid & 63;
+        static_assert(N % 64 == 0 && N <= 64 * 64, "two looks");
+        const uint64_t last = sums[min(lane, N / 64 - 1) * 64 + 63];
+        const int block = __popcll(__ballot(lane < N / 64 && last < target));
+        if (block == N / 64)
+            return N;
+        return block * 64 + __popcll(__ballot(sums[block * 64 + lane] < target));
+    }
+    static __device__ __forceinline__ uint64_t before(const uint64_t *sums, int b) {
+        return uniform(b > 0 ? sums[b - 1] : uint64_t(0));
     }
 
+    template <int N>
     __device__ __forceinline__ void clear(uint64_t *hist) {
-        for (int x = tid; x < BINS; x += THREADS)
+        for (int x = tid; x < N; x += THREADS)
             hist[x] = 0;
     }
     static __device__ __forceinline__ void add(uint64_t *p, uint64_t v) {
@@ -317,41 +368,54 @@ struct Draw {
         if (x < kSmall)
             few.element[x] = e;
     }
-    // Calls f(z, i) for the elements of the row with test(z), a few hundred of
-    // them, in two steps: the runs that hold one are listed, one count for those
+    // Calls f(z, i) for the elements of the row with miss(z) <= 0, a few hundred of
+    // them (numbers, since masks of lanes are slow to combine), in two steps: the runs that hold one are listed, one count for those
     // of a wave; then each thread takes some of them.  So the loop over the row
-    // has no more than the tests (a wave's 256 or 512 elements hold a hit more
+    // has little more than the tests (a wave's 256 or 512 elements hold a hit more
     // often than not).  Where there are more runs than `runs` holds, one step.
     template <typename P, typename F>
-    __device__ __forceinline__ void for_listed(const P &test, const F &f) {
+    __device__ __forceinline__ void for_listed(const P &miss, const F &f) {
         auto *runs = reinterpret_cast<int *>(s.other);
         constexpr int kRoom = 2 * BINS;
+        constexpr int U = 32 / V;
         __syncthreads();
         if (tid == 0)
             s.runs = 0;
         __syncthreads();
-        for_runs<32>([&](const float (&z)[V], int i) __attribute__((always_inline)) {
-            bool any = false;
+#pragma unroll 1
+        for (int base = 0; base < K; base += THREADS * 32) {
+            const int c0 = base + tid * V;
+            Packed<B, V> v[U];
+            load_block(v, base, c0, K);
+            uint32_t hits = 0;
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                any |= test(z[e]);
-            const uint64_t mask = __ballot(any);
-            if (mask == 0)
-                return;
-            int at = 0;
-            const int before = __builtin_amdgcn_mbcnt_hi(
-                static_cast<uint32_t>(mask >> 32),
-                __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
-            if (any && before == 0)
-                at = atomicAdd(&s.runs, __popcll(mask));
-            at = __builtin_amdgcn_readlane(at, __builtin_ctzll(mask)) + before;
-            if (any && at < kRoom)
-                runs[at] = i;
-        });
+            for (int x = 0; x < U; ++x) {
+                float least = INFINITY;
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    least = fminf(least, miss(T::widen(v[x].v[e])));
+                hits |= least <= 0.0f ? 1u << x : 0;
+            }
+            for (;;) {                                  // a run of each lane at a time
+                const uint64_t mask = __ballot(hits != 0);
+                if (mask == 0)
+                    break;
+                const int before = __builtin_amdgcn_mbcnt_hi(
+                    static_cast<uint32_t>(mask >> 32),
+                    __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+                int at = 0;
+                if (hits != 0 && before == 0)
+                    at = atomicAdd(&s.runs, __popcll(mask));
+                at = __builtin_amdgcn_readlane(at, __builtin_ctzll(mask)) + before;
+                if (hits != 0 && at < kRoom)
+                    runs[at] = c0 + __builtin_ctz(hits) * THREADS * V;
+                hits &= hits - 1;
+            }
+        }
         __syncthreads();
         const int n = s.runs;
         if (n > kRoom) {
-            for_some(test, f);
+            for_some([&](float z) __attribute__((always_inline)) { return miss(z) <= 0.0f; }, f);
             return;
         }
         for (int y = tid; y < n; y += THREADS) {
@@ -360,20 +424,23 @@ struct Draw {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float z = i + e < K ? T::widen(v.v[e]) : -INFINITY;
-                if (test(z))
+                if (miss(z) <= 0.0f)
                     f(z, i + e);
             }
         }
     }
+
     // For each of few elements, how many come before it in the order, and their
-    // weight.  Thread (part, x) adds up its part's share for element x.
-    __device__ __forceinline__ void rank_all(Few &few) {
+    // amounts (amount(z)).  Thread (part, x) adds up its part's share for element
+    // x.
+    template <typename F>
+    __device__ __forceinline__ void rank_all(const Few &few, const F &amount) {
         constexpr int kParts = THREADS / kSmall;
         const int n = few.count;
         if (tid < n) {
-            few.amount[tid] = amount_of<false>(few.element[tid]);
-            few.before[tid] = 0;
-            few.rank[tid] = 0;
+            s.amount[tid] = amount(value_of(static_cast<uint32_t>(few.element[tid] >> 32)));
+            s.before[tid] = 0;
+            s.rank[tid] = 0;
         }
         __syncthreads();
         const int x = tid % kSmall, part = tid / kSmall;
@@ -385,94 +452,103 @@ struct Draw {
 #pragma unroll 4
             for (int y = beg; y < end; ++y) {
                 const bool first = few.element[y] > mine;
-                sum += first ? few.amount[y] : 0;
+                sum += first ? s.amount[y] : 0;
                 rank += first;
             }
-            add(&few.before[x], sum);
-            atomicAdd(&few.rank[x], rank);
+            add(&s.before[x], sum);
+            atomicAdd(&s.rank[x], rank);
         }
+        __syncthreads();
+        if (tid < n && s.rank[tid] == n - 1)
+            s.total = s.before[tid] + s.amount[tid];
         __syncthreads();
     }
-    // Of few ranked elements the one at which the weight reaches `target`; `upto`
-    // is the weight with it.  Ends with a barrier.
+    // Of few ranked elements the one at which the amount reaches `target`, the
+    // last one with an amount where none does; `upto` is the amount with it.  Ends
+    // with a barrier.
     __device__ __forceinline__ uint64_t find_few(const Few &few, uint64_t target, uint64_t &upto) {
-        if (tid < few.count) {
-            const uint64_t at = few.before[tid], own = few.amount[tid];
-            if (at < target && target <= at + own) {
-                s.found_element = few.element[tid];
-                s.found_amount[0] = at + own;
-            }
+        const bool real = tid < few.count;
+        const uint64_t at = real ? s.before[tid] : 0, own = real ? s.amount[tid] : 0;
+        target = min(target, uniform(s.total));
+        if (real && at < target && target <= at + own) {
+            s.found_element = few.element[tid];
+            s.found_upto = at + own;
         }
         __syncthreads();
-        upto = s.found_amount[0];
-        const uint64_t e = s.found_element;
+        upto = uniform(s.found_upto);
+        const uint64_t e = uniform(s.found_element);
         __syncthreads();
         return e;
     }
 
-    // The element of bin b at which the running amount within the bin (of
-    // elements where COUNT, else of weight) reaches `target`, by the bits of their
-    // values, then, among equal ones, of their indexes; `upto` is that running
-    // amount, its own included.  For bins of many elements.
-    template <bool COUNT>
-    __device__ __forceinline__ uint64_t divide(int b, uint64_t target, uint64_t &upto) {
-        const float beg = static_cast<float>(b), end = static_cast<float>(b + 1);
-        __syncthreads();
+    // The value in bin b at which the running amount within the bin (of elements
+    // where `count`, else of units) reaches `target`, by the values' bits, and
+    // which of the elements of that value; `upto` is that running amount, its own
+    // included.  For bins of many elements.
+    __device__ __forceinline__ uint32_t divide(bool count, int b, uint64_t target, uint64_t &nth,
+                                               uint64_t &upto) {
+        auto inside = [&](float z) __attribute__((always_inline)) {
+            return in_span(z) && bin_of(z) == b;
+        };
         if (tid == 0) {
             s.lo = 0xffffffffu;
             s.hi = 0;
         }
         __syncthreads();
-        auto inside = [&](float z) __attribute__((always_inline)) {
-            const float x = place(z);
-            return x >= beg && x < end;
-        };
         for_kept(inside, [&](float z, int) __attribute__((always_inline)) {
             atomicMin(&s.lo, key_of(z));
             atomicMax(&s.hi, key_of(z));
         });
         __syncthreads();
-        uint32_t lo = s.lo, hi = s.hi;
+        uint32_t lo = uniform(s.lo), hi = uniform(s.hi);
         uint64_t sum = 0;
         while (lo < hi) {
             const int shift = max(0, 32 - __builtin_clz(hi - lo) - __builtin_ctz(BINS));
-            clear(s.other);
+            clear<BINS>(s.other);
             __syncthreads();
-            for_kept(inside, [&](float z, int i) __attribute__((always_inline)) {
+            for_kept(inside, [&](float z, int) __attribute__((always_inline)) {
                 const uint32_t key = key_of(z);
                 if (key >= lo && key <= hi)
-                    add(&s.other[(hi - key) >> shift], amount_of<COUNT>(element_of(key, i)));
+                    add(&s.other[(hi - key) >> shift], count ? uint64_t(1) : unit(z, b));
             });
-            if (!locate(s.other, target - sum))         // only if the row changed meanwhile
+            const uint64_t total =
+                run_sums<BINS>(s.other, [](int, uint64_t v) __attribute__((always_inline)) { return v; });
+            target = min(target, sum + total);
+            const int at = find<BINS>(s.other, target - sum);
+            sum += before(s.other, at);
+            __syncthreads();
+            if (at >= BINS)                             // only if the row changed meanwhile
                 break;
-            sum += s.found_before[0];
-            hi -= static_cast<uint32_t>(s.found[0]) << shift;
+            hi -= static_cast<uint32_t>(at) << shift;
             const uint32_t rest = (1u << shift) - 1;
             lo = hi - lo > rest ? hi - rest : lo;
         }
-        const uint32_t key = lo;
-        const uint64_t each = max(amount_of<COUNT>(element_of(key, 0)), uint64_t(1));
-        uint64_t nth = (target - sum + each - 1) / each;              // of the equal ones
+        const uint64_t each = uniform(count ? 1 : max(unit(value_of(lo), b), uint64_t(1)));
+        nth = max((target - sum + each - 1) / each, uint64_t(1));
         upto = sum + nth * each;
-        return element_of(key, nth_of(key, nth));
+        return lo;
     }
     // Index of the nth (from 1) element of this value.
     __device__ __forceinline__ int nth_of(uint32_t key, uint64_t nth) {
         int first = 0, last = K - 1;
         while (first < last) {
             const int shift = max(0, 32 - __builtin_clz(last - first) - __builtin_ctz(BINS));
-            __syncthreads();
-            clear(s.other);
+            clear<BINS>(s.other);
             __syncthreads();
             for_some([&](float z) __attribute__((always_inline)) { return key_of(z) == key; },
                      [&](float, int i) __attribute__((always_inline)) {
                          if (i >= first && i <= last)
                              add(&s.other[(i - first) >> shift], 1);
                      });
-            if (!locate(s.other, nth))
+            const uint64_t total =
+                run_sums<BINS>(s.other, [](int, uint64_t v) __attribute__((always_inline)) { return v; });
+            nth = min(nth, total);                      // less only if the row changed
+            const int at = find<BINS>(s.other, nth);
+            nth -= before(s.other, at);
+            __syncthreads();
+            if (at >= BINS || nth == 0)
                 break;
-            nth -= s.found_before[0];
-            first += s.found[0] << shift;
+            first += at << shift;
             last = min(last, first + (1 << shift) - 1);
         }
         return first;
@@ -483,272 +559,395 @@ struct Draw {
         const double at = static_cast<double>(u) * static_cast<double>(total);
         if (!(at > 0.0))
             return 1;
-        return at < static_cast<double>(total) ? min(static_cast<uint64_t>(at), total - 1) + 1
-                                               : total;
+        return uniform(at < static_cast<double>(total)
+                           ? min(static_cast<uint64_t>(at), total - 1) + 1
+                           : total);
     }
     // The least running weight that has p of `total`.
     static __device__ __forceinline__ uint64_t share(float p, uint64_t total) {
         const double want = ceil(static_cast<double>(p) * static_cast<double>(total));
-        return want >= 1.0 ? min(static_cast<uint64_t>(want), total) : uint64_t(1);
+        return uniform(want >= 1.0 ? min(static_cast<uint64_t>(want), total) : uint64_t(1));
     }
 
-    static __device__ __forceinline__ uint64_t least_weight(float min_p) {
-        return min_p > 0.0f ? static_cast<uint64_t>(ceil(fmin(static_cast<double>(min_p), 1.0) *
-                                                         (1ull << kWeightBits)))
-                            : 0;
-    }
-
-    // Gathers every element up to bin b into the list; false where they are more
-    // than it holds.
-    __device__ __forceinline__ bool gather(int b) {
-        const float end = static_cast<float>(b + 1);
+    // Gathers every element with place(z) <= end; their number, -1 where they are
+    // more than fit.
+    __device__ __forceinline__ int gather(float end) {
         __syncthreads();
         if (tid == 0)
             s.count = 0;
-        __syncthreads();
-        for_listed([&](float z) __attribute__((always_inline)) { return place(z) < end; },
+        for_listed([&](float z) __attribute__((always_inline)) { return place(z) - end; },
                    [&](float z, int i) __attribute__((always_inline)) {
                        const int x = atomicAdd(&s.count, 1);
-                       if (x < LIST)
-                           s.list[x] = element_of(key_of(z), i);
+                       if (x < 2 * BINS)
+                           s.wide[x] = element_of(key_of(z), i);
                    });
         __syncthreads();
-        const bool whole = s.count <= LIST;
-        listed = whole ? s.count : -1;
-        return whole;
+        return s.count <= 2 * BINS ? s.count : -1;
     }
 
-    // All that can be drawn is in the list and few: every border from their
-    // order.
-    __device__ __forceinline__ int from_few(int k, float p, float min_p, float u) {
+    // All that can be drawn is gathered and few: every border from their order.
+    __device__ __forceinline__ int from_few(int n, int k, float p, float min_p, float u) {
         Few &few = s.draw;
         __syncthreads();
-        if (tid < listed)
-            few.element[tid] = s.list[tid];
+        if (tid < n)
+            few.element[tid] = s.wide[tid];
         if (tid == 0)
-            few.count = listed;
+            few.count = n;
         __syncthreads();
-        rank_all(few);
-        const uint64_t least = least_weight(min_p);
+        rank_all(few, [&](float z) __attribute__((always_inline)) { return weight(z); });
         // Weight of the first k, and of those with w >= min_p.
-        uint64_t first = 0, likely = 0;
-        if (tid < listed) {
-            const uint64_t own = few.amount[tid];
-            first = few.rank[tid] < k ? own : 0;
-            likely = own >= least ? own : 0;
+        uint64_t total = uniform(s.total), likely = 0;
+        if (k < n) {
+            if (tid < n && s.rank[tid] == k - 1)
+                s.found_upto = s.before[tid] + s.amount[tid];
+            __syncthreads();
+            total = uniform(s.found_upto);
         }
-        uint64_t total = group_sum(first);
-        if (min_p > 0.0f)
-            likely = group_sum(likely);
+        if (min_p > 0.0f) {
+            const double least = fmin(static_cast<double>(min_p), 1.0) * (1ull << kWeightBits);
+            likely = group_sum(tid < n && static_cast<double>(s.amount[tid]) >= least ? s.amount[tid]
+                                                                                      : 0);
+        }
+        uint64_t upto;
         if (p < 1.0f) {
-            uint64_t upto;
             find_few(few, share(p, total), upto);
             total = upto;
         }
         if (min_p > 0.0f)
             total = min(total, likely);
-        uint64_t upto;
         return index_of(find_few(few, drawn(u, total), upto));
     }
 
-    // Logits of +infinity share the row: weights of one each.
-    __device__ __forceinline__ int from_infinities(float t, int k, float p, float u) {
-        uint64_t n = 0;
-        for_runs<32>([&](const float (&z)[V], int) __attribute__((always_inline)) {
+    // The histogram around ref of the whole row; returns the row's largest.
+    __device__ __forceinline__ float weigh_row() {
+        __syncthreads();
+        clear<2 * BINS>(s.wide);
+        __syncthreads();
+        float most = -INFINITY;
+        // The units of a run together, without a branch between them (outside the
+        // span they are anything).
+        for_runs<16>([&](const float (&z)[V], int) __attribute__((always_inline)) {
+            uint64_t w[V];
+            float x[V];
+            int b[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                most = fmaxf(most, z[e]);
+                x[e] = place(z[e]);
+                b[e] = static_cast<int>(floorf(x[e])) + BINS;
+                w[e] = unit(z[e], b[e]);
+            }
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                n += z[e] == INFINITY;
+                if (fabsf(x[e]) < kBins)
+                    add(&s.wide[b[e]], w[e]);
         });
-        n = group_sum(n);
-        if (k > 0)
-            n = min(n, static_cast<uint64_t>(k));
-        if (p < 1.0f)
-            n = (share(p, n << kWeightBits) + (1ull << kWeightBits) - 1) >> kWeightBits;
-        const uint64_t target = t > 0.0f ? drawn(u, n << kWeightBits) : 1;
-        return nth_of(key_of(INFINITY), (target + (1ull << kWeightBits) - 1) >> kWeightBits);
+        return group_most(most);
     }
 
     // The row's label, the same on every thread.
     __device__ __forceinline__ int run(float t, int k, float p, float min_p, float u) {
-        if (tid < kTable)
-            s.table[tid] = kEighths[tid >> 4] * k128ths[tid & 15];
-        clear(s.mass);
-        clear(s.other);
-        float mine = -INFINITY;
-        for_runs<32>([&](const float (&z)[V], int) __attribute__((always_inline)) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                mine = fmaxf(mine, z[e]);
-        });
-        float most = mine;
-#pragma unroll
-        for (int x = 32; x >= 1; x >>= 1)
-            most = fmaxf(most, __shfl_xor(most, x, 64));
-        if ((tid & 63) == 0)
-            s.most[tid >> 6] = most;
-        if (tid == 0)
-            s.count = K;
-        __syncthreads();
-        m = s.most[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w)
-            m = fmaxf(m, s.most[w]);
-        if (m == -INFINITY)
-            return -1;                                  // nothing to draw
-        if (m == INFINITY)
-            return from_infinities(t, k, p, u);
-        if (!(t > 0.0f)) {
-            int first = K;
-            for_some([&](float z) __attribute__((always_inline)) { return z == m; },
-                     [&](float, int i) __attribute__((always_inline)) { first = min(first, i); });
-            if (first < K)
-                atomicMin(&s.count, first);
-            __syncthreads();
-            return s.count;
-        }
-        t = fmaxf(t, 0x1p-120f);                        // scale stays finite
-        scale = BINS / kSpan / t;
-        rate = kTable * 1.44269504088896340736 / static_cast<double>(t);
-        limit = 0;
-        listed = -1;
         if (k <= 0 || k > K)
             k = K;
-
-        if (k < K) {
-            // The k-th largest of the threads' own largest is no larger than the
-            // row's k-th: all from its bin up are gathered, a few more than k.
-            // With more than THREADS to keep, or too many gathered, the row's own
-            // counts say where the k-th is.
-            const float x = place(mine);
-            if (x < static_cast<float>(BINS))
-                add(&s.other[static_cast<int>(x)], 1);
-            bool more = locate(s.other, k);             // than k in the span, or k
-            if (!more || !gather(s.found[0])) {
-                count_bins();
-                more = locate(s.other, k);
-                if (more && s.found_before[0] + s.found_amount[0] <= LIST)
-                    gather(s.found[0]);
-            }
-            if (listed >= 0 && listed <= kSmall)
-                return from_few(k, p, min_p, u);
-            if (more) {
-                if (listed >= 0) {
-                    count_bins();
-                    locate(s.other, k);
-                }
-                uint64_t upto;
-                const int at = s.found[0];
-                limit = divide<true>(at, k - s.found_before[0], upto);
-            }
-        } else if (min_p > 0.0f && !(p < 1.0f)) {
-            // Those with w >= min_p, and a bin more for roundings.
-            const float x = -logf(fminf(min_p, 1.0f)) * (BINS / kSpan);
-            if (x < static_cast<float>(BINS - 2) && gather(static_cast<int>(x) + 1) &&
-                listed <= kSmall)
-                return from_few(k, p, min_p, u);
-            listed = -1;
-        }
-
-        const uint64_t least = least_weight(min_p);
-        uint64_t likely = 0;                            // weight of those with w >= min_p
-        auto weigh = [&](float x, uint64_t w) __attribute__((always_inline)) {
-            add(&s.mass[static_cast<int>(x)], w);
-            if (min_p > 0.0f)
-                likely += w >= least ? w : 0;
-        };
-        if (listed >= 0 || limit != 0) {
-            for_kept(
-                [&](float z) __attribute__((always_inline)) { return in_span(z); },
-                [&](float z, int) __attribute__((always_inline)) { weigh(place(z), weight(z)); });
-        } else {
-            // The weights of a run together, without a branch between them (past
-            // the span they are anything).
-            for_runs<16>([&](const float (&z)[V], int) __attribute__((always_inline)) {
-                uint64_t w[V];
+        const bool greedy = !(t > 0.0f);
+        t = fminf(fmaxf(t, 0x1p-120f), 0x1p120f);       // scale and its inverse stay finite
+        scale = uniform(BINS / kSpan / t);
+        rate = uniform((BINS / kSpan) / static_cast<double>(t));
+        limit = 0;
+        make_table();
+        // What the loop below is to find: the border `border` in bin `bin`, where
+        // the running units (or elements) reach `target`, or the nth element of
+        // the value `key`.
+        enum { kValue, kLimit, kEnd, kDraw } border = kValue;
+        uint32_t key = 0;
+        uint64_t nth = 1, target = 0;
+        int bin = 0;
+        // Whether all may be drawn: then all are weighed, around the largest of
+        // the first ones.
+        bool weighed = false;
+        if (!greedy && K > kSmall && k == K && (p < 1.0f || !(min_p > 0.0f))) {
+            float most = -INFINITY;
+            for_runs<V>(min(K, kFirst), [&](const float (&z)[V], int) __attribute__((always_inline)) {
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    w[e] = weight(z[e]);
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (in_span(z[e]))
-                        weigh(place(z[e]), w[e]);
+                    most = fmaxf(most, z[e]);
             });
-        }
-        if (tid == 0)
-            s.end.count = s.draw.count = 0;
-        likely = min_p > 0.0f ? group_sum(likely) : ~0ull;
-        const Running r = running(s.mass);
-        // The weight of all kept lies between lo and hi: the nucleus ends within
-        // a bin.
-        uint64_t lo = r.total, hi = r.total, before_end = 0, in_end = 0;
-        int end = -1;
-        if (p < 1.0f) {
-            const uint64_t target = share(p, r.total);
-            find(r, target, target);
-            end = s.found[0];
-            before_end = s.found_before[0];
-            in_end = target - before_end;
-            lo = before_end + 1;
-            hi = before_end + s.found_amount[0];
-        }
-        lo = min(lo, likely);
-        hi = min(hi, likely);
-        find(r, drawn(u, lo), drawn(u, hi));
-        const int from = s.found[0], to = s.found[1];
-        const uint64_t before_from = s.found_before[0];
-        auto bin = [&](float z) __attribute__((always_inline)) {       // of any value
-            return static_cast<int>(fminf(place(z), static_cast<float>(BINS + 1)));
-        };
-        auto test = [&](float z) __attribute__((always_inline)) {
-            const int b = bin(z);
-            return b == end || static_cast<uint32_t>(b - from) <= static_cast<uint32_t>(to - from);
-        };
-        auto sort = [&](float z, int i) __attribute__((always_inline)) {
-            const int b = bin(z);
-            if (b == end)
-                put(s.end, element_of(key_of(z), i));
-            if (b >= from && b <= to)
-                put(s.draw, element_of(key_of(z), i));
-        };
-        if (listed >= 0 || limit != 0)
-            for_kept(test, sort);
-        else
-            for_listed(test, sort);
-        __syncthreads();
-        uint64_t total = hi, upto;
-        if (end >= 0) {
-            if (s.end.count <= kSmall) {
-                rank_all(s.end);
-                find_few(s.end, in_end, upto);
-            } else {
-                divide<false>(end, in_end, upto);
+            ref = group_most(most);
+            if (fabsf(ref) < INFINITY) {
+                // Again where the row's largest lies far above the first ones.
+                for (int twice = 0; twice < 2 && !weighed; ++twice) {
+                    m = weigh_row();
+                    weighed = m < INFINITY && place(m) > -kBins;
+                    ref = weighed ? ref : m;
+                    if (m == INFINITY)
+                        break;
+                }
             }
-            total = min(before_end + upto, likely);
         }
-        const uint64_t target = drawn(u, total);
-        if (s.draw.count <= kSmall) {
-            rank_all(s.draw);
-            return index_of(find_few(s.draw, target - before_from, upto));
+        if (!weighed) {
+            float mine = -INFINITY;
+            clear<BINS>(s.other);
+            for_runs<32>([&](const float (&z)[V], int) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    mine = fmaxf(mine, z[e]);
+            });
+            m = ref = group_most(mine);
+            if (m == -INFINITY)
+                return -1;                              // nothing to draw
+            if (greedy) {
+                int first = K;
+                for_some([&](float z) __attribute__((always_inline)) { return z == m; },
+                         [&](float, int i) __attribute__((always_inline)) { first = min(first, i); });
+                if (tid == 0)
+                    s.count = K;
+                __syncthreads();
+                if (first < K)
+                    atomicMin(&s.count, first);
+                __syncthreads();
+                return s.count;
+            } else if (m == INFINITY) {
+                // They share the row: weights of one each.
+                uint64_t n = 0;
+                for_runs<V>([&](const float (&z)[V], int) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        n += z[e] == INFINITY;
+                });
+                n = min(group_sum(n), static_cast<uint64_t>(k));
+                auto rounded_up = [](uint64_t v) {
+                    return (v + (1ull << kWeightBits) - 1) >> kWeightBits;
+                };
+                if (p < 1.0f)
+                    n = rounded_up(share(p, n << kWeightBits));
+                key = key_of(m);
+                nth = rounded_up(drawn(u, n << kWeightBits));
+            } else {
+                // The k-th largest of the threads' own largest is no larger than
+                // the row's k-th: all from its bin up are gathered, a few more
+                // than k.  Without k, those with w >= min_p and a bin more for
+                // roundings.  Of a short row, all.
+                float end = kBins;
+                if (k < K && K > kSmall) {
+                    if (in_span(mine))
+                        add(&s.other[bin_of(mine) - BINS], 1);
+                    run_sums<BINS>(s.other, [](int, uint64_t v) __attribute__((always_inline)) { return v; });
+                    end = static_cast<float>(find<BINS>(s.other, k) + 1);
+                    __syncthreads();
+                } else if (!(p < 1.0f) && K > kSmall) {
+                    end = floorf(-logf(fminf(min_p, 1.0f)) * (BINS / kSpan)) + 2.0f;
+                }
+                if (end < kBins || K <= kSmall) {
+                    const int n = gather(end);
+                    if (n >= 0 && n <= kSmall)
+                        return from_few(n, k, p, min_p, u);
+                }
+                if (k < K) {
+                    // The row's own counts say where the k-th is.
+                    __syncthreads();
+                    clear<BINS>(s.other);
+                    __syncthreads();
+                    for_some([&](float z) __attribute__((always_inline)) { return in_span(z); },
+                             [&](float z, int) __attribute__((always_inline)) {
+                                 add(&s.other[bin_of(z) - BINS], 1);
+                             });
+                    const uint64_t total = run_sums<BINS>(
+                        s.other, [](int, uint64_t v) __attribute__((always_inline)) { return v; });
+                    if (total > static_cast<uint64_t>(k)) {
+                        const int b = find<BINS>(s.other, k);
+                        target = k - before(s.other, b);
+                        bin = b + BINS;
+                        border = kLimit;
+                        __syncthreads();
+                    }
+                }
+            }
         }
-        find(r, target, target);
-        const int b = s.found[0];
-        return index_of(divide<false>(b, target - s.found_before[0], upto));
+
+        const bool direct = m == INFINITY;
+        if (!direct && border != kLimit)
+            border = kDraw;
+        bool fresh = !direct;                           // the borders' bins are to be gathered
+        // The weight of all kept: `top` as far as it is known, between lo and hi.
+        uint64_t top = 0, lo = 0, hi = 0, before_end = 0, end_amount = 0, before_likely = 0;
+        int from = 0, likely_from = -1, likely_to = -1;
+        uint32_t width = 0;                             // bins of the draw, from `from` on
+        // Units kept of the nucleus's last bin (a target brought to units may
+        // otherwise reach the element behind it).
+        int end_bin = -1;
+        uint64_t end_units = 0;
+#pragma unroll 1
+        for (;;) {
+            if (fresh && border != kLimit) {
+                if (!weighed && limit == 0) {
+                    weigh_row();
+                } else if (!weighed) {
+                    __syncthreads();
+                    clear<2 * BINS>(s.wide);
+                    __syncthreads();
+                    for_kept([&](float z) __attribute__((always_inline)) { return in_span(z); },
+                             [&](float z, int) __attribute__((always_inline)) {
+                                 add(&s.wide[bin_of(z)], unit(z, bin_of(z)));
+                             });
+                }
+                if (tid < 64)
+                    s.lift = exp((static_cast<double>(ref) - static_cast<double>(m)) * rate *
+                                 (kSpan / BINS));
+                top = run_sums<2 * BINS>(
+                    s.wide, [&](int b, uint64_t v) __attribute__((always_inline)) {
+                        const double f = v != 0 ? factor(b) : 0.0;
+                        return f > 0x1p-46 ? whole(static_cast<double>(v) * f) : uint64_t(0);
+                    });
+                lo = hi = top;
+                if (p < 1.0f) {
+                    border = kEnd;
+                    const uint64_t want = share(p, top);
+                    bin = find<2 * BINS>(s.wide, want);
+                    before_end = before(s.wide, bin);
+                    end_amount = uniform(s.wide[bin]) - before_end;
+                    target = want - before_end;
+                    lo = before_end + 1;
+                    hi = before_end + end_amount;
+                }
+                if (min_p > 0.0f) {
+                    // The bins that its border may lie in (roundings in 32 bits).
+                    const float far = place(m) - logf(fminf(min_p, 1.0f)) * (BINS / kSpan);
+                    if (far < kBins - 1.0f) {
+                        likely_from = uniform(max(static_cast<int>(floorf(far - 0x1p-6f)) + BINS, 0));
+                        likely_to = uniform(max(static_cast<int>(floorf(far + 0x1p-6f)) + BINS, 0));
+                        before_likely = before(s.wide, likely_from);
+                        lo = min(lo, max(before_likely, uint64_t(1)));
+                        hi = min(hi, uniform(s.wide[likely_to]));
+                    }
+                }
+                from = find<2 * BINS>(s.wide, drawn(u, lo));
+                width = find<2 * BINS>(s.wide, drawn(u, hi)) - from + 1;
+            }
+            if (fresh) {
+                const int end = border == kDraw ? -1 : bin;
+                // The middle and half the width of the logits that the bins may
+                // hold, wider by all roundings; a width below zero where there is
+                // no bin.
+                auto middle = [&](int b, int bins) __attribute__((always_inline)) {
+                    return uniform(ref - (static_cast<float>(b - BINS) +
+                                          0.5f * static_cast<float>(bins - 1)) / scale);
+                };
+                auto half = [&](int bins) __attribute__((always_inline)) {
+                    return uniform((0.5f * static_cast<float>(bins) + 0.01f + kBins * 0x1p-20f) /
+                                       scale + fabsf(ref) * 0x1p-20f);
+                };
+                const float a = end < 0 ? 0.0f : middle(end, 1);
+                const float a_half = end < 0 ? -1.0f : half(1);
+                const float b = middle(from, width), b_half = width == 0 ? -1.0f : half(width);
+                const int likely = likely_to - likely_from + 1;
+                const float c = likely_from < 0 ? 0.0f : middle(likely_from, likely);
+                const float c_half = likely_from < 0 ? -1.0f : half(likely);
+                __syncthreads();
+                if (tid == 0)
+                    s.end.count = s.draw.count = s.likely.count = 0;
+                for_listed(
+                    [&](float z) __attribute__((always_inline)) {
+                        return fminf(fminf(fabsf(z - a) - a_half, fabsf(z - b) - b_half),
+                                     fabsf(z - c) - c_half);
+                    },
+                    [&](float z, int i) __attribute__((always_inline)) {
+                        const int b = bin_of(z);
+                        const uint64_t e = element_of(key_of(z), i);
+                        if (!in_span(z) || e < limit)
+                            return;
+                        if (b == end)
+                            put(s.end, e);
+                        if (static_cast<uint32_t>(b - from) < width)
+                            put(s.draw, e);
+                        if (b == likely_from || b == likely_to)
+                            put(s.likely, e);
+                    });
+                __syncthreads();
+                fresh = false;
+            }
+            if (border == kEnd)
+                target = uniform(
+                    static_cast<uint64_t>(ceil(__ull2double_rz(target) / factor(bin))));
+            if (border == kDraw) {
+                uint64_t a = 0, b = 0;                  // units of min_p's bins that reach it
+                if (likely_from >= 0) {
+                    uint64_t sum[2] = {0, 0};
+                    const double least =
+                        fmin(static_cast<double>(min_p), 1.0) * (1ull << kWeightBits);
+                    auto reach = [&](float z, int) __attribute__((always_inline)) {
+                        const int b = bin_of(z);
+                        const uint64_t own = unit(z, b);
+                        if (static_cast<double>(own) * factor(b) >= least * (1.0 - 0x1p-43))
+                            sum[b != likely_from] += own;
+                    };
+                    if (s.likely.count <= kSmall) {
+                        if (tid < s.likely.count)
+                            reach(value_of(static_cast<uint32_t>(s.likely.element[tid] >> 32)), 0);
+                    } else {
+                        for_kept([&](float z) __attribute__((always_inline)) {
+                                     return in_span(z) &&
+                                            (bin_of(z) == likely_from || bin_of(z) == likely_to);
+                                 }, reach);
+                    }
+                    a = group_sum(sum[0]);
+                    b = likely_to != likely_from ? group_sum(sum[1]) : 0;
+                    top = min(top, uniform(before_likely +
+                                           whole(static_cast<double>(a) * factor(likely_from)) +
+                                           whole(static_cast<double>(b) * factor(likely_to))));
+                }
+                const uint64_t want = drawn(u, max(lo, min(hi, top)));
+                bin = find<2 * BINS>(s.wide, want);
+                // More than what `want` exceeds by one (rounded down: a sum of many
+                // equal weights is one that doubles hold).
+                target = uniform(1 + static_cast<uint64_t>(
+                    __ull2double_rz(want - 1 - before(s.wide, bin)) / factor(bin)));
+                if (bin == end_bin)
+                    target = min(target, end_units);
+                if (bin == likely_from)
+                    target = min(target, a);
+                else if (bin == likely_to)
+                    target = min(target, b);
+            }
+            Few &few = border == kDraw ? s.draw : s.end;
+            uint64_t e, upto = 0;
+            if (border != kValue && few.count <= kSmall) {
+                rank_all(few, [&](float z) __attribute__((always_inline)) {
+                    return border == kLimit ? 1 : bin_of(z) == bin ? unit(z, bin) : 0;
+                });
+                e = find_few(few, target, upto);
+            } else {
+                if (border != kValue)
+                    key = divide(border == kLimit, bin, target, nth, upto);
+                e = element_of(key, nth_of(key, nth));
+            }
+            if (border == kLimit) {
+                limit = e;
+                fresh = true;
+            } else if (border == kEnd) {
+                end_bin = bin;
+                end_units = upto;
+                // At least what was wanted, at most the bin's amount.
+                const uint64_t least = lo > before_end ? lo - before_end : 1;
+                top = before_end +
+                      uniform(max(least, min(whole(static_cast<double>(upto) * factor(bin)),
+                                             end_amount)));
+            } else {
+                return index_of(e);
+            }
+            border = kDraw;
+        }
     }
 };
 
-template <typename T, int THREADS, int BINS, int LIST>
+template <typename T, int THREADS, int BINS>
 __global__ __launch_bounds__(THREADS, 4)
 void sample_kernel(const Sample a) {
-    typedef Draw<T, THREADS, BINS, LIST> D;
+    typedef Draw<T, THREADS, BINS> D;
     __shared__ typename D::Shared s;
     const int64_t row = a.first + blockIdx.x;
     D d{s, static_cast<const typename T::bits *>(a.logits) + row * a.ld, a.K,
         static_cast<int>(threadIdx.x)};
-    // One value for the workgroup: kept in scalar registers.
-    auto uniform = [](float v) __attribute__((always_inline)) {
-        return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
-    };
-    const int k = __builtin_amdgcn_readfirstlane(a.top_ks != nullptr ? a.top_ks[row] : a.top_k);
+    const int k = uniform(a.top_ks != nullptr ? a.top_ks[row] : a.top_k);
     const int label =
         d.run(uniform(a.temperatures != nullptr ? a.temperatures[row] : a.temperature), k,
               uniform(a.top_ps != nullptr ? a.top_ps[row] : a.top_p),
@@ -769,12 +968,12 @@ hipError_t run_sample(Sample a, int64_t N, int compute_units, hipStream_t stream
         a.first = first;
         const dim3 grid(static_cast<unsigned>(std::min(kMaxGrid, N - first)));
         if (a.K <= 4096)
-            hipLaunchKernelGGL((sample_kernel<T, 256, 512, 1024>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((sample_kernel<T, 256, 512>), grid, dim3(256), 0, stream, a);
         else if (N <= compute_units)
-            hipLaunchKernelGGL((sample_kernel<T, 1024, 2048, 4096>), grid, dim3(1024), 0, stream,
+            hipLaunchKernelGGL((sample_kernel<T, 1024, 2048>), grid, dim3(1024), 0, stream,
                                a);
         else
-            hipLaunchKernelGGL((sample_kernel<T, 512, 2048, 4096>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((sample_kernel<T, 512, 2048>), grid, dim3(512), 0, stream, a);
         e = hipGetLastError();
     }
     return e;
