@@ -27,12 +27,12 @@
 // relative to the bin.  So a row is read from memory once for it (the weights
 // under the loads), and once more, from the caches, to gather.
 //
-// 512 x 65536 fp32, top-p: 67 us (134 MB; 25 us to read them once).  Each workgroup
+// 512 x 65536 fp32, top-p: 58 us (134 MB; 25 us to read them once).  Each workgroup
 // first waits for memory, then for its weights (22 VALU instructions an element,
 // 14 of them fp64), then for the second reading (10 us), and all run in step.
 // Three readings (maximum, weights, borders) took 81 us, five 125.  16 x 32768 with
-// top-k 50: 10 us of which 1.5 read the row, the rest 20 barriers; nucleus and
-// min_p 23.
+// top-k 50: 10 us of which 1.5 read the row, the rest 20 barriers; top-p and
+// the draw 21.
 #include <math.h>
 #include <stdint.h>
 
@@ -50,7 +50,6 @@ constexpr int kWeightBits = 43;
 constexpr float kSpan = 32.0f;       // temperatures that BINS bins span; labels that
                                      // far below the largest are never drawn
 constexpr int kFirst = 4096;         // values whose largest the bins lie around
-constexpr int kSmall = 256;          // elements compared with one another
 
 struct Sample {
     const void *logits;
@@ -101,7 +100,9 @@ struct Draw {
     typedef typename T::bits B;
     static constexpr int kWaves = THREADS / 64;
     static constexpr int V = 16 / sizeof(B);         // values of a load
-    static constexpr int kList = 2 * BINS;
+    // Elements compared with one another (a bin of 1/64 temperature of 131072 normal
+    // logits, deviation 3, holds up to 272: 256 rows of those 114 us with 256).
+    static constexpr int kSmall = THREADS < 512 ? THREADS : 512;
     static constexpr float kBins = BINS;
 
     struct Few {
@@ -111,16 +112,20 @@ struct Draw {
     struct Shared {
         uint64_t wide[2 * BINS];     // units by bin, then the running weight with
                                      // each; or all that may belong to the first k
-        uint64_t other[BINS];        // counts, the finer divisions, listed runs
+        union {                      // (LDS past 64 KB costs registers)
+            uint64_t other[BINS];    // counts, the finer divisions, listed runs
+            struct {                 // of few elements
+                uint64_t amount[kSmall], before[kSmall];
+                int rank[kSmall];
+            };
+        };
         Few end, draw, likely;       // around the k-th or the nucleus's end, around
                                      // the draw, around min_p
-        uint64_t amount[kSmall], before[kSmall];     // of few elements
-        int rank[kSmall];
         double coarse[2 * BINS / 64], fine[64], lift;   // see factor()
         uint64_t sums[2][kWaves];
         float most[kWaves];
-        uint64_t found_before, found_element, found_upto, total;
-        int found, count, runs;
+        uint64_t found_element, found_upto, total;
+        int count, runs;
         uint32_t lo, hi;
     };
 
@@ -253,7 +258,7 @@ struct Draw {
         static_assert(kCoarse + 64 <= THREADS, "one entry to a thread");
         if (tid < kCoarse + 64) {
             const int i = tid < kCoarse ? 64 * tid - BINS : tid - kCoarse;
-            (tid < kCoarse ? s.coarse[tid] : s.fine[i]) = exp(-(kSpan / BINS) * i);
+            (tid < kCoarse ? s.coarse[tid] : s.fine[i]) = exp(-static_cast<double>(kSpan / BINS) * i);
         }
     }
     static __device__ __forceinline__ uint64_t whole(double v) {
@@ -368,11 +373,12 @@ struct Draw {
         if (x < kSmall)
             few.element[x] = e;
     }
-    // Calls f(z, i) for the elements of the row with miss(z) <= 0, a few hundred of
-    // them (numbers, since masks of lanes are slow to combine), in two steps: the runs that hold one are listed, one count for those
-    // of a wave; then each thread takes some of them.  So the loop over the row
-    // has little more than the tests (a wave's 256 or 512 elements hold a hit more
-    // often than not).  Where there are more runs than `runs` holds, one step.
+    // Calls f(z, i) for the elements of the row with miss(z) <= 0 (a number, since
+    // masks of lanes are slow to combine), a few hundred of them, in two steps: the
+    // runs that hold one are listed, one count for those of a wave; then each thread
+    // takes some of them.  So the loop over the row has little more than the tests
+    // (a wave's 256 or 512 elements hold a hit more often than not).  Where there are
+    // more runs than `runs` holds, one step.
     template <typename P, typename F>
     __device__ __forceinline__ void for_listed(const P &miss, const F &f) {
         auto *runs = reinterpret_cast<int *>(s.other);
@@ -432,21 +438,22 @@ struct Draw {
 
     // For each of few elements, how many come before it in the order, and their
     // amounts (amount(z)).  Thread (part, x) adds up its part's share for element
-    // x.
+    // x, in as many parts as there are threads for.
     template <typename F>
     __device__ __forceinline__ void rank_all(const Few &few, const F &amount) {
-        constexpr int kParts = THREADS / kSmall;
-        const int n = few.count;
+        const int n = uniform(few.count);
         if (tid < n) {
             s.amount[tid] = amount(value_of(static_cast<uint32_t>(few.element[tid] >> 32)));
             s.before[tid] = 0;
             s.rank[tid] = 0;
         }
         __syncthreads();
-        const int x = tid % kSmall, part = tid / kSmall;
+        const int shift = n <= 64 ? 6 : n <= 128 ? 7 : n <= 256 ? 8 : 9;
+        const int x = tid & ((1 << shift) - 1), part = tid >> shift;
         if (x < n) {
             const uint64_t mine = few.element[x];
-            const int beg = n * part / kParts, end = n * (part + 1) / kParts;
+            const int parts = THREADS >> shift;
+            const int beg = n * part / parts, end = n * (part + 1) / parts;
             uint64_t sum = 0;
             int rank = 0;
 #pragma unroll 4
@@ -960,6 +967,16 @@ void sample_kernel(const Sample a) {
         static_cast<int32_t *>(a.labels)[row] = label;
 }
 
+// The more labels, the more threads and bins (few bins are quick to add up, many
+// leave few labels in one); of a few rows of most labels, each has 1024 threads.
+// us, plain draw and top-p:
+//   threads, bins   256, 512    512, 1024   512, 2048   1024, 2048
+//   4096 x 8192     66, 75      111, 132    133, 152
+//   2048 x 16384    59, 60      69, 79      79, 89
+//   256 x 16384     22, 23      15, 16.5    16.5, 18
+//   256 x 32768     89, 39      23, 24      20, 22      26, 29
+//   512 x 65536                 100, 61     52, 53      72, 80
+//   16 x 131072                 132, 56     48, 49      43, 43
 template <typename T>
 hipError_t run_sample(Sample a, int64_t N, int compute_units, hipStream_t stream) {
     constexpr int64_t kMaxGrid = int64_t(1) << 21;      // a launch has less than 2^32 threads
@@ -967,13 +984,14 @@ hipError_t run_sample(Sample a, int64_t N, int compute_units, hipStream_t stream
     for (int64_t first = 0; first < N && e == hipSuccess; first += kMaxGrid) {
         a.first = first;
         const dim3 grid(static_cast<unsigned>(std::min(kMaxGrid, N - first)));
-        if (a.K <= 4096)
+        if (a.K <= 8192 || (a.K <= 16384 && N > 2 * compute_units))
             hipLaunchKernelGGL((sample_kernel<T, 256, 512>), grid, dim3(256), 0, stream, a);
-        else if (N <= compute_units)
-            hipLaunchKernelGGL((sample_kernel<T, 1024, 2048>), grid, dim3(1024), 0, stream,
-                               a);
-        else
+        else if (a.K <= 16384)
+            hipLaunchKernelGGL((sample_kernel<T, 512, 1024>), grid, dim3(512), 0, stream, a);
+        else if (a.K <= 65536 || N > compute_units)
             hipLaunchKernelGGL((sample_kernel<T, 512, 2048>), grid, dim3(512), 0, stream, a);
+        else
+            hipLaunchKernelGGL((sample_kernel<T, 1024, 2048>), grid, dim3(1024), 0, stream, a);
         e = hipGetLastError();
     }
     return e;

@@ -477,6 +477,17 @@ def test_sample_follows_its_distribution():
     assert (torch.bincount(got.cpu().long(), minlength=6).double() - want).abs().max() <= 1
 
 
+@pytest.mark.parametrize("N,K", [(6, 9000), (600, 8200), (6, 17000), (300, 17000), (6, 131072),
+                                 (260, 66000)])
+@pytest.mark.parametrize("spread", [0.02, 0.4, 3.0])
+def test_sample_bins_of_many(N, K, spread):
+    """Every kernel, with hundreds to thousands of labels in one bin."""
+    logits = rand((N, K), F32, N + K, spread)
+    u = uniforms(N, K)
+    for kw in ({}, dict(top_p=0.7), dict(top_k=K // 3), dict(min_p=0.5)):
+        check_sample(logits, u, **kw)
+
+
 def test_sample_past_32_bit_offsets():
     N, K = 40000, 120000
     z = torch.zeros((N, K), dtype=BF, device="cuda")
