@@ -25,7 +25,7 @@
 // The histogram needs no maximum first: its bins lie around the largest of the
 // row's first values, BINS on either side, and the weights within a bin are
 // relative to the bin.  So a row is read from memory once for it (the weights
-// under the loads), and once more, from the caches, to gather.
+// under the loads), and once more, from the memory-side cache, to gather.
 //
 // 512 x 65536 fp32, top-p: 58 us (134 MB; 25 us to read them once).  Each workgroup
 // first waits for memory, then for its weights (22 VALU instructions an element,
@@ -125,6 +125,7 @@ struct Draw {
         uint64_t sums[2][kWaves];
         float most[kWaves];
         uint64_t found_element, found_upto, total;
+        uint64_t kept;               // by the first k, of few elements
         int count, runs;
         uint32_t lo, hi;
     };
@@ -606,9 +607,9 @@ struct Draw {
         uint64_t total = uniform(s.total), likely = 0;
         if (k < n) {
             if (tid < n && s.rank[tid] == k - 1)
-                s.found_upto = s.before[tid] + s.amount[tid];
+                s.kept = s.before[tid] + s.amount[tid];
             __syncthreads();
-            total = uniform(s.found_upto);
+            total = uniform(s.kept);
         }
         if (min_p > 0.0f) {
             const double least = fmin(static_cast<double>(min_p), 1.0) * (1ull << kWeightBits);
