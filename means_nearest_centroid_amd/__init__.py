@@ -876,7 +876,7 @@ def kmeans_sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     largest weight, and the one at which their running weight exceeds ``uniform``
     of the whole.  Each setting is a number or a tensor of one for each row (fp32,
     ``top_k`` int32); a temperature of 0 takes the largest logit.  ``out``: int32
-    (made when not given) or int64.  A row without a finite logit gets -1."""
+    (made when not given) or int64.  A row of -infinities and NaN gets -1."""
     import torch
     lead = logits.shape[:-1]
     z = _flat(logits, "logits") if logits.dim() != 1 else logits.view(1, -1)
