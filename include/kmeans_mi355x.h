@@ -439,7 +439,8 @@ kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t cou
  * times the e4m3 number.  The last block of a row may be narrower.
  *
  *     scale = max|v| / 448 over the block (fp32; 1 where all are zero, and no
- *             less than 2^-126),   q = v / scale rounded once
+ *             less than 2^-126),   q = v / scale (rounded to fp32, then to e4m3,
+ *             each to nearest, ties to even)
  *
  * A block with a NaN or an infinity has that magnitude as its scale, and at
  * least one NaN.

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "kmeans_internal.h"
@@ -43,18 +44,39 @@ __device__ __forceinline__ float fp8_scale(uint32_t most) {
     return most == 0 ? 1.0f : s < 0x1p-126f ? 0x1p-126f : s;
 }
 
-// The first n of 8 values, times `inv`, in e4m3 (to nearest, ties to even; the
-// scale keeps them at 448 or below but for a rounding).
+// The first n of 8 values, divided by their scale and rounded to e4m3 (to nearest,
+// ties to even; the scale keeps them at 448 or below but for a rounding).  The
+// quotient is the correctly rounded one: quotients of 16-bit values often lie on a
+// tie of e4m3, which a product with 1 / scale would leave to either side (one bf16
+// value of 2000).  q0 = v inv is off by a unit or two, and its remainder, exact in
+// one fused operation, brings it to the nearest (262144 x 128 in rows 22.7 us, 21.4
+// with the product alone, 26.2 with a division for each; 16384 x 4096 in the norm
+// 88, 88 and 96).  Remainders below 2^-149 are
+// kept from vanishing by a power of two on both sides; zeros keep their sign, and an
+// infinite scale makes zeros of finite values, as in a division.
 struct __attribute__((packed, aligned(1))) Fp8Run {
     uint32_t lo, hi;
 };
-__device__ __forceinline__ void store_fp8_run(uint8_t *p, int n, const float (&v)[8], float inv) {
+__device__ __forceinline__ void store_fp8_run(uint8_t *p, int n, float (&v)[8], float scale) {
 #if defined(__HIP_DEVICE_COMPILE__)
+    if (scale < 0x1p-90f) {
+        scale *= 0x1p60f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] *= 0x1p60f;
+    }
+    const float inv = 1.0f / scale;
+    const float finite = scale == INFINITY ? 0.0f : scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float q0 = v[e] * inv;
+        v[e] = fmaf(-fmaf(q0, finite, -v[e]), inv, q0);
+    }
     Fp8Run q;
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-    q.lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
-    q.hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, w, true);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    q.lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+    q.hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], w, true);
     if (n >= 8) {
         typedef uint32_t u32x2_bytes __attribute__((ext_vector_type(2), aligned(1)));
         *reinterpret_cast<u32x2_bytes *>(p) = __builtin_bit_cast(u32x2_bytes, q);

@@ -1,0 +1,113 @@
+"""Operators of label prediction (HIP, through the public binding): results that
+their definitions settle to the last bit, or to a bound taken block by block."""
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+km = pytest.importorskip("means_nearest_centroid_amd")
+
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+FP8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test run without a visible GPU")
+    km.load_library()
+    return torch.device("cuda:0")
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).cuda()
+
+
+# ---- quantisation: the correctly rounded quotient, rounded to e4m3 -----------
+
+def quantized(x, rows):
+    """(bits of e4m3(v / s), s) of the definition, on the CPU."""
+    x = x.detach().cpu().float()
+    N, D = x.shape
+    n, b = -(-N // rows), -(-D // 128)
+    wide = torch.nn.functional.pad(x, (0, b * 128 - D, 0, n * rows - N)).view(n, rows, b, 128)
+    most = wide.abs().amax((1, 3))
+    s = torch.where(most == 0, 1.0, (most / 448).clamp(min=2.0 ** -126))
+    q = (wide / s[:, None, :, None]).view(n * rows, b * 128)[:N, :D]
+    return q.to(FP8).view(torch.uint8), s
+
+
+def check_quotients(X, rows):
+    q, s = quantized(X, rows)
+    Q, S = km.kmeans_quantize(X, rows=rows)
+    assert torch.equal(S.cpu().nan_to_num(nan=-1.0), s.nan_to_num(nan=-1.0))
+    got = Q.view(torch.uint8).cpu()
+    bad = (got != q) & ~((got & 0x7f == 0x7f) & (q & 0x7f == 0x7f))      # NaN of either sign
+    assert not bad.any(), (f"{int(bad.sum())} of {q.numel()} values, first at "
+                           f"{torch.nonzero(bad)[0].tolist()}: {got[bad][0]:#x}, {q[bad][0]:#x}")
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_quotients_are_correctly_rounded(dtype, rows):
+    """Of 16-bit values one quotient of a few hundred lies on a tie of e4m3."""
+    for seed, scale in enumerate((1.0, 3e-5, 900.0)):
+        check_quotients(rand((2000, 640), dtype, seed, scale), rows)
+    check_quotients(rand((300, 77), dtype, 5), rows)
+
+
+def ties():
+    """All e4m3 values, and those halfway between two of them."""
+    v = torch.arange(0x7f, dtype=torch.uint8).view(FP8).float()
+    return torch.cat([v, (v[1:] + v[:-1]) / 2])
+
+
+@pytest.mark.parametrize("power", [-126, -125, -110, -92, -91, -90, -89, -60, 0, 3, 100, 118])
+def test_quotients_at_ties(power):
+    """Scales of 16 bits, so that the products of ties with them are exact in
+    fp32, and their neighbours on either side; the largest value sets the scale.
+    (The neighbour of zero on its own side is a NaN here: so is its whole block.)"""
+    g = torch.Generator().manual_seed(power + 200)
+    N = 200
+    s = (1 + torch.randint(0, 1 << 15, (N, 1), generator=g) * 2.0 ** -15).double() * 2.0 ** power
+    t = ties().double()
+    x = (s * t * torch.where(torch.rand(N, len(t), generator=g) < 0.5, -1.0, 1.0)).float()
+    assert power < -100 or torch.equal(x.double().abs(), s * t)
+    x = torch.cat([x, torch.nextafter(x, torch.tensor(0.0)),
+                   torch.nextafter(x, torch.sign(x) * torch.inf)], 1)
+    x = torch.where(x.abs() > (448 * s).float(), (448 * s).float() * x.sign(), x)
+    # blocks of 128 with the scale's own largest value in each
+    x = torch.nn.functional.pad(x, (0, -x.shape[1] % 127)).view(N, -1, 127)
+    x = torch.cat([x, (448 * s).float()[:, :, None].expand(-1, x.shape[1], 1)], 2)
+    check_quotients(x.reshape(N, -1).cuda(), 1)
+
+
+def test_quotients_of_zeros_and_infinities():
+    x = torch.zeros(4, 130)
+    x[0, ::2] = -0.0
+    x[1, 3], x[1, 4], x[1, 5] = -7.0, 0.0, -0.0
+    x[2, 9], x[2, 10:20] = torch.inf, -3.0
+    Q, s = km.kmeans_quantize(x.cuda())
+    bits = Q.view(torch.uint8).cpu()
+    assert (bits[0, ::2] == 0x80).all() and (bits[0, 1::2] == 0).all()
+    assert bits[1, 3:6].tolist() == [0xfe, 0, 0x80]
+    assert s[2, 0].isinf() and bits[2, 9] & 0x7f == 0x7f
+    assert (bits[2, 10:20] == 0x80).all() and (bits[2, 20:128] == 0).all()
+
+
+@pytest.mark.parametrize("D", [128, 300, 4096])
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_norm_quotients(D, dtype):
+    """Rows of two magnitudes only, whose mean square is a power of 4: r and y are
+    exact, and the 8-bit output is the definition's to the last bit."""
+    N = 40
+    g = torch.Generator().manual_seed(D)
+    x = torch.where(torch.rand(N, D, generator=g) < 0.5, -2.0, 2.0)
+    for _ in range(10):
+        w = torch.randn(D, generator=g).to(dtype)
+        Q, s = km.kmeans_rms_norm(x.to(dtype).cuda(), w.cuda(), eps=0.0, quantize=True)
+        q, want = quantized(x / 2 * w.float(), 1)
+        assert torch.equal(s.cpu(), want) and torch.equal(Q.view(torch.uint8).cpu(), q)
