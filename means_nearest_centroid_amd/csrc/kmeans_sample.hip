@@ -742,7 +742,7 @@ struct Draw {
                     run_sums<BINS>(s.other, [](int, uint64_t v) __attribute__((always_inline)) { return v; });
                     end = static_cast<float>(find<BINS>(s.other, k) + 1);
                     __syncthreads();
-                } else if (!(p < 1.0f) && K > kSmall) {
+                } else if (!(p < 1.0f) && K > kSmall && min_p > 0.0f) {
                     end = floorf(-logf(fminf(min_p, 1.0f)) * (BINS / kSpan)) + 2.0f;
                 }
                 if (end < kBins || K <= kSmall) {

@@ -8,6 +8,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 km = pytest.importorskip("means_nearest_centroid_amd")
+import prediction_reference as ref  # noqa: E402
 
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
 FP8 = torch.float8_e4m3fn
@@ -111,3 +112,41 @@ def test_norm_quotients(D, dtype):
         Q, s = km.kmeans_rms_norm(x.to(dtype).cuda(), w.cuda(), eps=0.0, quantize=True)
         q, want = quantized(x / 2 * w.float(), 1)
         assert torch.equal(s.cpu(), want) and torch.equal(Q.view(torch.uint8).cpu(), q)
+
+
+# ---- sampling ----------------------------------------------------------------
+
+def rows_of(N, **kw):
+    full = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
+    full.update({k: v.cpu().numpy() if isinstance(v, torch.Tensor) else v for k, v in kw.items()})
+    return {k: np.broadcast_to(np.asarray(v), (N,)) for k, v in full.items()}
+
+
+def check_draws(z, u, **kw):
+    got = km.kmeans_sample(z, u, **kw)
+    ref.check_sample(got, ref.sample(z, u.cpu().numpy(), **rows_of(len(z), **kw)))
+    return got
+
+
+def uniforms(N, seed):
+    return torch.rand(N, generator=torch.Generator().manual_seed(seed)).cuda()
+
+
+@pytest.mark.parametrize("K", [300, 9000, 40000, 70000])
+@pytest.mark.parametrize("masked", [0, 200, 4096, 5000])
+def test_settings_that_limit_nothing(K, masked):
+    """NaN, and values beyond the range where nothing is cut, as array values,
+    also where the row's first labels are all masked."""
+    N = 16
+    z = rand((N, K), F32, K, 0.5)
+    z[:, :min(masked, K - 50)] = -torch.inf
+    z[3, :min(masked, K - 50)] = torch.nan
+    u = uniforms(N, 7)
+    want = check_draws(z, u)
+    for least in (torch.nan, -1.0, -0.0, 0.0):
+        for p in (torch.nan, 1.0, 7.0):
+            for k in (0, -3, K, K + 5):
+                got = km.kmeans_sample(z, u, min_p=torch.full((N,), least).cuda(),
+                                       top_p=torch.full((N,), p).cuda(),
+                                       top_k=torch.full((N,), k, dtype=torch.int32).cuda())
+                assert torch.equal(got, want), (least, p, k)
