@@ -33,6 +33,7 @@
 // Three readings (maximum, weights, borders) took 81 us, five 125.  16 x 32768 with
 // top-k 50: 10 us of which 1.5 read the row, the rest 20 barriers; top-p and
 // the draw 21.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -835,10 +836,12 @@ struct Draw {
                 const int end = border == kDraw ? -1 : bin;
                 // The middle and half the width of the logits that the bins may
                 // hold, wider by all roundings; a width below zero where there is
-                // no bin.
+                // no bin.  A middle past the type's range is at its end: no
+                // logit is further out.
                 auto middle = [&](int b, int bins) __attribute__((always_inline)) {
-                    return uniform(ref - (static_cast<float>(b - BINS) +
-                                          0.5f * static_cast<float>(bins - 1)) / scale);
+                    const float at = ref - (static_cast<float>(b - BINS) +
+                                            0.5f * static_cast<float>(bins - 1)) / scale;
+                    return uniform(fminf(fmaxf(at, -FLT_MAX), FLT_MAX));
                 };
                 auto half = [&](int bins) __attribute__((always_inline)) {
                     return uniform((0.5f * static_cast<float>(bins) + 0.01f + kBins * 0x1p-20f) /

@@ -150,3 +150,24 @@ def test_settings_that_limit_nothing(K, masked):
                                        top_p=torch.full((N,), p).cuda(),
                                        top_k=torch.full((N,), k, dtype=torch.int32).cuda())
                 assert torch.equal(got, want), (least, p, k)
+
+
+@pytest.mark.parametrize("K", [6000, 20000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_at_the_ends_of_the_range(K, dtype, sign):
+    """Finite logits up to the type's last, at a temperature that tells them
+    apart: their distances and bins reach past the range."""
+    N = 24
+    g = torch.Generator().manual_seed(K)
+    last = torch.finfo(dtype).max
+    z = sign * last * (1 - 0.12 * torch.rand(N, K, generator=g))
+    z[:, 4500] = last if sign > 0 else 0.85 * -last        # the largest, behind the first ones
+    z[:, :4096] = torch.where(z[:, :4096] > 0.95 * last, 0.9 * last, z[:, :4096])
+    z[4, 1::2] = -torch.inf
+    z = z.to(dtype).cuda()
+    u = uniforms(N, 3)
+    u[0], u[1], u[2] = 0.0, 1e-3, 1e-4
+    for kw in (dict(), dict(top_p=0.02), dict(top_p=0.9), dict(top_k=900), dict(top_p=0.9, min_p=0.1),
+               dict(min_p=1e-6)):
+        check_draws(z, u, temperature=2.0 ** 120, **kw)
