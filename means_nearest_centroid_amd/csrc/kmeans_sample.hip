@@ -8,8 +8,9 @@
 //            weight of all kept
 //
 // Weights are summed in 64-bit integers, so that every sum is exact and the same
-// in any order, from atomics too: the label depends on the row alone, not on the
-// launch.  A weight is a multiple of 2^-43 of its bin's centre (below); a bin's sum
+// in any order, from atomics too: the label depends on the row and its settings
+// alone, not on the launch (which way below a row takes goes by its length, its
+// settings and its values).  A weight is a multiple of 2^-43 of its bin's centre (below); a bin's sum
 // is brought to the scale of the largest weight with one rounding, to 2^-43 of
 // that.  32-bit sums would shift the borders by 1e-7 of the whole and draw other
 // labels in one row of some thousands.
@@ -96,14 +97,15 @@ __device__ __forceinline__ double uniform(double v) {
     return __longlong_as_double(uniform(static_cast<uint64_t>(__double_as_longlong(v))));
 }
 
-template <typename T, int THREADS, int BINS>
+template <typename T, int THREADS, int BINS, int SMALL>
 struct Draw {
     typedef typename T::bits B;
     static constexpr int kWaves = THREADS / 64;
     static constexpr int V = 16 / sizeof(B);         // values of a load
-    // Elements compared with one another (a bin of 1/64 temperature of 131072 normal
+    // Most elements compared with one another (a bin of 1/64 temperature of 131072 normal
     // logits, deviation 3, holds up to 272: 256 rows of those 114 us with 256).
-    static constexpr int kSmall = THREADS < 512 ? THREADS : 512;
+    static constexpr int kSmall = SMALL;
+    static_assert(THREADS % SMALL == 0, "a thread for each, and whole parts of a row");
     static constexpr float kBins = BINS;
 
     struct Few {
@@ -732,13 +734,20 @@ struct Draw {
                 key = key_of(m);
                 nth = rounded_up(drawn(u, n << kWeightBits));
             } else {
-                // The k-th largest of the threads' own largest is no larger than
-                // the row's k-th: all from its bin up are gathered, a few more
-                // than k.  Without k, those with w >= min_p and a bin more for
-                // roundings.  Of a short row, all.
+                // The k-th largest of the largest of kSmall parts of the row is
+                // no larger than the row's k-th: all from its bin up are gathered,
+                // a few more than k.  Without k, those with w >= min_p and a bin
+                // more for roundings.  Of a short row, all.
                 float end = kBins;
                 if (k < K && K > kSmall) {
-                    if (in_span(mine))
+                    if constexpr (THREADS > kSmall) {
+                        auto *most = reinterpret_cast<float *>(s.wide);
+                        most[tid] = mine;
+                        __syncthreads();
+                        for (int x = tid + kSmall; x < THREADS; x += kSmall)
+                            mine = fmaxf(mine, most[x]);
+                    }
+                    if (tid < kSmall && in_span(mine))
                         add(&s.other[bin_of(mine) - BINS], 1);
                     run_sums<BINS>(s.other, [](int, uint64_t v) __attribute__((always_inline)) { return v; });
                     end = static_cast<float>(find<BINS>(s.other, k) + 1);
@@ -950,10 +959,10 @@ struct Draw {
     }
 };
 
-template <typename T, int THREADS, int BINS>
+template <typename T, int THREADS, int BINS, int SMALL>
 __global__ __launch_bounds__(THREADS, 4)
 void sample_kernel(const Sample a) {
-    typedef Draw<T, THREADS, BINS> D;
+    typedef Draw<T, THREADS, BINS, SMALL> D;
     __shared__ typename D::Shared s;
     const int64_t row = a.first + blockIdx.x;
     D d{s, static_cast<const typename T::bits *>(a.logits) + row * a.ld, a.K,
@@ -971,16 +980,23 @@ void sample_kernel(const Sample a) {
         static_cast<int32_t *>(a.labels)[row] = label;
 }
 
-// The more labels, the more threads and bins (few bins are quick to add up, many
-// leave few labels in one); of a few rows of most labels, each has 1024 threads.
-// us, plain draw and top-p:
-//   threads, bins   256, 512    512, 1024   512, 2048   1024, 2048
-//   4096 x 8192     66, 75      111, 132    133, 152
-//   2048 x 16384    59, 60      69, 79      79, 89
-//   256 x 16384     22, 23      15, 16.5    16.5, 18
-//   256 x 32768     89, 39      23, 24      20, 22      26, 29
-//   512 x 65536                 100, 61     52, 53      72, 80
-//   16 x 131072                 132, 56     48, 49      43, 43
+// The bins, and how many labels are compared with one another, go by the number of
+// labels alone: roundings differ with them, and a row's label does not depend on the
+// batch.  Few bins are quick to add up, many leave few labels in one.  The threads
+// change no result: many rows fill the CUs with small workgroups, of few rows each
+// has a large one.  us, plain draw and top-p:
+//   bins 1024, threads      256         512
+//   2048 x 16384            62, 67      73, 83
+//   600 x 16384             28, 31      30, 34
+//   512 x 16384             24, 27      21, 24
+//   16 x 16384              18, 20      15, 17
+//   bins 2048, threads      512         1024
+//   512 x 65536             55, 58      74, 82
+//   256 x 32768             22, 24      25, 28
+//   300 x 131072            95, 99      107, 116
+//   256 x 131072            78, 84      71, 75
+//   16 x 131072             56, 66      47, 54
+// (1024 threads spill 11 to 15 registers.)
 template <typename T>
 hipError_t run_sample(Sample a, int64_t N, int compute_units, hipStream_t stream) {
     constexpr int64_t kMaxGrid = int64_t(1) << 21;      // a launch has less than 2^32 threads
@@ -988,14 +1004,16 @@ hipError_t run_sample(Sample a, int64_t N, int compute_units, hipStream_t stream
     for (int64_t first = 0; first < N && e == hipSuccess; first += kMaxGrid) {
         a.first = first;
         const dim3 grid(static_cast<unsigned>(std::min(kMaxGrid, N - first)));
-        if (a.K <= 8192 || (a.K <= 16384 && N > 2 * compute_units))
-            hipLaunchKernelGGL((sample_kernel<T, 256, 512>), grid, dim3(256), 0, stream, a);
+        if (a.K <= 8192)
+            hipLaunchKernelGGL((sample_kernel<T, 256, 512, 256>), grid, dim3(256), 0, stream, a);
+        else if (a.K <= 16384 && N > 2 * compute_units)
+            hipLaunchKernelGGL((sample_kernel<T, 256, 1024, 256>), grid, dim3(256), 0, stream, a);
         else if (a.K <= 16384)
-            hipLaunchKernelGGL((sample_kernel<T, 512, 1024>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((sample_kernel<T, 512, 1024, 256>), grid, dim3(512), 0, stream, a);
         else if (a.K <= 65536 || N > compute_units)
-            hipLaunchKernelGGL((sample_kernel<T, 512, 2048>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((sample_kernel<T, 512, 2048, 512>), grid, dim3(512), 0, stream, a);
         else
-            hipLaunchKernelGGL((sample_kernel<T, 1024, 2048>), grid, dim3(1024), 0, stream, a);
+            hipLaunchKernelGGL((sample_kernel<T, 1024, 2048, 512>), grid, dim3(1024), 0, stream, a);
         e = hipGetLastError();
     }
     return e;

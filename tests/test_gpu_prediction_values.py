@@ -171,3 +171,42 @@ def test_logits_at_the_ends_of_the_range(K, dtype, sign):
     for kw in (dict(), dict(top_p=0.02), dict(top_p=0.9), dict(top_k=900), dict(top_p=0.9, min_p=0.1),
                dict(min_p=1e-6)):
         check_draws(z, u, temperature=2.0 ** 120, **kw)
+
+
+def near_ties(rows, of, rest, seed):
+    """Rows of `of` labels of two values, `rest` far below, and a temperature for
+    each, so that half of the weight ends as closely at a whole number of labels
+    as the roundings to 2^-43 of a weight see: (logits, temperatures)."""
+    rng = np.random.default_rng(seed)
+    wide, eight = np.longdouble, 8
+    z, temps = np.full((rows, of + rest), -200.0, np.float32), np.empty(rows, np.float32)
+    for r in range(0, rows, eight):
+        first = int(rng.integers(of // 3, of // 2))
+        t = rng.uniform(0.6, 1.9, 200000).astype(np.float32)
+        n = rng.integers(first // 2 + of // 50 + 1, first, len(t))
+        w = (2 * n - first).astype(wide) / wide(of - first)
+        d = (-np.log(w) * t.astype(wide)).astype(np.float32)
+        half = (first + (of - first) * np.exp(-d.astype(wide) / t.astype(wide))) / 2
+        for i, best in enumerate(np.argsort(np.abs(half / n - 1))[:eight]):
+            at = rng.permutation(of + rest)
+            z[r + i, at[:first]], z[r + i, at[first:of]] = 0.0, -d[best]
+            temps[r + i] = t[best]
+    return torch.from_numpy(z).cuda(), torch.from_numpy(temps).cuda()
+
+
+@pytest.mark.parametrize("of,rest,top_k", [(12000, 0, 0), (400, 11600, 400), (400, 69600, 400),
+                                           (300, 7000, 300), (70000, 0, 0)])
+def test_labels_do_not_depend_on_the_batch(of, rest, top_k):
+    """Border cases one by one, and all in one call of more rows than the GPU has
+    room for at once: the same labels."""
+    N = 640
+    z, t = near_ties(128, of, rest, of + rest)
+    z, t = z.repeat(N // 128, 1), t.repeat(N // 128)
+    u = torch.full((N,), 0.5).cuda()
+    for kw in (dict(top_k=top_k), dict(top_k=top_k, top_p=0.5)):
+        got = km.kmeans_sample(z, u, temperature=t, **kw)
+        assert torch.equal(got, got[:128].repeat(N // 128))
+        for n in (1, 40):
+            for i in range(0, 128, n):
+                few = km.kmeans_sample(z[i:i + n], u[:n], temperature=t[i:i + n], **kw)
+                assert torch.equal(few, got[i:i + len(few)]), (kw, n, i)
