@@ -478,7 +478,8 @@ kmeans_status_t kmeans_rms_norm(const void *X, int64_t x_stride, const void *res
  * it wrote, or X where there was no residual).  With g = dY w:
  *
  *     dX = r g - H r^3 mean_j(g H) + dH         (fp32, rounded once)
- *     dweight = sum_i dY_i H_i r_i              (fp32, rounded once)
+ *     dweight = sum_i dY_i H_i r_i              (fp32 over a few rows, fp64 over
+ *                                                those sums, rounded once)
  *
  *   dY, H     [N][D] of `dtype`.   weight  [D] of `dtype`, or NULL (w = 1).
  *   dH        [N][D] of `dtype`, or NULL: the gradient that reaches the sum
@@ -486,7 +487,7 @@ kmeans_status_t kmeans_rms_norm(const void *X, int64_t x_stride, const void *res
  *   dX        [N][D] of `dtype`, written: the gradient of X and of the residual.
  *   dweight   [D] of `dtype`, written, or NULL (N == 0: zeros).
  *
- * dweight's partial sums are the stream's workspace: at most D floats for each of
+ * dweight's partial sums are the stream's workspace: at most D doubles for each of
  * four workgroups per compute unit (D > 16384: and one float per row).
  */
 kmeans_status_t kmeans_rms_norm_grad(const void *dY, int64_t dy_stride, const void *H,

@@ -247,23 +247,76 @@ struct NormGrad {
     const void *weight;      // or null
     const void *dh;          // or null
     void *dx;
-    float *dw_partial;       // [rows of workgroups][D], or null
+    void *dw_partial;        // [rows of workgroups][D], or null: fp64 where DEEP, else fp32
     float *r;                // [N]: 1 / rms of each row, for wide rows' dw
     int64_t ldy, ldh, lddh, ldx;
     int N, D;
     float eps;
 };
 
+// Terms of dw that a lane adds one after another in fp32, and at most 15 sums of
+// other lanes with them: past that (but for eight partial sums in pairs) the sums go
+// on in fp64, so that no error grows with the rows (in fp32 alone a lane adds 8192
+// terms of 2^27 rows, up to 2^-11 off).
+constexpr int kDepth = 44;
+
+// dw of a workgroup's rows so far, summed over its groups, to its row of partial
+// sums; DEEP: added to what lies there where `more`, and dw begins anew.
+template <int G, int R, bool DEEP>
+__device__ __forceinline__ void leave_sums(const NormGrad &a, float (&dw)[R][kRun], float *across,
+                                           bool more) {
+    constexpr int kThreads = threads_for(G);
+    constexpr int kRows = kThreads / G;
+    const int lane = threadIdx.x % G, group = threadIdx.x / G;
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * a.D;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * G + lane) * kRun;
+        if constexpr (kRows > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                across[e * kThreads + threadIdx.x] = dw[i][e];
+            __syncthreads();
+            if (group == 0)
+#pragma unroll
+                for (int e = 0; e < kRun; ++e)
+                    for (int q = 1; q < kRows; ++q)
+                        dw[i][e] += across[e * kThreads + q * G + lane];
+        }
+        if (group == 0 && c < a.D) {
+            if constexpr (DEEP) {
+                double *sum = static_cast<double *>(a.dw_partial) + out + c;
+#pragma unroll
+                for (int e = 0; e < kRun; ++e)
+                    if (c + e < a.D)
+                        sum[e] = more ? sum[e] + dw[i][e] : dw[i][e];
+            } else {
+                Packed<float, kRun> p;
+#pragma unroll
+                for (int e = 0; e < kRun; ++e)
+                    p.v[e] = dw[i][e];
+                store_run<float, kRun>(static_cast<float *>(a.dw_partial) + out + c, a.D - c, p);
+            }
+        }
+        if constexpr (DEEP)
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                dw[i][e] = 0.0f;
+    }
+}
+
 // Rows of a workgroup, one after another (kRows at a time): dx from the row's
-// two sums, dw summed in registers over the workgroup's rows in their order,
-// then over its groups in LDS.  The next row is on its way while this one is
+// two sums, dw summed in registers over kDepth of a lane's rows in their order,
+// then over the workgroup's groups in LDS (fp64 there would cost 4 us of 262144 x
+// 128), and those of more rows in fp64 in its row of partial sums.  The next row is on its way while this one is
 // worked, where registers hold both (R = 1); rows stay in their own type for
 // that.  As many workgroups as the CUs hold (16 waves each): 16384 x 4096 bf16
 // with dh 105 us (537 MB, 5.1 TB/s), 119 with twice and 149 with half as many,
 // and 171 with 256 lanes to a row.  WHOLE: D is a multiple of 8, and no run is
 // cut short (50021 x 321 fp32 42 us, 193 MB; 45 with its last runs loaded whole
-// and shifted).
-template <typename T, int G, int R, bool WHOLE>
+// and shifted).  DEEP: a lane has more than kDepth rows.
+template <typename T, int G, int R, bool WHOLE, bool DEEP>
 __global__ __launch_bounds__(threads_for(G))
 void norm_grad_kernel(const NormGrad a) {
     typedef typename T::bits B;
@@ -305,6 +358,8 @@ void norm_grad_kernel(const NormGrad a) {
     const float inv_d = 1.0f / static_cast<float>(a.D);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
     int turn = 0;
+    [[maybe_unused]] int held = 0;
+    bool more = false;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
     load(row);
     for (; row - group < a.N; row += stride) {
@@ -349,33 +404,15 @@ void norm_grad_kernel(const NormGrad a) {
         }
         if (R > 1)
             load(row + stride);
+        if constexpr (DEEP)
+            if (++held == kDepth) {
+                leave_sums<G, R, DEEP>(a, dw, across, more);
+                held = 0;
+                more = true;
+            }
     }
-    if (a.dw_partial == nullptr)
-        return;
-    float *out = a.dw_partial + static_cast<int64_t>(blockIdx.x) * a.D;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int c = (i * G + lane) * kRun;
-        if constexpr (kRows > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < kRun; ++e)
-                across[e * kThreads + threadIdx.x] = dw[i][e];
-            __syncthreads();
-            if (group == 0)
-#pragma unroll
-                for (int e = 0; e < kRun; ++e)
-                    for (int q = 1; q < kRows; ++q)
-                        dw[i][e] += across[e * kThreads + q * G + lane];
-        }
-        if (group == 0 && c < a.D) {
-            Packed<float, kRun> p;
-#pragma unroll
-            for (int e = 0; e < kRun; ++e)
-                p.v[e] = dw[i][e];
-            store_run<float, kRun>(out + c, a.D - c, p);
-        }
-    }
+    if (a.dw_partial != nullptr)
+        leave_sums<G, R, DEEP>(a, dw, across, more);
 }
 
 // Wide rows: dx by two readings of the row (the second from the caches).
@@ -431,7 +468,7 @@ void norm_grad_long_kernel(const NormGrad a, int64_t first) {
 }
 
 // Wide rows: dw's partial sums over a workgroup's rows, a run of columns to each
-// lane.
+// lane, every kDepth rows in fp64.
 template <typename T>
 __global__ __launch_bounds__(kNormThreads)
 void norm_columns_kernel(const NormGrad a, int rows_per_wg) {
@@ -441,45 +478,61 @@ void norm_columns_kernel(const NormGrad a, int rows_per_wg) {
         return;
     const int64_t end = min(static_cast<int64_t>(a.N),
                             (static_cast<int64_t>(blockIdx.x) + 1) * rows_per_wg);
-    float dw[kRun] = {};
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_wg; row < end; ++row) {
-        float h[kRun], y[kRun];
-        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.h) + row * a.ldh + c, a.D - c), h);
-        widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.dy) + row * a.ldy + c, a.D - c), y);
-        const float r = a.r[row];
+    double sum[kRun] = {};
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_wg; row < end;) {
+        float dw[kRun] = {};
+        for (const int64_t stop = min(end, row + kDepth); row < stop; ++row) {
+            float h[kRun], y[kRun];
+            widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.h) + row * a.ldh + c, a.D - c),
+                         h);
+            widen_run<T>(load_run<B, kRun>(static_cast<const B *>(a.dy) + row * a.ldy + c, a.D - c),
+                         y);
+            const float r = a.r[row];
+#pragma unroll
+            for (int e = 0; e < kRun; ++e)
+                dw[e] = fmaf(y[e] * h[e], r, dw[e]);
+        }
 #pragma unroll
         for (int e = 0; e < kRun; ++e)
-            dw[e] = fmaf(y[e] * h[e], r, dw[e]);
+            sum[e] += dw[e];
     }
     Packed<float, kRun> p;
 #pragma unroll
     for (int e = 0; e < kRun; ++e)
-        p.v[e] = dw[e];
-    store_run<float, kRun>(a.dw_partial + static_cast<int64_t>(blockIdx.x) * a.D + c, a.D - c, p);
+        p.v[e] = static_cast<float>(sum[e]);
+    store_run<float, kRun>(static_cast<float *>(a.dw_partial) +
+                               static_cast<int64_t>(blockIdx.x) * a.D + c, a.D - c, p);
 }
 
-// dw[c] = sum of the partials of column c: kJoinCols columns to a workgroup,
-// kJoinShares threads to a column, kJoinBatch loads of each in flight, joined in
-// LDS in their order (1024 rows of 321: 3 us, 11 with one load in flight).
+// dw[c] = sum of the partials (of type P) of column c: kJoinCols columns to a
+// workgroup, kJoinShares threads to a column, kJoinBatch loads of each in flight (1024
+// rows of 321: 3 us, 11 with one load), added in pairs and then in fp64 (all of it
+// in fp64 1.4 us more), joined in LDS in their order.
 constexpr int kJoinCols = 32;
 constexpr int kJoinShares = 32;
 constexpr int kJoinBatch = 8;
-template <typename T>
+template <typename T, typename P>
 __global__ __launch_bounds__(kJoinCols * kJoinShares)
-void norm_join_kernel(const float *partial, int rows, int D, void *dw) {
-    __shared__ float sums[kJoinShares][kJoinCols + 1];
+void norm_join_kernel(const P *partial, int rows, int D, void *dw) {
+    __shared__ double sums[kJoinShares][kJoinCols + 1];
     const int c = threadIdx.x % kJoinCols, share = threadIdx.x / kJoinCols;
     const int col = blockIdx.x * kJoinCols + c;
-    float v = 0.0f;
+    double v = 0.0;
     if (col < D)
         for (int r0 = share; r0 < rows; r0 += kJoinBatch * kJoinShares) {
-            float x[kJoinBatch];
+            P x[kJoinBatch];
 #pragma unroll
             for (int u = 0; u < kJoinBatch; ++u)
                 x[u] = partial[static_cast<int64_t>(min(r0 + u * kJoinShares, rows - 1)) * D + col];
 #pragma unroll
             for (int u = 0; u < kJoinBatch; ++u)
-                v += r0 + u * kJoinShares < rows ? x[u] : 0.0f;
+                x[u] = r0 + u * kJoinShares < rows ? x[u] : P(0);
+#pragma unroll
+            for (int half = kJoinBatch / 2; half >= 1; half /= 2)
+#pragma unroll
+                for (int u = 0; u < half; ++u)
+                    x[u] += x[u + half];
+            v += x[0];
         }
     sums[share][c] = v;
     __syncthreads();
@@ -487,7 +540,7 @@ void norm_join_kernel(const float *partial, int rows, int D, void *dw) {
         return;
     for (int q = 1; q < kJoinShares; ++q)
         v += sums[q][c];
-    static_cast<typename T::bits *>(dw)[col] = T::narrow(v);
+    static_cast<typename T::bits *>(dw)[col] = T::narrow(static_cast<float>(v));
 }
 
 template <typename T>
@@ -637,7 +690,7 @@ hipError_t run_norm(const Norm &a, hipStream_t stream) {
 // How the rows of a gradient are divided: workgroups (each leaves one row of
 // dw's partial sums) and, for wide rows, how many rows each takes.
 struct NormGradPlan {
-    bool wide;
+    bool wide, deep;
     int rows_at_once;        // of a workgroup
     int wgs, rows_per_wg;
     NormGradPlan(int64_t N, int64_t D, int compute_units) : wide(D > kMaxHeld) {
@@ -649,10 +702,13 @@ struct NormGradPlan {
         const int64_t most = wide ? 64 : 1024 / threads_for(lanes) * compute_units;
         wgs = static_cast<int>(std::min<int64_t>(most, (N + rows_at_once - 1) / rows_at_once));
         rows_per_wg = static_cast<int>((N + wgs - 1) / wgs);
+        deep = !wide && rows_per_wg > kDepth * rows_at_once;
         if (wide)
             wgs = static_cast<int>((N + rows_per_wg - 1) / rows_per_wg);
     }
-    size_t partial_bytes(int64_t D) const { return static_cast<size_t>(wgs) * D * sizeof(float); }
+    size_t partial_bytes(int64_t D) const {
+        return static_cast<size_t>(wgs) * D * (deep ? sizeof(double) : sizeof(float));
+    }
 };
 
 template <int N>
@@ -679,12 +735,20 @@ hipError_t run_norm_grad(const NormGrad &a, const NormGradPlan &p, void *dw, hip
     } else {
         auto launch = [&](auto lanes, auto held) {
             constexpr int G = decltype(lanes)::value, R = decltype(held)::value;
-            if (a.D % kRun == 0)
-                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, true>), grid, dim3(threads_for(G)), 0,
+            const dim3 threads(threads_for(G));
+            const bool deep = p.deep && dw != nullptr;
+            if (a.D % kRun == 0 && !deep)
+                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, true, false>), grid, threads, 0,
+                                   stream, a);
+            else if (a.D % kRun == 0)
+                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, true, true>), grid, threads, 0,
+                                   stream, a);
+            else if (!deep)
+                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, false, false>), grid, threads, 0,
                                    stream, a);
             else
-                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, false>), grid, dim3(threads_for(G)),
-                                   0, stream, a);
+                hipLaunchKernelGGL((norm_grad_kernel<T, G, R, false, true>), grid, threads, 0,
+                                   stream, a);
         };
         if (runs <= 16)
             launch(Int<16>{}, Int<1>{});
@@ -705,8 +769,13 @@ hipError_t run_norm_grad(const NormGrad &a, const NormGradPlan &p, void *dw, hip
         e = hipGetLastError();
     }
     if (e == hipSuccess && dw != nullptr) {
-        hipLaunchKernelGGL((norm_join_kernel<T>), dim3((a.D + kJoinCols - 1) / kJoinCols),
-                           dim3(kJoinCols * kJoinShares), 0, stream, a.dw_partial, p.wgs, a.D, dw);
+        const dim3 columns((a.D + kJoinCols - 1) / kJoinCols), threads(kJoinCols * kJoinShares);
+        if (p.deep)
+            hipLaunchKernelGGL((norm_join_kernel<T, double>), columns, threads, 0, stream,
+                               static_cast<const double *>(a.dw_partial), p.wgs, a.D, dw);
+        else
+            hipLaunchKernelGGL((norm_join_kernel<T, float>), columns, threads, 0, stream,
+                               static_cast<const float *>(a.dw_partial), p.wgs, a.D, dw);
         e = hipGetLastError();
     }
     return e;
@@ -856,7 +925,7 @@ extern "C" kmeans_status_t kmeans_rms_norm_grad(const void *dY, int64_t dy_strid
                         hipGetErrorString(lease->error()));
         char *ws = static_cast<char *>(lease->ptr());
         a.r = p.wide ? reinterpret_cast<float *>(ws) : nullptr;
-        a.dw_partial = reinterpret_cast<float *>(ws + r_bytes);
+        a.dw_partial = ws + r_bytes;
     }
     const hipError_t e = dtype == KMEANS_BF16   ? run_norm_grad<Bf16>(a, p, dweight, stream)
                          : dtype == KMEANS_FP16 ? run_norm_grad<Fp16>(a, p, dweight, stream)

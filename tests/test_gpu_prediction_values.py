@@ -210,3 +210,47 @@ def test_labels_do_not_depend_on_the_batch(of, rest, top_k):
             for i in range(0, 128, n):
                 few = km.kmeans_sample(z[i:i + n], u[:n], temperature=t[i:i + n], **kw)
                 assert torch.equal(few, got[i:i + len(few)]), (kw, n, i)
+
+
+# ---- the norm's weight gradient over many rows --------------------------------
+
+def check_dw(dY, H, w, exact):
+    """dw against `exact`, whose terms all have one sign.  At most 44 terms, then
+    16 such sums, then eight of those in pairs are added in fp32, all that follows
+    in fp64: 61 roundings, one to spare, one of a partial sum, one of the term's product, and of r: each square, the sum
+    of D of them (8 + log2(D / 8) in a row), the division, eps and the root
+    halve, then the reciprocal."""
+    _, dw = km.kmeans_rms_norm_grad(dY, H, w)
+    D = H.shape[1]
+    bound = (63 + 1 + 1 + (9 + np.ceil(np.log2(max(1, D / 8))) + 2) / 2 + 2) * 2.0 ** -24
+    got = dw.double().cpu()
+    off = ((got - exact) / exact).abs().max()
+    assert off <= bound + 2.0 ** -24, f"{float(off):.3g}, {float(bound):.3g}"
+
+
+@pytest.mark.parametrize("N,D", [((1 << 26) + 5, 2), ((1 << 22) + 1, 60), (3_000_001, 129),
+                                 (400_000, 1000), (70_003, 8200), (150_000, 16392)])
+def test_dw_of_many_rows(N, D):
+    """Every row the same, for several such rows: the roundings of each addition
+    then tend to one side, and in fp32 alone the error grows with the rows."""
+    g = torch.Generator().manual_seed(D)
+    w = torch.ones(D).cuda()
+    eps = float(np.float32(1e-6))
+    for _ in range(3):
+        h, dy = (torch.rand(D, generator=g) + 0.25 for _ in range(2))
+        H, dY = torch.empty(N, D, device="cuda"), torch.empty(N, D, device="cuda")
+        H.copy_(h), dY.copy_(dy)
+        r = 1 / torch.sqrt(h.double().square().mean() + eps)
+        check_dw(dY, H, w, N * (dy.double() * h.double() * r))
+        del H, dY
+
+
+@pytest.mark.parametrize("N,D", [(2_000_003, 40), (100_000, 700)])
+def test_dw_of_many_rows_of_any_kind(N, D):
+    """Against a sum in fp64 on the GPU; terms of one sign."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    H = torch.rand(N, D, generator=g, device="cuda") + 0.01
+    dY = torch.rand(N, D, generator=g, device="cuda")
+    r = 1 / torch.sqrt(H.double().square().mean(1, keepdim=True) + float(np.float32(1e-6)))
+    exact = (dY.double() * H.double() * r).sum(0).cpu()
+    check_dw(dY, H, torch.ones(D).cuda(), exact)
