@@ -892,6 +892,7 @@ def kmeans_sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     kind = _labels(out, device.index)
     t, ts = _setting(temperature, "temperature", torch.float32, N, device, 1.0)
     k, ks = _setting(top_k, "top_k", torch.int32, N, device, 0)
+    k = max(-1 << 31, min(k, (1 << 31) - 1))          # 32 bits of it would be taken else
     p, ps = _setting(top_p, "top_p", torch.float32, N, device, 1.0)
     m, ms = _setting(min_p, "min_p", torch.float32, N, device, 0.0)
     settings = _Sampling(t, p, m, k, ts, ps, ms, ks)

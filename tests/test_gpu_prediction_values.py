@@ -254,3 +254,14 @@ def test_dw_of_many_rows_of_any_kind(N, D):
     r = 1 / torch.sqrt(H.double().square().mean(1, keepdim=True) + float(np.float32(1e-6)))
     exact = (dY.double() * H.double() * r).sum(0).cpu()
     check_dw(dY, H, torch.ones(D).cuda(), exact)
+
+
+def test_top_k_of_any_integer():
+    """More than 32 bits hold is more than all labels; below zero is refused."""
+    z, u = rand((40, 900), F32, 3, 2.0), uniforms(40, 5)
+    want = km.kmeans_sample(z, u)
+    for k in (900, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 3, 2 ** 32 + 1, 2 ** 40 + 2):
+        assert torch.equal(km.kmeans_sample(z, u, top_k=k), want), k
+    for k in (-1, -2 ** 31, -2 ** 31 - 1, -2 ** 32 + 1):
+        with pytest.raises(km.KmeansError, match="top_k"):
+            km.kmeans_sample(z, u, top_k=k)
