@@ -692,11 +692,10 @@ extern "C" kmeans_status_t kmeans_linear_fp8(const void *X, int64_t x_stride, co
     const Scales sc{x_scales, w_scales, xs_stride, ws_stride,
                     static_cast<int>((F + kFp8Block - 1) / kFp8Block)};
     Product g{};
-    g.I = static_cast<int>(N);
-    g.J = static_cast<int>(F);
-    g.epi = {bias, residual, residual_stride, Y, y_stride, nullptr, 0, activation};
     std::optional<WorkspaceLease> lease;
     if (N <= kMaxFewRows) {
+        g.I = static_cast<int>(N);
+        g.J = static_cast<int>(F);
         g.shape = kRows;
         g.P = X;
         g.Q = W;
@@ -706,10 +705,7 @@ extern "C" kmeans_status_t kmeans_linear_fp8(const void *X, int64_t x_stride, co
     } else {
         size_t bytes = 0;
         Layout x = layout_of(X, x_stride, N, D, bytes), w = layout_of(W, w_stride, F, D, bytes);
-        // In pairs of 8-bit values from here on.
-        g.K = static_cast<int>((D + 15) / 16 * 8);
-        g.dma = true;
-        plan_product(g, cus, dtype != KMEANS_FP32);
+        g = fp8_product(N, D, F, cus, dtype != KMEANS_FP32);
         if (tiles_of(g, 128) > kMaxRows / kMaxKSplits)
             return fail(KMEANS_ERR_UNSUPPORTED, "N=%lld x F=%lld: too many outputs",
                         static_cast<long long>(N), static_cast<long long>(F));
@@ -739,6 +735,7 @@ extern "C" kmeans_status_t kmeans_linear_fp8(const void *X, int64_t x_stride, co
         g.ldp = x.ld / 2;
         g.ldq = w.ld / 2;
     }
+    g.epi = {bias, residual, residual_stride, Y, y_stride, nullptr, 0, activation};
     const hipError_t e = dtype == KMEANS_BF16   ? run_product<Bf16>(g, sc, cus, stream)
                          : dtype == KMEANS_FP16 ? run_product<Fp16>(g, sc, cus, stream)
                                                 : run_product<Fp32>(g, sc, cus, stream);

@@ -273,6 +273,19 @@ inline Product forward_product(Operand &x, Operand &w, int compute_units, size_t
     }
     return g;
 }
+// The product of 8-bit operands, more than kMaxFewRows rows of which lie as the
+// copies take them, in pairs of values from here on; `wide` where the kernel has the
+// shape (outputs of 16 bits).  The times that the plan goes by were measured with
+// 16-bit operands.
+inline Product fp8_product(int64_t N, int64_t D, int64_t F, int compute_units, bool wide) {
+    Product g{};
+    g.I = static_cast<int>(N);
+    g.J = static_cast<int>(F);
+    g.K = static_cast<int>((D + 15) / 16 * 8);
+    g.dma = true;
+    plan_product(g, compute_units, wide);
+    return g;
+}
 inline Product input_grad_product(int64_t N, Operand &w, int compute_units, size_t &bytes) {
     Product g{};
     g.Q = w.p;
