@@ -777,28 +777,31 @@ def kmeans_rms_norm_grad(dY, H, weight=None, eps: float = 1e-6, dH=None, need_dw
 
 
 def kmeans_quantize(X, rows: int = 1, out=None, scales=None, stream=None):
-    """``X`` (``[N, D]`` bf16, fp16 or fp32) as ``float8_e4m3fn`` values with an
-    fp32 scale for each block of ``rows`` (1 or 128) x 128: ``(Q, scales)``."""
-    x_stride = _rows(X, "X")
-    code = _dtype(X, "X")
-    N, D = X.shape
+    """``X`` (bf16, fp16 or fp32; ``[..., D]``, or ``[N, D]`` for blocks of 128 rows)
+    as ``float8_e4m3fn`` values with an fp32 scale for each block of ``rows`` (1 or
+    128) x 128: ``(Q, scales)``, ``scales`` ``[..., ceil(D / 128)]`` or
+    ``[ceil(N / 128), ceil(D / 128)]``."""
+    x = _as_rows(X, "X") if rows == 1 else X
+    x_stride = _rows(x, "X")
+    code = _dtype(x, "X")
+    N, D = x.shape
     if rows not in (1, FP8_BLOCK):
         raise ValueError(f"rows must be 1 or {FP8_BLOCK} (got {rows})")
     if _FP8 is None:
         _types()
     shape = (-(-N // rows), _blocks(D))
     if out is None:
-        out = X.new_empty((N, D), dtype=_FP8)
+        out = x.new_empty(X.shape, dtype=_FP8)
         q_stride = D
     else:
-        q_stride = _typed_rows(out, "out", _FP8, X.get_device(), (N, D))
+        q_stride = _typed_rows(_as_rows(out, "out"), "out", _FP8, x.get_device(), (N, D))
     if scales is None:
-        scales = X.new_empty(shape, dtype=_F32)
+        scales = x.new_empty(shape if x is X else (*X.shape[:-1], shape[1]), dtype=_F32)
         s_stride = shape[1]
     else:
-        s_stride = _typed_rows(scales, "scales", _F32, X.get_device(), shape)
+        s_stride = _typed_rows(_as_rows(scales, "scales"), "scales", _F32, x.get_device(), shape)
     lib = load_library()
-    _launch(lib.kmeans_quantize, X.device, stream, X.data_ptr(), x_stride, N, D, code, rows,
+    _launch(lib.kmeans_quantize, x.device, stream, x.data_ptr(), x_stride, N, D, code, rows,
             out.data_ptr(), q_stride, scales.data_ptr(), s_stride)
     return out, scales
 

@@ -265,3 +265,24 @@ def test_top_k_of_any_integer():
     for k in (-1, -2 ** 31, -2 ** 31 - 1, -2 ** 32 + 1):
         with pytest.raises(km.KmeansError, match="top_k"):
             km.kmeans_sample(z, u, top_k=k)
+
+
+def test_quantize_of_any_shape():
+    """Rows of [..., D], as the norm and the product beside it take them."""
+    x = rand((2, 3, 5, 200), BF, 1)
+    want, s = km.kmeans_quantize(x.view(-1, 200))
+    Q, t = km.kmeans_quantize(x)
+    assert Q.shape == x.shape and t.shape == (2, 3, 5, 2)
+    assert torch.equal(Q.view(torch.uint8).view(-1, 200), want.view(torch.uint8))
+    assert torch.equal(t.view(-1, 2), s)
+    out, scales = torch.empty_like(Q), torch.empty_like(t)
+    got = km.kmeans_quantize(x, out=out, scales=scales)
+    assert got[0] is out and got[1] is scales
+    assert torch.equal(out.view(torch.uint8), Q.view(torch.uint8)) and torch.equal(scales, t)
+    assert km.kmeans_quantize(x[:0])[1].shape == (0, 3, 5, 2)
+    W, sw = km.kmeans_quantize(rand((70, 200), BF, 2), rows=128)
+    assert km.kmeans_linear_fp8(Q, t, W, sw).shape == (2, 3, 5, 70)
+    with pytest.raises(ValueError, match="2-D"):
+        km.kmeans_quantize(x, rows=128)
+    with pytest.raises(ValueError, match="evenly spaced"):
+        km.kmeans_quantize(x.transpose(1, 2))
