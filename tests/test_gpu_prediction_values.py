@@ -286,3 +286,25 @@ def test_quantize_of_any_shape():
         km.kmeans_quantize(x, rows=128)
     with pytest.raises(ValueError, match="evenly spaced"):
         km.kmeans_quantize(x.transpose(1, 2))
+
+
+def test_dw_of_many_rows_in_a_graph():
+    """The workspace's partial sums begin anew in every replay."""
+    N, D = 800_000, 40
+    H, dY, w = rand((N, D), BF, 1), rand((N, D), BF, 2), rand((D,), BF, 3)
+    want = km.kmeans_rms_norm_grad(dY, H, w)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = km.kmeans_rms_norm_grad(dY, H, w)
+    for i in range(4):
+        with torch.cuda.stream(s):
+            g.replay()
+            now = [t.clone() for t in got]
+            km.kmeans_rms_norm_grad(dY[:N - 7 * i], H[:N - 7 * i], w)
+        s.synchronize()
+        for a, b in zip(now, want):
+            assert torch.equal(a, b), i
+    del g
+    km.kmeans_release_workspace(stream=s)
