@@ -464,8 +464,8 @@ kmeans_status_t kmeans_clip_gradients(const kmeans_gradient_t *list, int64_t cou
  *   Q         [N][D] e4m3 and scales fp32 [N][ceil(D / 128)], or NULL.  One of
  *             Y and Q is given.
  *
- * Squares are summed in fp32: a row with a value of magnitude 2^63 or more gives
- * zeros (or NaN).
+ * Squares are summed in fp32: a row whose squares add up to 2^128 or more gives zeros
+ * (NaN for its infinities), and magnitudes below 2^-75 add nothing.
  */
 kmeans_status_t kmeans_rms_norm(const void *X, int64_t x_stride, const void *residual,
                                 int64_t residual_stride, const void *weight, int64_t N, int64_t D,

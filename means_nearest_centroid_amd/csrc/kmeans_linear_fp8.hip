@@ -57,7 +57,8 @@ __device__ __forceinline__ f32x4 mfma_block(const Halves &a, const Halves &b) {
 
 // The same with full fp32 sums, at half the rate: e4m3 values are bf16 values,
 // whose matrix instruction keeps every bit of a product (4e-8 of the magnitudes
-// in sums of 128).  For fp32 outputs, and where memory bounds the product.
+// in sums of 128).  For fp32 outputs, and where memory bounds the product (64 rows x
+// 4096 x 65536 75 us, 512 rows 257, 4096 rows 1900, 1160 TFLOP/s).
 struct Widened {
     Bf16::mfma v[4];
 };
@@ -94,10 +95,10 @@ __device__ __forceinline__ f32x4 mfma_block(const Widened &a, const Widened &b) 
 // phase's P fragment is read one phase ahead.  A product is scaled and added two
 // products after its own, so that no instruction waits for the matrix pipe.
 //
-// 8192 x 8192 x 8192 467 us (2350 TFLOP/s; the library's product with one scale
-// each 2660), 16384 x 4096 x 4096 250 to 265 us (2080 to 2210; 2430).  What is left
-// there: the first copies of each of four rounds, and the output.  With tanh-gelu,
-// bias and residual 305 us: with one workgroup per CU nothing hides the residual's
+// 8192 x 8192 x 8192 467 to 500 us by device (2200 to 2350 TFLOP/s; the library's
+// product with one scale each 2660), 16384 x 4096 x 4096 250 to 270 us (2040 to 2200;
+// 2430).  What is left there: the first copies of each of four rounds, and the output.
+// With tanh-gelu, bias and residual 305 to 327 us: with one workgroup per CU nothing hides the residual's
 // 134 MB and the output's (both passes' residual loads ahead of the first spill:
 // 352).  128 x 128 tiles in pairs hide them, but read LDS twice as often: 364.
 template <typename T, int WI, int WJ, int TI, int TJ, int S>
@@ -464,7 +465,7 @@ __device__ __forceinline__ u32x4 load_bytes(const uint8_t *p, int n) {
 // turns and add their sums in LDS in wave order.  Loads are at the rows' own
 // alignment; a lane takes bytes 16 q .. and 64 + 16 q .. of a block, so that a load
 // of a wave covers 64 bytes of each row.  1 x 4096 x 32768: 28.6 us (134 MB, 4.7
-// TB/s), 16 rows 30.3; with FB = 1 33 and 42, with two or four blocks of k at
+// TB/s), 16 rows 30 to 35; with FB = 1 33 and 42, with two or four blocks of k at
 // once 29 to 34.  1 x 8192 x 8192 13.6 us (4.9 TB/s).
 template <typename T, int WAVES, int FB>
 __global__ __launch_bounds__(WAVES * 64)

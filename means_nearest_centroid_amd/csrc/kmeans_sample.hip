@@ -31,9 +31,10 @@
 // 512 x 65536 fp32, top-p: 58 us (134 MB; 25 us to read them once).  Each workgroup
 // first waits for memory, then for its weights (22 VALU instructions an element,
 // 14 of them fp64), then for the second reading (10 us), and all run in step.
-// Three readings (maximum, weights, borders) took 81 us, five 125.  16 x 32768 with
-// top-k 50: 10 us of which 1.5 read the row, the rest 20 barriers; top-p and
-// the draw 21.
+// The adds of a row's many likely labels to a few bins cost LDS conflicts too (0.63 of
+// the LDS's active cycles).  Three readings (maximum, weights, borders) took 81 us,
+// five 125.  16 x 32768 with top-k 50: 10 us of which 1.5 read the row, the rest 20
+// barriers; top-p and the draw 21, the histogram and the second reading more.
 #include <float.h>
 #include <math.h>
 #include <stdint.h>

@@ -1,6 +1,6 @@
-// kmeans_types.h -- element types of the codebook-training kernels (lookup,
-// linear, gradient clipping): bf16, fp16 and fp32 in memory, fp32 (or more)
-// in every sum.  Not part of the public interface.
+// kmeans_types.h -- element types of the kernels around a codebook (lookup,
+// linear, gradient clipping, norm, quantisation, sampling): bf16, fp16 and fp32 in
+// memory, fp32 (or more) in every sum.  Not part of the public interface.
 #pragma once
 
 #include <hip/hip_runtime.h>
