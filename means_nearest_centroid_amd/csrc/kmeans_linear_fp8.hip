@@ -98,9 +98,9 @@ __device__ __forceinline__ f32x4 mfma_block(const Widened &a, const Widened &b) 
 // 8192 x 8192 x 8192 467 to 500 us by device (2200 to 2350 TFLOP/s; the library's
 // product with one scale each 2660), 16384 x 4096 x 4096 250 to 270 us (2040 to 2200;
 // 2430).  What is left there: the first copies of each of four rounds, and the output.
-// With tanh-gelu, bias and residual 305 to 327 us: with one workgroup per CU nothing hides the residual's
-// 134 MB and the output's (both passes' residual loads ahead of the first spill:
-// 352).  128 x 128 tiles in pairs hide them, but read LDS twice as often: 364.
+// With tanh-gelu, bias and residual 305 to 327 us: with one workgroup per CU nothing
+// hides the residual's 134 MB and the output's (both passes' residual loads ahead of
+// the first spill: 352).  128 x 128 tiles in pairs hide them, but read LDS twice as often: 364.
 template <typename T, int WI, int WJ, int TI, int TJ, int S>
 __global__ __launch_bounds__(WI * WJ * 64, 2)
 void linear_fp8_kernel(const Product g, const Scales sc) {

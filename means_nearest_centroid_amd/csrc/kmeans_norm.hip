@@ -132,8 +132,8 @@ __device__ __forceinline__ void norm_out(const Norm &a, int64_t row, int c, floa
 // G lanes to a row, R runs to a lane: run i of the row is lane i % G's.  One run to
 // a lane as far as workgroups go: more rows are on their way at once than with
 // more runs to fewer lanes (16384 x 4096 bf16 with residual to 8 bits 88 to 90 us, 471
-// MB at 5.3 TB/s, 5 to 8 us more with 256 lanes; 4096 x 8192 44 us, 54; 2048 x 16384
-// fp16 48 us, 73 with 8 runs to 256 lanes).
+// MB at 5.3 TB/s, 93 with 256 lanes where it took 86; 4096 x 8192 44 us, 54 so; 2048 x
+// 16384 fp16 48 us, 73 with 8 runs to 256 lanes).
 template <typename T, bool QUANT, int G, int R>
 __global__ __launch_bounds__(threads_for(G))
 void norm_kernel(const Norm a) {
@@ -311,10 +311,10 @@ __device__ __forceinline__ void leave_sums(const NormGrad &a, float (&dw)[R][kRu
 // then over the workgroup's groups in LDS, and those of more rows in fp64 in its row
 // of partial sums.  The next row is on its way while this one is worked, where
 // registers hold both (R = 1; two runs to a lane, rows of more than 8192, spill 5 to
-// 29 of them: 2048 x 16384 68 us, 4096 x 8192 of the same bytes 57); rows stay in their
-// own type for that.  As many workgroups as the CUs hold (16 waves each): 16384 x 4096 bf16
-// with dh 102 us (537 MB, 5.3 TB/s), 119 with twice and 149 with half as many,
-// and 171 with 256 lanes to a row.  WHOLE: D is a multiple of 8, and no run is
+// 29 of them: 2048 x 16384 68 us, 4096 x 8192 of the same bytes 57); rows stay in
+// their own type for that.  As many workgroups as the CUs hold (16 waves each): 16384 x
+// 4096 bf16 with dh 102 us (537 MB, 5.3 TB/s), 119 with twice and 149 with half as
+// many, and 171 with 256 lanes to a row.  WHOLE: D is a multiple of 8, and no run is
 // cut short (50021 x 321 fp32 40 us, 193 MB; 45 with its last runs loaded whole
 // and shifted).  DEEP: a lane has more than kDepth rows.
 template <typename T, int G, int R, bool WHOLE, bool DEEP>
