@@ -1,7 +1,7 @@
 // kmeans_linear_plan.h -- the arithmetic of kmeans_linear.hip and
 // kmeans_linear_fp8.hip that needs no GPU: which bytes of an operand the staging
-// reads, and how a product is tiled and split.  Plain C++, so that tests can follow it on the CPU.  Not part of
-// the public interface.
+// reads, and how a product is tiled and split.  Plain C++, so that tests can
+// follow it on the CPU.  Not part of the public interface.
 #pragma once
 
 #include <stddef.h>

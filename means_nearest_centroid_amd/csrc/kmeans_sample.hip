@@ -10,9 +10,9 @@
 // Weights are summed in 64-bit integers, so that every sum is exact and the same
 // in any order, from atomics too: the label depends on the row and its settings
 // alone, not on the launch (which way below a row takes goes by its length, its
-// settings and its values).  A weight is a multiple of 2^-43 of its bin's centre (below); a bin's sum
-// is brought to the scale of the largest weight with one rounding, to 2^-43 of
-// that.  32-bit sums would shift the borders by 1e-7 of the whole and draw other
+// settings and its values).  A weight is a multiple of 2^-43 of its bin's centre
+// (below); a bin's sum is brought to the scale of the largest weight with one
+// rounding, to 2^-43 of that.  32-bit sums would shift the borders by 1e-7 of the whole and draw other
 // labels in one row of some thousands.
 //
 // All borders (the k-th value, the nucleus's end, the draw) are one thing: the

@@ -217,9 +217,9 @@ def test_labels_do_not_depend_on_the_batch(of, rest, top_k):
 def check_dw(dY, H, w, exact):
     """dw against `exact`, whose terms all have one sign.  At most 44 terms, then
     16 such sums, then eight of those in pairs are added in fp32, all that follows
-    in fp64: 61 roundings, one to spare, one of a partial sum, one of the term's product, and of r: each square, the sum
-    of D of them (8 + log2(D / 8) in a row), the division, eps and the root
-    halve, then the reciprocal."""
+    in fp64: 61 roundings, one to spare, one of a partial sum, one of the term's
+    product, and of r: each square, the sum of D of them (8 + log2(D / 8) in a
+    row), the division, eps and the root halve, then the reciprocal."""
     _, dw = km.kmeans_rms_norm_grad(dY, H, w)
     D = H.shape[1]
     bound = (63 + 1 + 1 + (9 + np.ceil(np.log2(max(1, D / 8))) + 2) / 2 + 2) * 2.0 ** -24
